@@ -7,7 +7,9 @@
  *
  * in its weight-only (W8A16), static int8-activation (W8A8, one or two passes)
  * and dynamic int8-activation x int4-group-weight (8da4w) forms, plus the
- * quantizers that produce its operands.  Sources of each definition:
+ * quantizers that produce its operands, the W8A16 linear with low-rank adapters (forward
+ * and backward), and 8-bit activation checkpoints with the weight gradient that reads them.
+ * Sources of each definition:
  *
  *   [ROCm-INT8]  code/quant/int8_linear.py (Ming-Image-0.1-Design ROCm INT8):
  *                quantize_weight, QUANT_RULE, Int8Linear
@@ -84,7 +86,9 @@ typedef struct {
 typedef enum {
     Q8_OP_LINEAR_W8A8 = 0,
     Q8_OP_LINEAR_DQ8CA_Q4GSW = 1,
-    Q8_OP_GPTQ_INT8 = 3             /* q8_gptq_int8 (M unused, extra = block) */
+    Q8_OP_GPTQ_INT8 = 3,            /* q8_gptq_int8 (M unused, extra = block) */
+    Q8_OP_LINEAR_W8A16_LORA = 4,           /* q8_linear_w8a16_lora (extra = rank)          */
+    Q8_OP_LINEAR_W8A16_LORA_BACKWARD = 5   /* q8_linear_w8a16_lora_backward (extra = rank) */
 } q8_op;
 
 /* Host.  Human-readable name of a status code (static string). */
@@ -306,6 +310,106 @@ q8_status q8_linear_dq8ca_q4gsw(const void* x, const uint8_t* q4, const float* g
                                 float* y, int64_t M, int64_t N, int64_t K,
                                 void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------- low-rank adapters */
+
+/* A pool of `count` low-rank adapters of one rank for one linear layer.  Adapter i adds
+ * scale[i] * (x a[i]^T) b[i]^T to the layer's output.  All members are read, and none is
+ * kept after a call returns.
+ *   a device bf16 [count, rank, K]; b device bf16 [count, N, rank]; scale device fp32 [count]
+ *   rank in 8, 16, ... 256 (a multiple of 8; pad adapters of lower rank with zeros);
+ *   count in [1, 1024].  Q8_ERR_ARG otherwise. */
+typedef struct {
+    const void* a;
+    const void* b;
+    const float* scale;
+    int64_t count;
+    int64_t rank;
+} q8_adapters;
+
+/* W8A16 with a low-rank adapter for each row beside the shared projection (one batch may
+ * use many adapters; rows of one adapter need not be neighbours):
+ *     h[m,r] = sum_k x[m,k] a[i][r,k]                     i = ids[m]
+ *     y[m,n] = s_w[n] * sum_k x[m,k] q[n,k] + bias[n] + scale[i] * sum_r h[m,r] b[i][n,r]
+ * fp32 accumulation, one rounding to yt.  A row whose id is outside [0, count) (-1 by
+ * convention) has no adapter: its h is 0 and its y is q8_linear_w8a16_bias's sum.
+ *   x device bf16 [M, K]; q device int8 [N, K]; s_w device fp32 [N]; bias device fp32 [N]
+ *   (nullable, 4-byte aligned); ids device int32 [M] (4-byte aligned, values checked on the
+ *   device only); y device [M, N] of type yt (Q8_BF16 or Q8_F32); h device fp32 [M, rank]
+ *   (written; the backward pass reads it).
+ *   workspace: at least q8_workspace_bytes(Q8_OP_LINEAR_W8A16_LORA, M, N, K, rank) bytes
+ *   (may be NULL when that is 0); its contents on entry do not matter.  Calls that overlap
+ *   on the GPU, replays of captured graphs among them, need a workspace each.
+ * Finite inputs are a precondition, as everywhere: adapters that no row uses are not read,
+ * but a non-finite weight of an adapter in use may reach the other rows of its tile. */
+q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
+                               const float* bias, const q8_adapters* adapters,
+                               const int32_t* ids, void* y, q8_dtype yt, float* h, int64_t M,
+                               int64_t N, int64_t K, void* workspace, size_t ws_bytes,
+                               void* stream);
+
+/* A layer input kept for the backward pass: group == 0: x is bf16 [M, K] (exps unused);
+ * else x is int8 codes [M, K] and exps uint8 [M, K / group] of q8_checkpoint_save. */
+typedef struct {
+    const void* x;
+    const uint8_t* exps;
+    int32_t group;
+} q8_saved_input;
+
+/* Backward pass of q8_linear_w8a16_lora; q, s_w and the bias are frozen.  With i = ids[m]:
+ *     g[m,r]     = scale[i] * sum_n dy[m,n] b[i][n,r]            (0 without an adapter)
+ *     dx[m,k]    = sum_n dy[m,n] * (s_w[n] * q[n,k]) + sum_r g[m,r] a[i][r,k]
+ *     da[i][r,k] = sum_{m: ids[m] = i} g[m,r] x[m,k]
+ *     db[i][n,r] = scale[i] * sum_{m: ids[m] = i} dy[m,n] h[m,r]
+ * fp32 accumulation.  s_w[n] * q[n,k] is rounded to bf16 once on its way to the tensor
+ * cores (s_w varies along the summed axis, so it cannot be applied after the sum); dx is
+ * rounded to bf16 once.  Sums are taken in an order that depends on sizes and ids only.
+ *   dy device bf16 [M, N]; ids, adapters, q, s_w as in the forward call; h device fp32
+ *   [M, rank] as the forward call wrote it (read iff db); input: the layer's input (read iff
+ *   da; exps of any alignment, group 0, 32, 64, 128 or 256 with K % group == 0);
+ *   dx device bf16 [M, K], da device fp32 [count, rank, K], db device fp32 [count, N, rank]:
+ *   each nullable, not computed when NULL.
+ *   accumulate != 0 adds to da and db instead of overwriting them (adapters that no row
+ *   uses: left as they are, or set to 0 when overwriting).  M == 0 is a batch without rows.
+ *   N % 8 == 0 (Q8_ERR_SHAPE otherwise).
+ *   workspace: at least q8_workspace_bytes(Q8_OP_LINEAR_W8A16_LORA_BACKWARD, M, N, K, rank)
+ *   bytes, with the rules of the forward call. */
+q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const float* s_w,
+                                        const q8_adapters* adapters, const int32_t* ids,
+                                        const float* h, const q8_saved_input* input, void* dx,
+                                        float* da, float* db, int accumulate, int64_t M,
+                                        int64_t N, int64_t K, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
+/* ------------------------------------------------ 8-bit activation checkpoints */
+
+/* Keeps an activation for the backward pass in 8 bits: per row and group of `group`
+ * consecutive k, with e the smallest whole number such that absmax(x) <= 127 * 2^e,
+ * clamped to [-126, 121],
+ *     exps[m,g]  = e + 127
+ *     codes[m,k] = clamp(round(x[m,k] * 2^-e), -127, 127)       (ties to even)
+ * An all-zero group gets exponent byte 1 and codes 0.  code * 2^e is a bf16 number, so
+ * nothing is rounded again when the checkpoint is restored or used.
+ *   x device [M, K] of type xt (Q8_BF16 or Q8_F32); codes device int8 [M, K]; exps device
+ *   uint8 [M, K / group], of any alignment; group 32, 64, 128 or 256 (Q8_ERR_ARG),
+ *   K % group == 0 (Q8_ERR_SHAPE).  Codes and exponents are bit-identical to the definition. */
+q8_status q8_checkpoint_save(const void* x, q8_dtype xt, int64_t M, int64_t K, int group,
+                             int8_t* codes, uint8_t* exps, void* stream);
+
+/* The values a checkpoint stands for, code * 2^(exps - 127), exact in either type.
+ *   y device [M, K] of type yt; the other arguments as q8_checkpoint_save. */
+q8_status q8_checkpoint_load(const int8_t* codes, const uint8_t* exps, int group, void* y,
+                             q8_dtype yt, int64_t M, int64_t K, void* stream);
+
+/* Weight gradient of a linear from the checkpoint of its input:
+ *     dw[n,k] = sum_m dy[m,n] * codes[m,k] * 2^(exps[m,k/group] - 127)
+ * exact products, fp32 accumulation.
+ *   dy device bf16 [M, N] (N % 8 == 0, Q8_ERR_SHAPE otherwise); codes, exps, group as
+ *   written by q8_checkpoint_save; dw device fp32 [N, K]: overwritten, or added to when
+ *   accumulate != 0.  M == 0 sets dw to 0 (leaves it when accumulating). */
+q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t* exps,
+                              int group, float* dw, int accumulate, int64_t M, int64_t N,
+                              int64_t K, void* stream);
+
 /* ------------------------------------------------------------- GPTQ (offline) */
 
 /* Calibration Hessian ([SmolVLM-Q8] hessians): the sum over calibration batches of x^T x,
@@ -341,8 +445,8 @@ q8_status q8_gptq_int8(const float* W, const double* H, int64_t N, int64_t K, do
                        size_t ws_bytes, void* stream);
 
 /* Host.  Workspace bytes a linear needs for these sizes (0 if none).  `extra` is
- * "two-pass" (0/1) for Q8_OP_LINEAR_W8A8, G for Q8_OP_LINEAR_DQ8CA_Q4GSW and the block
- * size for Q8_OP_GPTQ_INT8.  The 8da4w size for 17..64 rows also depends on the current
+ * "two-pass" (0/1) for Q8_OP_LINEAR_W8A8, G for Q8_OP_LINEAR_DQ8CA_Q4GSW, the block
+ * size for Q8_OP_GPTQ_INT8 and the rank for the two adapter calls.  The 8da4w size for 17..64 rows also depends on the current
  * device's SM count (it sizes the K split of the 17..64-row GEMM).
  * Returns 0 for invalid arguments as well; the linear then reports the error. */
 size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K, int extra);

@@ -26,6 +26,7 @@ Q8_ERR_UNSUPPORTED_ARCH, Q8_ERR_LAUNCH, Q8_ERR_WORKSPACE, Q8_ERR_DEVICE = 5, 6, 
 Q8_F32, Q8_BF16 = 0, 1
 Q8_OP_LINEAR_W8A8, Q8_OP_LINEAR_DQ8CA_Q4GSW = 0, 1
 Q8_OP_GPTQ_INT8 = 3
+Q8_OP_LINEAR_W8A16_LORA, Q8_OP_LINEAR_W8A16_LORA_BACKWARD = 4, 5
 Q8_GRID_SYM127, Q8_GRID_FULL128 = 0, 1
 _GRIDS = {"sym127": Q8_GRID_SYM127, "full128": Q8_GRID_FULL128}
 
@@ -39,6 +40,8 @@ SYMBOLS = (
     "q8_quantize_weight_grid", "q8_linear_w8a16_bias", "q8_linear_w8a8_bias",
     "q8_observe_residual_minmax", "q8_hessian_accumulate", "q8_gptq_int8",
     "q8_quantize_weight_nvfp4", "q8_linear_w4a16_nvfp4",
+    "q8_linear_w8a16_lora", "q8_linear_w8a16_lora_backward",
+    "q8_checkpoint_save", "q8_checkpoint_load", "q8_checkpoint_wgrad",
 )
 # Built-in scratch of q8_linear_w8a8_noalloc (bytes).
 Q8_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -53,6 +56,15 @@ class Q8Error(RuntimeError):
 
 class q8_qparams(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("zero_point", ctypes.c_int32)]
+
+
+class q8_adapters(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("count", ctypes.c_int64), ("rank", ctypes.c_int64)]
+
+
+class q8_saved_input(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("exps", ctypes.c_void_p), ("group", ctypes.c_int32)]
 
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -121,6 +133,20 @@ def _lib() -> ctypes.CDLL:
     L.q8_linear_w8a8_noalloc.restype = st
     L.q8_linear_w8a8_noalloc.argtypes = [_vp, q8_qparams, ctypes.POINTER(q8_qparams), _vp, _vp,
                                          _vp, _vp, _i64, _i64, _i64, _vp]
+    _ad = ctypes.POINTER(q8_adapters)
+    L.q8_linear_w8a16_lora.restype = st
+    L.q8_linear_w8a16_lora.argtypes = [_vp, _vp, _vp, _vp, _ad, _vp, _vp, st, _vp, _i64, _i64,
+                                       _i64, _vp, _sz, _vp]
+    L.q8_linear_w8a16_lora_backward.restype = st
+    L.q8_linear_w8a16_lora_backward.argtypes = [_vp, _vp, _vp, _ad, _vp, _vp,
+                                                ctypes.POINTER(q8_saved_input), _vp, _vp, _vp,
+                                                st, _i64, _i64, _i64, _vp, _sz, _vp]
+    L.q8_checkpoint_save.restype = st
+    L.q8_checkpoint_save.argtypes = [_vp, st, _i64, _i64, st, _vp, _vp, _vp]
+    L.q8_checkpoint_load.restype = st
+    L.q8_checkpoint_load.argtypes = [_vp, _vp, st, _vp, st, _i64, _i64, _vp]
+    L.q8_checkpoint_wgrad.restype = st
+    L.q8_checkpoint_wgrad.argtypes = [_vp, _vp, _vp, st, _vp, st, _i64, _i64, _i64, _vp]
     _LIB = L
     return L
 
@@ -400,6 +426,198 @@ def q8_linear_w8a8_noalloc(x: torch.Tensor, first, q: torch.Tensor, wsum: torch.
                                          _ptr(s_w), _ptr(y), M, N, K, _stream(stream)),
            "q8_linear_w8a8_noalloc")
     return y
+
+
+# ------------------------------------------------- low-rank adapters and 8-bit checkpoints
+
+
+def _same_device(first: torch.Tensor, *tensors) -> None:
+    """Every tensor on the current device: its stream is the one the call is enqueued on."""
+    dev = first.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors are on {dev} and {t.device}")
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream the call runs on (the caching allocator
+    may hand its memory on in that stream's order only)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(t, name, dtype, shape, device, stream):
+    if t is None:
+        return _empty(shape, dtype, device, stream)
+    _need(t, name, dtype, shape)
+    return t
+
+
+def _adapters(a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, N: int, K: int):
+    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+        raise ValueError("a must be 3-D [count, rank, K]")
+    L, R, _ = a.shape
+    _need(a, "a", torch.bfloat16, (L, R, K))
+    _need(b, "b", torch.bfloat16, (L, N, R))
+    _need(scale, "scale", torch.float32, (L,))
+    return q8_adapters(a.data_ptr(), b.data_ptr(), scale.data_ptr(), L, R)
+
+
+def q8_linear_w8a16_lora(x: torch.Tensor, q: torch.Tensor, s_w: torch.Tensor, a: torch.Tensor,
+                         b: torch.Tensor, scale: torch.Tensor, ids: torch.Tensor, y=None, h=None,
+                         out_dtype: torch.dtype = torch.bfloat16, workspace=None, stream=None,
+                         bias: Optional[torch.Tensor] = None):
+    """q8_linear_w8a16 plus each row's own low-rank adapter -> (y [M,N], h fp32 [M,rank]);
+    a bf16 [count,rank,K], b bf16 [count,N,rank], scale fp32 [count], ids int32 [M] (a row
+    whose id is outside [0, count) has no adapter)."""
+    M, K = x.shape
+    N = q.shape[0]
+    _need(x, "x", torch.bfloat16, (M, K))
+    _need(q, "q", torch.int8, (N, K))
+    _need(s_w, "s_w", torch.float32, (N,))
+    ad = _adapters(a, b, scale, N, K)
+    _need(ids, "ids", torch.int32, (M,))
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (N,))
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    y = _result(y, "y", out_dtype, (M, N), x.device, stream)
+    h = _result(h, "h", torch.float32, (M, ad.rank), x.device, stream)
+    _same_device(x, q, s_w, a, b, scale, ids, bias, y, h, workspace)
+    nbytes = _lib().q8_workspace_bytes(Q8_OP_LINEAR_W8A16_LORA, M, N, K, ad.rank)
+    if nbytes and workspace is None:
+        workspace = _empty((nbytes,), torch.uint8, x.device, stream)
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib().q8_linear_w8a16_lora(_ptr(x), _ptr(q), _ptr(s_w), _ptr(bias), ctypes.byref(ad),
+                                       _ptr(ids), _ptr(y),
+                                       Q8_BF16 if out_dtype == torch.bfloat16 else Q8_F32,
+                                       _ptr(h), M, N, K, _ptr(workspace), wsb, _stream(stream)),
+           "q8_linear_w8a16_lora")
+    return y, h
+
+
+def q8_linear_w8a16_lora_backward(dy: torch.Tensor, q: torch.Tensor, s_w: torch.Tensor,
+                                  a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor,
+                                  ids: torch.Tensor, h: Optional[torch.Tensor] = None, x=None,
+                                  codes=None, exps=None, dx=None, da=None, db=None,
+                                  want_dx: bool = True, want_da: bool = True,
+                                  want_db: bool = True, accumulate: bool = False,
+                                  workspace=None, stream=None):
+    """Gradients of q8_linear_w8a16_lora -> (dx bf16 [M,K], da fp32 [count,rank,K],
+    db fp32 [count,N,rank]), None for those not wanted.  The layer's input is x (bf16) or its
+    checkpoint (codes, exps of q8_checkpoint_save); h is the forward call's.  accumulate adds
+    to the given da and db."""
+    M, N = dy.shape
+    K = q.shape[1]
+    _need(dy, "dy", torch.bfloat16, (M, N))
+    _need(q, "q", torch.int8, (N, K))
+    _need(s_w, "s_w", torch.float32, (N,))
+    ad = _adapters(a, b, scale, N, K)
+    L, R = int(ad.count), int(ad.rank)
+    _need(ids, "ids", torch.int32, (M,))
+    want_dx, want_da, want_db = (want_dx or dx is not None, want_da or da is not None,
+                                 want_db or db is not None)
+    if accumulate and ((want_da and da is None) or (want_db and db is None)):
+        raise ValueError("accumulate adds to da and db: pass them")
+    saved = q8_saved_input(None, None, 0)
+    if want_da:
+        if (x is None) == (codes is None) or (codes is None) != (exps is None):
+            raise ValueError("pass x, or codes and exps")
+        if x is not None:
+            _need(x, "x", torch.bfloat16, (M, K))
+            saved = q8_saved_input(x.data_ptr(), None, 0)
+        else:
+            saved = _saved(codes, exps, M, K)
+    if want_db:
+        if h is None:
+            raise ValueError("db needs h, the forward call's second result")
+        _need(h, "h", torch.float32, (M, R))
+    dev = dy.device
+    dx = _result(dx, "dx", torch.bfloat16, (M, K), dev, stream) if want_dx else None
+    da = _result(da, "da", torch.float32, (L, R, K), dev, stream) if want_da else None
+    db = _result(db, "db", torch.float32, (L, N, R), dev, stream) if want_db else None
+    _same_device(dy, q, s_w, a, b, scale, ids, h, x, codes, exps, dx, da, db, workspace)
+    nbytes = _lib().q8_workspace_bytes(Q8_OP_LINEAR_W8A16_LORA_BACKWARD, M, N, K, R)
+    if nbytes and workspace is None:
+        workspace = _empty((nbytes,), torch.uint8, dev, stream)
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib().q8_linear_w8a16_lora_backward(
+        _ptr(dy), _ptr(q), _ptr(s_w), ctypes.byref(ad), _ptr(ids), _ptr(h), ctypes.byref(saved),
+        _ptr(dx), _ptr(da), _ptr(db), int(bool(accumulate)), M, N, K, _ptr(workspace), wsb,
+        _stream(stream)), "q8_linear_w8a16_lora_backward")
+    return dx, da, db
+
+
+def _saved(codes: torch.Tensor, exps: torch.Tensor, M: int, K: int) -> q8_saved_input:
+    _need(codes, "codes", torch.int8, (M, K))
+    G = _group_of(exps, K)
+    _need(exps, "exps", torch.uint8, (M, K // G))
+    return q8_saved_input(codes.data_ptr(), exps.data_ptr(), G)
+
+
+def _group_of(exps: torch.Tensor, K: int) -> int:
+    if not isinstance(exps, torch.Tensor) or exps.dim() != 2 or exps.shape[1] < 1 or \
+            K % exps.shape[1]:
+        raise ValueError("exps must be 2-D [M, K / group]")
+    return K // exps.shape[1]
+
+
+def q8_checkpoint_save(x: torch.Tensor, group: int = 128, codes=None, exps=None, stream=None):
+    """8-bit checkpoint of a bf16 or fp32 [M, K] activation -> (codes int8 [M,K], exponent
+    bytes uint8 [M, K/group]); a code counts steps of 2^(byte - 127)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be 2-D [M, K]")
+    M, K = x.shape
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("x must be bfloat16 or float32")
+    _need(x, "x", x.dtype, (M, K))
+    if group not in (32, 64, 128, 256) or K % group:
+        raise ValueError("group must be 32, 64, 128 or 256 and divide K")
+    codes = _result(codes, "codes", torch.int8, (M, K), x.device, stream)
+    exps = _result(exps, "exps", torch.uint8, (M, K // group), x.device, stream)
+    _same_device(x, codes, exps)
+    _check(_lib().q8_checkpoint_save(_ptr(x), Q8_BF16 if x.dtype == torch.bfloat16 else Q8_F32,
+                                     M, K, int(group), _ptr(codes), _ptr(exps),
+                                     _stream(stream)), "q8_checkpoint_save")
+    return codes, exps
+
+
+def q8_checkpoint_load(codes: torch.Tensor, exps: torch.Tensor, y=None,
+                       out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values a checkpoint stands for, bf16 or fp32 [M, K] (exact in both)."""
+    M, K = codes.shape
+    saved = _saved(codes, exps, M, K)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    y = _result(y, "y", out_dtype, (M, K), codes.device, stream)
+    _same_device(codes, exps, y)
+    _check(_lib().q8_checkpoint_load(_ptr(codes), _ptr(exps), saved.group, _ptr(y),
+                                     Q8_BF16 if out_dtype == torch.bfloat16 else Q8_F32, M, K,
+                                     _stream(stream)), "q8_checkpoint_load")
+    return y
+
+
+def q8_checkpoint_wgrad(dy: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor, dw=None,
+                        accumulate: bool = False, stream=None) -> torch.Tensor:
+    """dw [N, K] (= or, with accumulate, +=) dy^T x of a bf16 [M, N] gradient and the
+    checkpoint of the layer's input x [M, K]; fp32."""
+    M, N = dy.shape
+    K = codes.shape[1]
+    _need(dy, "dy", torch.bfloat16, (M, N))
+    saved = _saved(codes, exps, M, K)
+    if accumulate and dw is None:
+        raise ValueError("accumulate adds to dw: pass it")
+    dw = _result(dw, "dw", torch.float32, (N, K), dy.device, stream)
+    _same_device(dy, codes, exps, dw)
+    _check(_lib().q8_checkpoint_wgrad(_ptr(dy), _ptr(codes), _ptr(exps), saved.group, _ptr(dw),
+                                      int(bool(accumulate)), M, N, K, _stream(stream)),
+           "q8_checkpoint_wgrad")
+    return dw
 
 
 def q8_hessian_accumulate(x: torch.Tensor, H: Optional[torch.Tensor] = None,

@@ -1,0 +1,130 @@
+// k_checkpoint.cu -- 8-bit activation checkpoints.
+//
+// A group of G consecutive values of a row is kept as G int8 codes and one exponent byte b:
+//     e = the smallest whole number with absmax <= 127 * 2^e, clamped to [-126, 121]
+//     code = clamp(round(x * 2^-e), -127, 127)      (ties to even; b = e + 127)
+// The step is a power of two so that code * 2^e is a bf16 number: restoring rounds nothing,
+// and the weight gradient can feed restored values to the bf16 tensor cores exactly.  The
+// price is a step of up to twice absmax / 127.
+//
+// With absmax = 1.f * 2^p (fraction bits f), 127 * 2^e >= absmax first holds at e = p - 6
+// when 1.f <= 127 / 64, else at p - 5; in exponent bytes b = byte(absmax) - 6 (+ 1 when the
+// fraction is above 0x7E0000).  -126 keeps 2^e a normal number, 121 keeps 127 * 2^e finite.
+#include "q8_kernels.cuh"
+
+namespace q8 {
+
+__device__ __forceinline__ uint32_t ckpt_exponent(float amax) {
+    const uint32_t u = __float_as_uint(amax) & 0x7FFFFFFFu;
+    const int b = (int)(u >> 23) - 6 + ((u & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
+    return (uint32_t)min(max(b, 1), 248);
+}
+
+// One thread per 16 values; the G / 16 threads of a group are neighbours in a warp.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_checkpoint_save(const void* __restrict__ x, int64_t n16,
+                                                         int G, int8_t* __restrict__ codes,
+                                                         uint8_t* __restrict__ exps) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int per = G >> 4;
+    const bool live = i < n16;
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+    if (live) {
+        if (BF16) {
+            const uint4* p = reinterpret_cast<const uint4*>(x) + 2 * i;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 w = ldg_stream(p + h);
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[8 * h + 2 * j] = bf16lo(ws[j]);
+                    v[8 * h + 2 * j + 1] = bf16hi(ws[j]);
+                }
+            }
+        } else {
+            const float4* p = reinterpret_cast<const float4*>(x) + 4 * i;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const float4 w = ldg_f4(reinterpret_cast<const float*>(p + h));
+                v[4 * h] = w.x;
+                v[4 * h + 1] = w.y;
+                v[4 * h + 2] = w.z;
+                v[4 * h + 3] = w.w;
+            }
+        }
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    for (int o = per >> 1; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (!live) return;
+    const uint32_t b = ckpt_exponent(amax);
+    const float inv = __uint_as_float((254u - b) << 23);       // 2^-e
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        int c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            c[k] = __float2int_rn(fminf(fmaxf(rintf(v[4 * j + k] * inv), -127.0f), 127.0f));
+        o[j] = pack4_s8(c[0], c[1], c[2], c[3]);
+    }
+    reinterpret_cast<uint4*>(codes)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    if ((i & (per - 1)) == 0) exps[i / per] = (uint8_t)b;
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_checkpoint_load(const int8_t* __restrict__ codes,
+                                                         const uint8_t* __restrict__ exps,
+                                                         int64_t n16, int G, void* __restrict__ y) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n16) return;
+    const int per = G >> 4;
+    const uint4 w = ldg_stream(reinterpret_cast<const uint4*>(codes) + i);
+    const float s = __uint_as_float((uint32_t)__ldg(exps + i / per) << 23);
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = (float)(int8_t)(ws[j >> 2] >> (8 * (j & 3))) * s;
+    if (BF16) {
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)       // exact: the high halves of the fp32 values
+            o[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
+        uint4* out = reinterpret_cast<uint4*>(y) + 2 * i;
+        out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    } else {
+        float4* out = reinterpret_cast<float4*>(y) + 4 * i;
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            out[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+    }
+}
+
+cudaError_t launch_checkpoint_save(const void* x, int x_bf16, int64_t M, int K, int G,
+                                   int8_t* codes, uint8_t* exps, cudaStream_t st) {
+    const int64_t n16 = M * (K / 16);
+    const unsigned grid = (unsigned)((n16 + 255) / 256);
+    if (x_bf16)
+        k_checkpoint_save<true><<<grid, 256, 0, st>>>(x, n16, G, codes, exps);
+    else
+        k_checkpoint_save<false><<<grid, 256, 0, st>>>(x, n16, G, codes, exps);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_checkpoint_load(const int8_t* codes, const uint8_t* exps, int64_t M, int K,
+                                   int G, void* y, int y_bf16, cudaStream_t st) {
+    const int64_t n16 = M * (K / 16);
+    const unsigned grid = (unsigned)((n16 + 255) / 256);
+    if (y_bf16)
+        k_checkpoint_load<true><<<grid, 256, 0, st>>>(codes, exps, n16, G, y);
+    else
+        k_checkpoint_load<false><<<grid, 256, 0, st>>>(codes, exps, n16, G, y);
+    return cudaGetLastError();
+}
+
+}  // namespace q8

@@ -205,6 +205,26 @@ static Q4Plan plan_q4(int64_t M, int64_t N, int64_t K, int G, int sms) {
 }
 static inline bool valid_group(int G) { return G == 32 || G == 64 || G == 128 || G == 256; }
 
+// ------------------------------------------------------------------ adapters
+constexpr int64_t kMaxAdapters = 1024;
+constexpr int64_t kMaxRank = 256;
+static inline bool valid_rank(int64_t r) { return r >= 8 && r <= kMaxRank && r % 8 == 0; }
+
+static q8_status check_adapters(const q8_adapters* ad) {
+    if (!ad) return Q8_ERR_NULL;
+    if (ad->count < 1 || ad->count > kMaxAdapters || !valid_rank(ad->rank)) return Q8_ERR_ARG;
+    return Q8_OK;
+}
+static q8_status check_adapter_pointers(const q8_adapters* ad, const int32_t* ids) {
+    if (!ad->a || !ad->b || !ad->scale || !ids) return Q8_ERR_NULL;
+    if (!aligned16(ad->a) || !aligned16(ad->b) || !aligned4(ad->scale) || !aligned4(ids))
+        return Q8_ERR_ALIGN;
+    return Q8_OK;
+}
+
+// Workspace of the backward pass: g fp32 [M, R].
+static size_t lora_bwd_bytes(int64_t M, int64_t R) { return align_up((size_t)M * R * 4, 256); }
+
 // Self-test of the bounded-wait path: one CTA waits on an mbarrier that nothing will ever
 // complete, with a short limit; the wait gives up, records kStatusWaitTimeout in the status
 // word and the kernel returns normally.
@@ -383,6 +403,10 @@ size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K, int extra) 
         case Q8_OP_GPTQ_INT8:
             if (K > kGptqMaxK || !gptq_block_ok(extra)) return 0;
             return plan_gptq(N, K).bytes;
+        case Q8_OP_LINEAR_W8A16_LORA: return 0;
+        case Q8_OP_LINEAR_W8A16_LORA_BACKWARD:
+            if (M > 0x7fffffff || !valid_rank(extra)) return 0;
+            return lora_bwd_bytes(M, extra);
         case Q8_OP_LINEAR_DQ8CA_Q4GSW: {
             if (!valid_group(extra) || K % 128 != 0 || K % extra != 0) return 0;
             int sms = 0;
@@ -391,6 +415,173 @@ size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K, int extra) 
         }
     }
     return 0;
+}
+
+q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
+                               const float* bias, const q8_adapters* ad, const int32_t* ids,
+                               void* y, q8_dtype yt, float* h, int64_t M, int64_t N, int64_t K,
+                               void* workspace, size_t ws_bytes, void* stream) {
+    if (yt != Q8_F32 && yt != Q8_BF16) return Q8_ERR_ARG;
+    if (M < 0 || M > 0x7fffffff || N < 1 || N > 0x7fffffff) return Q8_ERR_SHAPE;
+    Q8_TRY(check_k(K));
+    Q8_TRY(check_adapters(ad));
+    if (M == 0) return Q8_OK;
+    if (!x || !q || !s_w || !y || !h) return Q8_ERR_NULL;
+    Q8_TRY(check_adapter_pointers(ad, ids));
+    if (!aligned16(x) || !aligned16(q) || !aligned16(y) || !aligned16(h) || !aligned4(s_w) ||
+        !aligned4(bias))
+        return Q8_ERR_ALIGN;
+    int sms = 0;
+    int* status = nullptr;
+    Q8_TRY(current_device(sms, &status));
+    cudaStream_t st = (cudaStream_t)stream;
+    const int R = (int)ad->rank, L = (int)ad->count;
+    Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
+                                       ad->scale, ids, h, M, (int)K, R, L, st)));
+    LoraGemm a = {};
+    a.q = q;
+    a.t = (const uint16_t*)x;
+    a.s_w = s_w;
+    a.bias = bias;
+    a.out = y;
+    a.out_bf16 = yt == Q8_BF16;
+    a.P = (int)N;
+    a.C = (int)K;
+    a.T = M;
+    a.ids = ids;
+    a.low = (const uint16_t*)ad->b;
+    a.h = h;
+    a.scale = ad->scale;
+    a.R = R;
+    a.L = L;
+    return launched(launch_lora_gemm(LORA_FWD, a, st));
+}
+
+q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const float* s_w,
+                                        const q8_adapters* ad, const int32_t* ids,
+                                        const float* h, const q8_saved_input* input, void* dx,
+                                        float* da, float* db, int accumulate, int64_t M,
+                                        int64_t N, int64_t K, void* workspace, size_t ws_bytes,
+                                        void* stream) {
+    if (M < 0 || M > 0x7fffffff || N < 1 || N > 0x7fffffff || N % 8) return Q8_ERR_SHAPE;
+    Q8_TRY(check_k(K));
+    Q8_TRY(check_adapters(ad));
+    if (da && M > 0) {
+        if (!input) return Q8_ERR_NULL;
+        if (input->group != 0 && !valid_group(input->group)) return Q8_ERR_ARG;
+        if (input->group != 0 && K % input->group) return Q8_ERR_SHAPE;
+        if (!input->x || (input->group != 0 && !input->exps)) return Q8_ERR_NULL;
+        if (!aligned16(input->x)) return Q8_ERR_ALIGN;
+    }
+    if (!aligned16(da) || !aligned16(db)) return Q8_ERR_ALIGN;
+    if (!dx && !da && !db) return Q8_OK;
+    const int R = (int)ad->rank, L = (int)ad->count;
+    const size_t an = (size_t)L * R * (size_t)K * 4, bn = (size_t)L * (size_t)N * R * 4;
+    cudaStream_t st = (cudaStream_t)stream;
+    int sms = 0;
+    int* status = nullptr;
+    if (M == 0) {
+        if (accumulate || (!da && !db)) return Q8_OK;
+        Q8_TRY(current_device(sms, &status));
+        if (da) Q8_TRY(launched(cudaMemsetAsync(da, 0, an, st)));
+        if (db) Q8_TRY(launched(cudaMemsetAsync(db, 0, bn, st)));
+        return Q8_OK;
+    }
+    if (!dy || (dx && (!q || !s_w)) || (db && !h)) return Q8_ERR_NULL;
+    Q8_TRY(check_adapter_pointers(ad, ids));
+    if (!aligned16(dy) || !aligned16(q) || !aligned16(dx) || !aligned16(h) || !aligned4(s_w))
+        return Q8_ERR_ALIGN;
+    const size_t need = lora_bwd_bytes(M, R);
+    if (!workspace || ws_bytes < need) return Q8_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return Q8_ERR_ALIGN;
+    Q8_TRY(current_device(sms, &status));
+    float* g = (float*)workspace;
+    if (dx || da)
+        Q8_TRY(launched(launch_lora_shrink(true, (const uint16_t*)dy, (const uint16_t*)ad->b,
+                                           ad->scale, ids, g, M, (int)N, R, L, st)));
+    if (dx) {
+        LoraGemm a = {};
+        a.q = q;
+        a.t = (const uint16_t*)dy;
+        a.s_w = s_w;
+        a.out = dx;
+        a.out_bf16 = 1;
+        a.P = (int)K;
+        a.C = (int)N;
+        a.T = M;
+        a.ids = ids;
+        a.low = (const uint16_t*)ad->a;
+        a.h = g;
+        a.scale = ad->scale;
+        a.R = R;
+        a.L = L;
+        Q8_TRY(launched(launch_lora_gemm(LORA_DGRAD, a, st)));
+    }
+    if (da)
+        Q8_TRY(launched(launch_lora_wgrad(false, input->x, input->exps, input->group, g,
+                                          ad->scale, ids, da, accumulate, M, (int)K, R, L, st)));
+    if (db)
+        Q8_TRY(launched(launch_lora_wgrad(true, dy, nullptr, 0, h, ad->scale, ids, db, accumulate,
+                                          M, (int)N, R, L, st)));
+    return Q8_OK;
+}
+
+q8_status q8_checkpoint_save(const void* x, q8_dtype xt, int64_t M, int64_t K, int group,
+                             int8_t* codes, uint8_t* exps, void* stream) {
+    if ((xt != Q8_F32 && xt != Q8_BF16) || !valid_group(group)) return Q8_ERR_ARG;
+    if (M < 0 || M > 0x7fffffff) return Q8_ERR_SHAPE;
+    Q8_TRY(check_k(K));
+    if (K % group) return Q8_ERR_SHAPE;
+    if (M == 0) return Q8_OK;
+    if (!x || !codes || !exps) return Q8_ERR_NULL;
+    if (!aligned16(x) || !aligned16(codes)) return Q8_ERR_ALIGN;
+    int sms = 0;
+    Q8_TRY(current_device(sms));
+    return launched(launch_checkpoint_save(x, xt == Q8_BF16, M, (int)K, group, codes, exps,
+                                           (cudaStream_t)stream));
+}
+
+q8_status q8_checkpoint_load(const int8_t* codes, const uint8_t* exps, int group, void* y,
+                             q8_dtype yt, int64_t M, int64_t K, void* stream) {
+    if ((yt != Q8_F32 && yt != Q8_BF16) || !valid_group(group)) return Q8_ERR_ARG;
+    if (M < 0 || M > 0x7fffffff) return Q8_ERR_SHAPE;
+    Q8_TRY(check_k(K));
+    if (K % group) return Q8_ERR_SHAPE;
+    if (M == 0) return Q8_OK;
+    if (!codes || !exps || !y) return Q8_ERR_NULL;
+    if (!aligned16(y) || !aligned16(codes)) return Q8_ERR_ALIGN;
+    int sms = 0;
+    Q8_TRY(current_device(sms));
+    return launched(launch_checkpoint_load(codes, exps, M, (int)K, group, y, yt == Q8_BF16,
+                                           (cudaStream_t)stream));
+}
+
+q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t* exps, int group,
+                              float* dw, int accumulate, int64_t M, int64_t N, int64_t K,
+                              void* stream) {
+    if (!valid_group(group)) return Q8_ERR_ARG;
+    if (M < 0 || M > 0x7fffffff || N < 1 || N > 0x7fffffff || N % 8) return Q8_ERR_SHAPE;
+    Q8_TRY(check_k(K));
+    if (K % group) return Q8_ERR_SHAPE;
+    if (M == 0 && accumulate) return Q8_OK;
+    if (!dw || (M > 0 && (!dy || !codes || !exps))) return Q8_ERR_NULL;
+    if (!aligned16(dw) || !aligned16(dy) || !aligned16(codes)) return Q8_ERR_ALIGN;
+    int sms = 0;
+    int* status = nullptr;
+    Q8_TRY(current_device(sms, &status));
+    cudaStream_t st = (cudaStream_t)stream;
+    if (M == 0) return launched(cudaMemsetAsync(dw, 0, (size_t)N * (size_t)K * 4, st));
+    LoraGemm a = {};
+    a.q = codes;
+    a.t = (const uint16_t*)dy;
+    a.exps = exps;
+    a.G = group;
+    a.out = dw;
+    a.accumulate = accumulate != 0;
+    a.P = (int)K;
+    a.C = (int)M;
+    a.T = N;
+    return launched(launch_lora_gemm(LORA_WGRAD, a, st));
 }
 
 q8_status q8_quantize_weight_nvfp4(const float* W, int64_t N, int64_t K, uint8_t* q4, uint8_t* sf,

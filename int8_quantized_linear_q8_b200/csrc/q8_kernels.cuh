@@ -120,6 +120,45 @@ cudaError_t launch_q4_gemm_tc(const uint16_t* wb, const uint16_t* xz, const floa
                               const float* s, float* y, int G, int64_t M, int64_t N, int K,
                               cudaStream_t st, int num_sms, int* status);
 
+// k_checkpoint.cu
+cudaError_t launch_checkpoint_save(const void* x, int x_bf16, int64_t M, int K, int G,
+                                   int8_t* codes, uint8_t* exps, cudaStream_t st);
+cudaError_t launch_checkpoint_load(const int8_t* codes, const uint8_t* exps, int64_t M, int K,
+                                   int G, void* y, int y_bf16, cudaStream_t st);
+
+// k_lora.cu
+// The three products of the adapter linear and of the checkpoint's weight gradient,
+//   out[t, p] = sum_c P(p, c) T(t, c) + ...:
+//   LORA_FWD    p = n, t = m, c = k:  q[p, c] x[t, c], times s_w[p], + bias[p] + adapter term
+//   LORA_DGRAD  p = k, t = m, c = n:  s_w[c] q[c, p] dy[t, c], + adapter term
+//   LORA_WGRAD  p = k, t = n, c = m:  codes[c, p] 2^e dy[c, t]
+enum { LORA_FWD = 0, LORA_DGRAD = 1, LORA_WGRAD = 2 };
+struct LoraGemm {
+    const int8_t* q;            // int8 operand
+    const uint16_t* t;          // bf16 operand
+    const float* s_w;
+    const float* bias;          // nullable
+    const uint8_t* exps;        // LORA_WGRAD
+    int G;
+    void* out;
+    int out_bf16, accumulate;
+    int P, C;
+    int64_t T;
+    // adapter term (ids == nullptr: none): low = b (LORA_FWD) or a (LORA_DGRAD)
+    const int32_t* ids;
+    const uint16_t* low;
+    const float* h;             // [T, R]; LORA_DGRAD: g, scale included
+    const float* scale;
+    int R, L;
+};
+cudaError_t launch_lora_gemm(int mode, const LoraGemm& a, cudaStream_t st);
+cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, const float* scale,
+                               const int32_t* ids, float* h, int64_t M, int C, int R, int L,
+                               cudaStream_t st);
+cudaError_t launch_lora_wgrad(bool db, const void* x, const uint8_t* exps, int G, const float* low,
+                              const float* scale, const int32_t* ids, float* out, int accumulate,
+                              int64_t M, int P, int R, int L, cudaStream_t st);
+
 // k_gptq.cu
 struct GptqPlan {
     size_t buf0, buf1, buf2, w, err, dead, bytes;     // byte offsets in the workspace
