@@ -1,0 +1,709 @@
+// k_lora_tc.cu -- the three large products of the adapter linear and of the 8-bit checkpoint
+// on the tcgen05 tensor cores, one bf16 operand and one int8 operand:
+//
+//   out[t, p] = sum_c P(p, c) T(t, c) + ...
+//   LORA_FWD    p = n, t = m, c = k   P = q[p, c],            T = x[t, c]
+//               y = s_w[p] * sum + bias[p] + sum_r b[i][p, r] (scale[i] h[t, r]),  i = ids[t]
+//   LORA_DGRAD  p = k, t = m, c = n   P = s_w[c] q[c, p],     T = dy[t, c]
+//               dx = sum + sum_r a[i][r, p] g[t, r]
+//   LORA_WGRAD  p = k, t = n, c = m   P = codes[c, p] 2^e,    T = dy[c, t]
+//
+// The int8 operand stays int8 in HBM and L2 and becomes bf16 in shared memory: exactly for the
+// forward pass (codes; s_w comes after the sum) and the weight gradient (codes times a power
+// of two), with one rounding of s_w * q for dgrad, where s_w varies along the sum.
+//
+// A pair of CTAs (a cluster of two) computes a tile of 256 p x BN t with cta_group::2 MMAs:
+// each CTA holds 128 rows of P, half of the T rows, and the accumulators of its own 128 rows
+// (BN columns of tensor memory).  Against one CTA with 128 x 256 tiles this halves the shared
+// memory traffic of the T operand, which leaves room for the conversion's.  BN is the T extent
+// split evenly into tiles of at most 256, rounded up to 32.
+//
+// The adapter term is more of the same contraction: for the adapters that the tile's tokens
+// use (a list made per tile beforehand), the rank's columns of b (or a) on the P side and of
+// scale * h (or g) on the T side, zero for tokens of other adapters.  h is split into two bf16
+// parts (high and the rest: off by at most 2^-17), so an adapter takes 2 * rank columns.  Forward
+// it goes to the other accumulator buffer, since s_w applies to the base sum alone.
+//
+// Roles (18 warps): 0 TMA producer; 1 tensor-memory allocator and, in the pair's first CTA,
+// MMA issuer; 2-9 converters, two groups of four that take every other stage; 10-17
+// epilogue.  A stage is 64 of c: the int8 box (8 KB), the bf16 P tile that the converters write
+// (16 KB) and the T tile (16 KB, TMA).  Every wait is bounded.
+#include "q8_kernels.cuh"
+
+namespace q8 {
+
+constexpr int LT_BK = 64;
+constexpr int LT_STAGES = 5;
+constexpr int LT_A = 128 * 128, LT_B = 128 * 128, LT_RAW = 128 * 64;
+constexpr int LT_STAGE = LT_A + LT_B + LT_RAW;
+constexpr int LT_CONV = 8, LT_EPI = 8;
+constexpr int LT_THREADS = 32 * (2 + LT_CONV + LT_EPI);
+constexpr int LT_SMEM = LT_STAGES * LT_STAGE + 1024 + 512;
+static_assert(LT_STAGE % 1024 == 0 && LT_SMEM <= 227 * 1024, "shared memory");
+
+// ------------------------------------------------------------------ cluster and tcgen05
+__device__ __forceinline__ uint32_t lt_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t lt_map(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void lt_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// arrive on a barrier of either CTA of the pair (a shared::cluster address)
+__device__ __forceinline__ void lt_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+// mbar_wait for barriers on which the other CTA's threads arrive
+__device__ __forceinline__ bool lt_wait(uint64_t* bar, uint32_t parity, int* status,
+                                        volatile int* abort_flag) {
+    const unsigned long long t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSleepNs)
+            : "memory");
+        if (ok) return true;
+        if ((i & 7u) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                *abort_flag = 1;
+                atomicExch(status, kStatusWaitTimeout);
+                return false;
+            }
+        }
+    }
+}
+// TMA load into this CTA's shared memory, completion on a barrier of the pair's first CTA
+__device__ __forceinline__ void lt_tma_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+// 128-byte-swizzled operand tiles.  K-major: rows of 64 c, groups of 8 rows 1024 bytes apart.
+// MN-major: blocks of 64 rows (8192 bytes: 64 c of 128 bytes), groups of 8 c 1024 bytes apart.
+__device__ __forceinline__ uint64_t lt_desc(uint32_t saddr, bool mn_major) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(mn_major ? 8192 >> 4 : 1) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16: bf16 operands, fp32 accumulator, M = 256 over the pair
+__device__ __forceinline__ uint32_t lt_idesc(int bn, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(bn >> 3) << 17) | (16u << 24);
+}
+__device__ __forceinline__ void lt_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// arrives on the barrier at the same offset in both CTAs once the MMAs issued so far are done
+__device__ __forceinline__ void lt_commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+        ".b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void lt_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void lt_ld_wait() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+// ------------------------------------------------------------------------- conversion
+// Four int8 codes -> bf16 (b0, b1), (b2, b3), exact: as s8x4_to_bf16x2_eo, in order.
+__device__ __forceinline__ void s8x4_to_bf16x2_seq(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t l = __byte_perm(w, 0, 0x4140), h = __byte_perm(w, 0, 0x4342);
+    lo = bf16x2_sub(lop_and_or(l, 0x007F007Fu, 0x43004300u),
+                    lop_and_or(l, 0x00800080u, 0x43004300u));
+    hi = bf16x2_sub(lop_and_or(h, 0x007F007Fu, 0x43004300u),
+                    lop_and_or(h, 0x00800080u, 0x43004300u));
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16_bits_rn(float v) {
+    return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// What a converter thread multiplies its codes by: nothing (forward), s_w as the bf16 pair
+// hi + lo (hi * q + lo * q is rounded once, to bf16), or a power of two.
+struct LtScale {
+    uint32_t hi, lo;
+};
+template <int MODE>
+__device__ __forceinline__ LtScale lt_scale(const LoraGemm& a, int c, int p) {
+    LtScale s = {0u, 0u};
+    if (MODE == LORA_DGRAD && c < a.C) {
+        const float v = __ldg(a.s_w + c);
+        const uint32_t h = bf16_bits_rn(v);
+        const uint32_t l = bf16_bits_rn(v - __uint_as_float(h << 16));
+        s.hi = h | h << 16;
+        s.lo = l | l << 16;
+    }
+    if (MODE == LORA_WGRAD && c < a.C && p < a.P) {
+        const uint32_t b = __ldg(a.exps + (int64_t)c * (a.P >> a.gshift) + (p >> a.gshift));
+        s.hi = b << 7 | b << 23;
+    }
+    return s;
+}
+template <int MODE>
+__device__ __forceinline__ uint32_t lt_apply(uint32_t v, const LtScale& s) {
+    if (MODE == LORA_DGRAD) return bf16x2_fma(v, s.hi, bf16x2_mul(v, s.lo));
+    if (MODE == LORA_WGRAD) return bf16x2_mul(v, s.hi);
+    return v;
+}
+
+// the tile's adapter list: [0] their number, then their ids in ascending order
+constexpr int LT_LIST = 260;
+
+// ------------------------------------------------------------------------- the kernel
+template <int MODE>
+__global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
+    const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap tmap,
+    const LoraGemm a, int BN, int num_p, int num_t, int* status) {
+    constexpr bool A_MN = MODE != LORA_FWD;             // int8 operand with p contiguous
+    constexpr bool B_MN = MODE == LORA_WGRAD;           // bf16 operand with t contiguous
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint64_t* rawfull = reinterpret_cast<uint64_t*>(smem + LT_STAGES * LT_STAGE);
+    uint64_t* bfull = rawfull + LT_STAGES;              // first CTA: both halves of T landed
+    uint64_t* aready = bfull + LT_STAGES;               // first CTA: both CTAs converted
+    uint64_t* empty = aready + LT_STAGES;
+    uint64_t* tfull = empty + LT_STAGES;
+    uint64_t* tempty = tfull + 2;                       // first CTA
+    uint64_t* mma_done = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = lt_rank();
+    const int units = num_p * num_t;
+    const int nk = (a.C + LT_BK - 1) / LT_BK;
+    const int half = BN >> 1;
+    // Tiles run over t first, in blocks of 16 t tiles: the pairs that run at once share both
+    // operands through L2 and the int8 operand is read from HBM once per block.
+    auto tile_of = [&](int u, int& p0, int& t0) {
+        const int full = num_p * 16, blk = u / full, rem = u - blk * full;
+        const int tb = min(16, num_t - blk * 16);
+        p0 = rem / tb * 256 + (int)rank * 128;
+        t0 = (blk * 16 + rem % tb) * BN;
+    };
+    // stages of adapter columns after the tile's nk base stages
+    auto low_stages = [&](int t0) {
+        if (MODE == LORA_WGRAD || !a.ids) return 0;
+        const int cnt = __ldg(a.lists + (int64_t)(t0 / BN) * LT_LIST);
+        return (cnt * 2 * a.R + LT_BK - 1) / LT_BK;
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < LT_STAGES; ++s) {
+            mbar_init(&rawfull[s], 1);
+            mbar_init(&bfull[s], 1);
+            mbar_init(&aready[s], 8);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 2 * LT_EPI);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(tmem_slot)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    lt_cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- producer
+        if (lane == 0) {
+            tma_prefetch_desc(&pmap);
+            tma_prefetch_desc(&tmap);
+        }
+        const uint32_t bfull0 = lt_map(smem_u32(bfull), 0);
+        int s = 0, it = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
+            int p0, t0;
+            tile_of(u, p0, t0);
+            const int total = nk + low_stages(t0);
+            for (int kb = 0; kb < total; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, status, abort_flag));
+                if (!ok) break;
+                if (lane == 0) {
+                    uint8_t* st = smem + (size_t)s * LT_STAGE;
+                    if (kb < nk) {
+                        const int c0 = kb * LT_BK;
+                        mbar_expect_tx(&rawfull[s], LT_RAW);
+                        if (A_MN)
+                            tma_load_2d(st + LT_A + LT_B, &pmap, p0, c0, &rawfull[s]);
+                        else
+                            tma_load_2d(st + LT_A + LT_B, &pmap, c0, p0, &rawfull[s]);
+                        if (rank == 0) mbar_expect_tx(&bfull[s], (uint32_t)BN * 128u);
+                        const uint32_t bt = smem_u32(st + LT_A);
+                        const int tr = t0 + (int)rank * half;
+                        if (B_MN)
+                            for (int b = 0; b < half / 64; ++b)
+                                lt_tma_pair(bt + b * 8192, &tmap, (tr + b * 64) * 2, c0,
+                                            bfull0 + s * 8);
+                        else
+                            lt_tma_pair(bt, &tmap, c0 * 2, tr, bfull0 + s * 8);
+                    } else {                            // written by the converters alone
+                        mbar_arrive(&rawfull[s]);
+                        if (rank == 0) mbar_arrive(&bfull[s]);
+                    }
+                }
+                ++it;
+                if (++s == LT_STAGES) { s = 0; ph ^= 1u; }
+            }
+        }
+        // copies issued here have landed before the CTA leaves
+        for (int i = max(0, it - LT_STAGES); i < it; ++i) {
+            mbar_drain(&rawfull[i % LT_STAGES], (uint32_t)(i / LT_STAGES) & 1u, status);
+            if (rank == 0)
+                mbar_drain(&bfull[i % LT_STAGES], (uint32_t)(i / LT_STAGES) & 1u, status);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer
+        if (rank == 0) {
+            const uint32_t idesc = lt_idesc(BN, A_MN, B_MN);
+            int s = 0, buf = 0;
+            uint32_t ph = 0, bph = 0;
+            bool ok = true;
+            for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
+                int p0, t0;
+                tile_of(u, p0, t0);
+                const int total = nk + low_stages(t0);
+                for (int kb = 0; kb < total && ok; ++kb) {
+                    const bool fresh = kb == 0 || (MODE == LORA_FWD && kb == nk);
+                    if (fresh) {
+                        if (kb) {                       // base sum complete
+                            lt_commit(&tfull[buf]);
+                            if (++buf == 2) { buf = 0; bph ^= 1u; }
+                        }
+                        ok = __all_sync(0xffffffffu,
+                                        lt_wait(&tempty[buf], bph ^ 1u, status, abort_flag));
+                        if (!ok) break;
+                    }
+                    ok = __all_sync(0xffffffffu, lt_wait(&aready[s], ph, status, abort_flag) &&
+                                                     lt_wait(&bfull[s], ph, status, abort_flag));
+                    if (!ok) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t st = smem_u32(smem + (size_t)s * LT_STAGE);
+                    const uint64_t ad = lt_desc(st, A_MN), bd = lt_desc(st + LT_A, B_MN);
+                    const uint32_t d = tmem + (uint32_t)(buf * 256);
+#pragma unroll
+                    for (int k = 0; k < LT_BK / 16; ++k)
+                        lt_mma(d, ad + (A_MN ? 128 : 2) * k, bd + (B_MN ? 128 : 2) * k, idesc,
+                               !(fresh && k == 0));
+                    lt_commit(&empty[s]);
+                    if (++s == LT_STAGES) { s = 0; ph ^= 1u; }
+                }
+                if (!ok) break;
+                lt_commit(&tfull[buf]);
+                if (++buf == 2) { buf = 0; bph ^= 1u; }
+            }
+            lt_commit(mma_done);                        // before tensor memory is released
+            mbar_drain(mma_done, 0, status);
+        }
+        __syncwarp();
+    } else if (warp < 2 + LT_CONV) {
+        // ---------------------------------------------------------------- converters
+        const int grp = (warp - 2) >> 2;
+        const int tid = threadIdx.x - 64 - grp * 128;
+        const uint32_t aready0 = lt_map(smem_u32(aready), 0);
+        int s = 0, it = 0;
+        uint32_t ph = 0;
+        bool live = true;
+        for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
+            int p0, t0;
+            tile_of(u, p0, t0);
+            const int total = nk + low_stages(t0);
+            // the next stage's scales, loaded a turn ahead
+            LtScale nxt[4];
+            if (A_MN) {
+                const int kb = (it & 1) == grp ? 0 : 1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    nxt[i] = lt_scale<MODE>(a, kb * LT_BK + i * 16 + (tid >> 3),
+                                            p0 + (tid & 7) * 16);
+            }
+            for (int kb = 0; kb < total; ++kb) {
+                if ((it & 1) == grp) {
+                    const bool okw = mbar_wait(&rawfull[s], ph, status, abort_flag);
+                    live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
+                    const uint32_t at = smem_u32(smem + (size_t)s * LT_STAGE);
+                    if (live && kb < nk) {
+                        const uint32_t raw = at + LT_A + LT_B;
+                        if (!A_MN) {
+                            // thread: row tid, 64 codes (16-byte pieces swizzled over 64)
+                            uint4 w[4];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                w[c] = lds128(raw + tid * 64 + ((c ^ ((tid >> 1) & 3)) << 4));
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t o[8];
+                                s8x4_to_bf16x2_seq(w[c].x, o[0], o[1]);
+                                s8x4_to_bf16x2_seq(w[c].y, o[2], o[3]);
+                                s8x4_to_bf16x2_seq(w[c].z, o[4], o[5]);
+                                s8x4_to_bf16x2_seq(w[c].w, o[6], o[7]);
+                                const uint32_t row = at + tid * 128;
+                                sts128(row + (((2 * c) ^ (tid & 7)) << 4), o[0], o[1], o[2], o[3]);
+                                sts128(row + (((2 * c + 1) ^ (tid & 7)) << 4), o[4], o[5], o[6],
+                                       o[7]);
+                            }
+                        } else {
+                            // thread: 16 codes of p in each of 4 rows of c; the two 16-byte
+                            // pieces are written in an order that keeps the 64-p blocks of a
+                            // row on different banks
+                            LtScale cur[4];
+                            uint4 w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                cur[i] = nxt[i];
+                                w[i] = lds128(raw + (i * 16 + (tid >> 3)) * 128 + (tid & 7) * 16);
+                            }
+                            if (kb + 2 < nk)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    nxt[i] = lt_scale<MODE>(
+                                        a, (kb + 2) * LT_BK + i * 16 + (tid >> 3),
+                                        p0 + (tid & 7) * 16);
+                            const int ch = tid & 7, odd = ch >> 2;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t o[8];
+                                s8x4_to_bf16x2_seq(w[i].x, o[0], o[1]);
+                                s8x4_to_bf16x2_seq(w[i].y, o[2], o[3]);
+                                s8x4_to_bf16x2_seq(w[i].z, o[4], o[5]);
+                                s8x4_to_bf16x2_seq(w[i].w, o[6], o[7]);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) o[j] = lt_apply<MODE>(o[j], cur[i]);
+                                const int c = i * 16 + (tid >> 3);
+                                const uint32_t row = at + odd * 8192 + c * 128;
+                                const int j0 = (ch & 3) * 2;
+                                const uint32_t e0 = odd ? o[4] : o[0], e1 = odd ? o[5] : o[1];
+                                const uint32_t e2 = odd ? o[6] : o[2], e3 = odd ? o[7] : o[3];
+                                const uint32_t f0 = odd ? o[0] : o[4], f1 = odd ? o[1] : o[5];
+                                const uint32_t f2 = odd ? o[2] : o[6], f3 = odd ? o[3] : o[7];
+                                sts128(row + (((j0 + odd) ^ (c & 7)) << 4), e0, e1, e2, e3);
+                                sts128(row + (((j0 + 1 - odd) ^ (c & 7)) << 4), f0, f1, f2, f3);
+                            }
+                        }
+                    }
+                    if (MODE != LORA_WGRAD && live && kb >= nk) {
+                        // Columns (kb - nk) * 64 .. +64 of the adapter term, in pieces of 8:
+                        // per adapter of the list R / 8 pieces against the high parts and
+                        // R / 8 against the rest.
+                        const int rc = a.R >> 3;
+                        const int* list = a.lists + (int64_t)(t0 / BN) * LT_LIST;
+                        const int cnt = __ldg(list);
+                        const int t = t0 + (int)rank * half + tid;
+                        const bool row_t = tid < half;
+                        const int id = row_t && t < a.T ? __ldg(a.ids + t) : -1;
+#pragma unroll 2
+                        for (int c = 0; c < 8; ++c) {
+                            const int piece = (kb - nk) * 8 + c;
+                            const int e = piece / (2 * rc);
+                            const int in = piece - e * 2 * rc;
+                            const int low = in >= rc, r0 = (in - low * rc) * 8;
+                            const int i = e < cnt ? __ldg(list + 1 + e) : -1;
+                            if (!A_MN) {
+                                uint4 w = make_uint4(0, 0, 0, 0);
+                                const int p = p0 + tid;
+                                if (i >= 0 && p < a.P)
+                                    w = ldg_keep(a.low + ((int64_t)i * a.P + p) * a.R + r0);
+                                sts128(at + tid * 128 + ((c ^ (tid & 7)) << 4), w.x, w.y, w.z,
+                                       w.w);
+                            } else {
+                                // row 8 c + (tid >> 4) of the 64, piece tid & 15 of 128 p
+                                const int r = tid >> 4, pc = tid & 15;
+                                const int p = p0 + pc * 8;
+                                uint4 w = make_uint4(0, 0, 0, 0);
+                                if (i >= 0 && p < a.P)
+                                    w = ldg_keep(a.low + ((int64_t)i * a.R + r0 + r) * a.P + p);
+                                sts128(at + (pc >> 3) * 8192 + (8 * c + r) * 128 +
+                                           (((pc & 7) ^ r) << 4),
+                                       w.x, w.y, w.z, w.w);
+                            }
+                            if (row_t) {
+                                uint32_t o[4] = {0, 0, 0, 0};
+                                if (i >= 0 && id == i) {
+                                    const float sc = MODE == LORA_FWD ? __ldg(a.scale + i) : 1.0f;
+                                    const float4* hp = reinterpret_cast<const float4*>(
+                                        a.h + (int64_t)t * a.R + r0);
+                                    const float4 h0 = hp[0], h1 = hp[1];
+                                    const float v[8] = {h0.x * sc, h0.y * sc, h0.z * sc,
+                                                        h0.w * sc, h1.x * sc, h1.y * sc,
+                                                        h1.z * sc, h1.w * sc};
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) {
+                                        uint32_t b = bf16_bits_rn(v[j]);
+                                        if (low) b = bf16_bits_rn(v[j] - __uint_as_float(b << 16));
+                                        o[j >> 1] |= b << (16 * (j & 1));
+                                    }
+                                }
+                                sts128(at + LT_A + tid * 128 + ((c ^ (tid & 7)) << 4), o[0], o[1],
+                                       o[2], o[3]);
+                            }
+                        }
+                    }
+                    // make the generic-proxy writes visible to the tensor core, then hand over
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) lt_arrive(aready0 + s * 8);
+                }
+                ++it;
+                if (++s == LT_STAGES) { s = 0; ph ^= 1u; }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- epilogue
+        // warp w: lane quarter w % 4 of the CTA's 128 p, every other chunk of 32 t
+        const int q = warp & 3, par = (warp - 2 - LT_CONV) >> 2;
+        const uint32_t tempty0 = lt_map(smem_u32(tempty), 0);
+        int buf = 0;
+        uint32_t bph = 0;
+        bool live = true;
+        for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
+            int p0, t0;
+            tile_of(u, p0, t0);
+            const int p = p0 + q * 32 + lane;
+            const bool low = MODE == LORA_FWD && low_stages(t0) > 0;
+            float sw = 1.0f, bs = 0.0f;
+            if (MODE == LORA_FWD && p < a.P) {
+                sw = __ldg(a.s_w + p);
+                if (a.bias) bs = __ldg(a.bias + p);
+            }
+            const int buf2 = buf ^ 1;
+            const uint32_t bph2 = buf == 1 ? bph ^ 1u : bph;
+            bool okw = mbar_wait(&tfull[buf], bph, status, abort_flag);
+            if (low) okw = mbar_wait(&tfull[buf2], bph2, status, abort_flag) && okw;
+            live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+            for (int c = par; live && c < BN / 32; c += 2) {
+                uint32_t r[32];
+                lt_ld32(lanes + (uint32_t)(buf * 256 + c * 32), r);
+                float v[32];
+                if (low) {
+                    uint32_t r2[32];
+                    lt_ld32(lanes + (uint32_t)(buf2 * 256 + c * 32), r2);
+                    lt_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = fmaf(__uint_as_float(r[j]), sw, bs) + __uint_as_float(r2[j]);
+                } else {
+                    lt_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = MODE == LORA_FWD ? fmaf(__uint_as_float(r[j]), sw, bs)
+                                                : __uint_as_float(r[j]);
+                }
+                const int tc = t0 + c * 32;
+                if (MODE != LORA_WGRAD && a.out_bf16 && (a.P & 1) == 0) {
+                    // neighbouring lanes exchange, so that each stores two p of one t
+                    uint32_t* out = reinterpret_cast<uint32_t*>(a.out);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const bool od = lane & 1;
+                        const float got =
+                            __shfl_xor_sync(0xffffffffu, od ? v[j] : v[j + 1], 1);
+                        const uint32_t lo = bf16_bits_rn(od ? got : v[j]);
+                        const uint32_t hi = bf16_bits_rn(od ? v[j + 1] : got);
+                        const int64_t t = tc + j + (od ? 1 : 0);
+                        if (t < a.T && p < a.P)
+                            out[(t * a.P + (p & ~1)) >> 1] = lo | hi << 16;
+                    }
+                } else if (MODE != LORA_WGRAD && a.out_bf16) {
+                    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (tc + j < a.T && p < a.P)
+                            out[(int64_t)(tc + j) * a.P + p] = __float2bfloat16_rn(v[j]);
+                } else {
+                    float* out = reinterpret_cast<float*>(a.out) + (int64_t)tc * a.P + p;
+                    if (MODE == LORA_WGRAD && a.accumulate) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (tc + j < a.T && p < a.P) v[j] += out[(int64_t)j * a.P];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (tc + j < a.T && p < a.P) out[(int64_t)j * a.P] = v[j];
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                lt_arrive(tempty0 + buf * 8);
+                if (low) lt_arrive(tempty0 + buf2 * 8);
+            }
+            if (!low) {
+                if (++buf == 2) { buf = 0; bph ^= 1u; }
+            } else {
+                bph ^= 1u;                              // two buffers further: the same one
+            }
+        }
+    }
+
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    lt_cluster_sync();      // the other CTA's MMAs, copies and arrivals here are complete
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                     : "memory");
+}
+
+// The adapters that the tokens of each tile use, ascending; a CTA per tile.
+__global__ __launch_bounds__(256) void k_lora_lists(const int32_t* __restrict__ ids, int64_t T,
+                                                    int BN, int L, int* __restrict__ lists) {
+    __shared__ uint32_t seen[32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x < 32) seen[threadIdx.x] = 0;
+    __syncthreads();
+    const int64_t t = (int64_t)blockIdx.x * BN + threadIdx.x;
+    if ((int)threadIdx.x < BN && t < T) {
+        const int id = __ldg(ids + t);
+        if (id >= 0 && id < L) atomicOr(&seen[id >> 5], 1u << (id & 31));
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int* out = lists + (int64_t)blockIdx.x * LT_LIST;
+        uint32_t w = seen[threadIdx.x];
+        int n = __popc(w), before = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, before, o);
+            if ((int)threadIdx.x >= o) before += v;
+        }
+        if (threadIdx.x == 31) out[0] = before;
+        before -= n;
+        while (w) {
+            const int b = __ffs(w) - 1;
+            w &= w - 1;
+            out[1 + before++] = (int)threadIdx.x * 32 + b;
+        }
+    }
+}
+
+// ----------------------------------------------------------------------- host side
+int lora_tc_tile(int mode, int64_t T) {
+    const int64_t tiles = (T + 255) / 256;
+    const int step = mode == LORA_WGRAD ? 128 : 32;
+    const int64_t each = (T + tiles - 1) / tiles;
+    return (int)((each + step - 1) / step * step);
+}
+size_t lora_list_bytes(int64_t T) {
+    const int64_t BN = lora_tc_tile(LORA_FWD, T);
+    return (size_t)((T + BN - 1) / BN) * LT_LIST * sizeof(int);
+}
+cudaError_t launch_lora_lists(const int32_t* ids, int64_t T, int L, int* lists, cudaStream_t st) {
+    const int BN = lora_tc_tile(LORA_FWD, T);
+    k_lora_lists<<<(unsigned)((T + BN - 1) / BN), 256, 0, st>>>(ids, T, BN, L, lists);
+    return cudaGetLastError();
+}
+
+template <int MODE>
+static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, int* status) {
+    const int BN = lora_tc_tile(MODE, a.T);
+    CUtensorMap pm, tm;
+    const bool okp = MODE == LORA_FWD
+                         ? make_tmap_u8_2d(&pm, a.q, a.P, a.C, LT_BK, 128, CU_TENSOR_MAP_SWIZZLE_64B)
+                         : make_tmap_u8_2d(&pm, a.q, a.C, a.P, 128, LT_BK,
+                                           CU_TENSOR_MAP_SWIZZLE_NONE);
+    const bool okt = MODE == LORA_WGRAD
+                         ? make_tmap_u8_2d(&tm, a.t, a.C, a.T * 2, 128, LT_BK,
+                                           CU_TENSOR_MAP_SWIZZLE_128B)
+                         : make_tmap_u8_2d(&tm, a.t, a.T, (int64_t)a.C * 2, 128, BN / 2,
+                                           CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!okp || !okt) return cudaErrorInvalidValue;
+    cudaError_t e = ensure_dyn_smem<k_lora_tc<MODE>>(LT_SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t num_p = (a.P + 255) / 256, num_t = (a.T + BN - 1) / BN;
+    if (num_p * num_t > 0x3fffffff) return cudaErrorInvalidValue;
+    const int64_t pairs = num_p * num_t < num_sms / 2 ? num_p * num_t : num_sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(LT_THREADS);
+    cfg.dynamicSmemBytes = LT_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_lora_tc<MODE>, pm, tm, a, BN, (int)num_p, (int)num_t,
+                              status);
+}
+
+cudaError_t launch_lora_tc(int mode, const LoraGemm& a, cudaStream_t st, int num_sms,
+                           int* status) {
+    if (mode == LORA_FWD) return launch_tc<LORA_FWD>(a, st, num_sms, status);
+    if (mode == LORA_DGRAD) return launch_tc<LORA_DGRAD>(a, st, num_sms, status);
+    return launch_tc<LORA_WGRAD>(a, st, num_sms, status);
+}
+
+}  // namespace q8

@@ -222,8 +222,13 @@ static q8_status check_adapter_pointers(const q8_adapters* ad, const int32_t* id
     return Q8_OK;
 }
 
-// Workspace of the backward pass: g fp32 [M, R].
-static size_t lora_bwd_bytes(int64_t M, int64_t R) { return align_up((size_t)M * R * 4, 256); }
+// Workspaces: the tiles' adapter lists; backward, g fp32 [M, R] before them.
+static size_t lora_fwd_bytes(int64_t M) { return M > 0 ? align_up(lora_list_bytes(M), 256) : 0; }
+static size_t lora_bwd_g_bytes(int64_t M, int64_t R) { return align_up((size_t)M * R * 4, 256); }
+static size_t lora_bwd_bytes(int64_t M, int64_t R) {
+    return lora_bwd_g_bytes(M, R) + lora_fwd_bytes(M);
+}
+static inline int log2_of(int g) { return g == 32 ? 5 : g == 64 ? 6 : g == 128 ? 7 : 8; }
 
 // Self-test of the bounded-wait path: one CTA waits on an mbarrier that nothing will ever
 // complete, with a short limit; the wait gives up, records kStatusWaitTimeout in the status
@@ -403,7 +408,9 @@ size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K, int extra) 
         case Q8_OP_GPTQ_INT8:
             if (K > kGptqMaxK || !gptq_block_ok(extra)) return 0;
             return plan_gptq(N, K).bytes;
-        case Q8_OP_LINEAR_W8A16_LORA: return 0;
+        case Q8_OP_LINEAR_W8A16_LORA:
+            if (M > 0x7fffffff || !valid_rank(extra)) return 0;
+            return lora_fwd_bytes(M);
         case Q8_OP_LINEAR_W8A16_LORA_BACKWARD:
             if (M > 0x7fffffff || !valid_rank(extra)) return 0;
             return lora_bwd_bytes(M, extra);
@@ -431,11 +438,16 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     if (!aligned16(x) || !aligned16(q) || !aligned16(y) || !aligned16(h) || !aligned4(s_w) ||
         !aligned4(bias))
         return Q8_ERR_ALIGN;
+    const size_t need = lora_fwd_bytes(M);
+    if (!workspace || ws_bytes < need) return Q8_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     int sms = 0;
     int* status = nullptr;
     Q8_TRY(current_device(sms, &status));
     cudaStream_t st = (cudaStream_t)stream;
     const int R = (int)ad->rank, L = (int)ad->count;
+    int* lists = (int*)workspace;
+    Q8_TRY(launched(launch_lora_lists(ids, M, L, lists, st)));
     Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
                                        ad->scale, ids, h, M, (int)K, R, L, st)));
     LoraGemm a = {};
@@ -452,9 +464,10 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     a.low = (const uint16_t*)ad->b;
     a.h = h;
     a.scale = ad->scale;
+    a.lists = lists;
     a.R = R;
     a.L = L;
-    return launched(launch_lora_gemm(LORA_FWD, a, st));
+    return launched(launch_lora_tc(LORA_FWD, a, st, sms, status));
 }
 
 q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const float* s_w,
@@ -496,6 +509,8 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
     if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     Q8_TRY(current_device(sms, &status));
     float* g = (float*)workspace;
+    int* lists = (int*)((uint8_t*)workspace + lora_bwd_g_bytes(M, R));
+    if (dx) Q8_TRY(launched(launch_lora_lists(ids, M, L, lists, st)));
     if (dx || da)
         Q8_TRY(launched(launch_lora_shrink(true, (const uint16_t*)dy, (const uint16_t*)ad->b,
                                            ad->scale, ids, g, M, (int)N, R, L, st)));
@@ -513,9 +528,10 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
         a.low = (const uint16_t*)ad->a;
         a.h = g;
         a.scale = ad->scale;
+        a.lists = lists;
         a.R = R;
         a.L = L;
-        Q8_TRY(launched(launch_lora_gemm(LORA_DGRAD, a, st)));
+        Q8_TRY(launched(launch_lora_tc(LORA_DGRAD, a, st, sms, status)));
     }
     if (da)
         Q8_TRY(launched(launch_lora_wgrad(false, input->x, input->exps, input->group, g,
@@ -575,13 +591,13 @@ q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t
     a.q = codes;
     a.t = (const uint16_t*)dy;
     a.exps = exps;
-    a.G = group;
+    a.gshift = log2_of(group);
     a.out = dw;
     a.accumulate = accumulate != 0;
     a.P = (int)K;
     a.C = (int)M;
     a.T = N;
-    return launched(launch_lora_gemm(LORA_WGRAD, a, st));
+    return launched(launch_lora_tc(LORA_WGRAD, a, st, sms, status));
 }
 
 q8_status q8_quantize_weight_nvfp4(const float* W, int64_t N, int64_t K, uint8_t* q4, uint8_t* sf,

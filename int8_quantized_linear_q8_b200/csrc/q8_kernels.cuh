@@ -138,8 +138,8 @@ struct LoraGemm {
     const uint16_t* t;          // bf16 operand
     const float* s_w;
     const float* bias;          // nullable
-    const uint8_t* exps;        // LORA_WGRAD
-    int G;
+    const uint8_t* exps;        // LORA_WGRAD: exponent bytes of groups of 1 << gshift
+    int gshift;
     void* out;
     int out_bf16, accumulate;
     int P, C;
@@ -149,15 +149,21 @@ struct LoraGemm {
     const uint16_t* low;
     const float* h;             // [T, R]; LORA_DGRAD: g, scale included
     const float* scale;
+    const int* lists;           // launch_lora_lists
     int R, L;
 };
-cudaError_t launch_lora_gemm(int mode, const LoraGemm& a, cudaStream_t st);
 cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, const float* scale,
                                const int32_t* ids, float* h, int64_t M, int C, int R, int L,
                                cudaStream_t st);
 cudaError_t launch_lora_wgrad(bool db, const void* x, const uint8_t* exps, int G, const float* low,
                               const float* scale, const int32_t* ids, float* out, int accumulate,
                               int64_t M, int P, int R, int L, cudaStream_t st);
+
+// k_lora_tc.cu
+size_t lora_list_bytes(int64_t T);
+cudaError_t launch_lora_lists(const int32_t* ids, int64_t T, int L, int* lists, cudaStream_t st);
+cudaError_t launch_lora_tc(int mode, const LoraGemm& a, cudaStream_t st, int num_sms,
+                           int* status);
 
 // k_gptq.cu
 struct GptqPlan {
