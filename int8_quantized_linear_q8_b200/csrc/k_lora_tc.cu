@@ -24,22 +24,37 @@
 // parts (high and the rest: off by at most 2^-17), so an adapter takes 2 * rank columns.  Forward
 // it goes to the other accumulator buffer, since s_w applies to the base sum alone.
 //
-// Roles (18 warps): 0 TMA producer; 1 tensor-memory allocator and, in the pair's first CTA,
-// MMA issuer; 2-9 converters, two groups of four that take every other stage; 10-17
-// epilogue.  A stage is 64 of c: the int8 box (8 KB), the bf16 P tile that the converters write
-// (16 KB) and the T tile (16 KB, TMA).  Every wait is bounded.
+// Roles (19 warps): 0 and 2 TMA producers of the int8 and the bf16 operand; 1 tensor-memory
+// allocator and, in the pair's first CTA, MMA issuer; 3-10 converters, two groups of four
+// that take every other stage; 11-18 epilogue.  A stage is 64 of c.  Its int8 box (8 KB), its
+// converted P tile (16 KB) and its T tile (16 KB) live in rings of their own depth: the int8
+// path is the longest (copy, conversion, MMA) and its boxes the smallest, so it gets the
+// deepest ring and runs ahead; a converted tile only waits for the tensor core.  With one
+// ring of five whole stages the copies could not run ahead far enough (wgrad 4096 x 11008 x
+// 4096: 571 us).  Every wait is bounded.
 #include "q8_kernels.cuh"
 
 namespace q8 {
 
 constexpr int LT_BK = 64;
-constexpr int LT_STAGES = 5;
 constexpr int LT_A = 128 * 128, LT_B = 128 * 128, LT_RAW = 128 * 64;
-constexpr int LT_STAGE = LT_A + LT_B + LT_RAW;
-constexpr int LT_CONV = 8, LT_EPI = 8;
-constexpr int LT_THREADS = 32 * (2 + LT_CONV + LT_EPI);
-constexpr int LT_SMEM = LT_STAGES * LT_STAGE + 1024 + 512;
-static_assert(LT_STAGE % 1024 == 0 && LT_SMEM <= 227 * 1024, "shared memory");
+constexpr int LT_NA = 3, LT_NB = 7, LT_NR = 8;          // ring depths
+constexpr int LT_AT = 0, LT_BT = LT_AT + LT_NA * LT_A, LT_RT = LT_BT + LT_NB * LT_B;
+constexpr int LT_CTRL = LT_RT + LT_NR * LT_RAW;
+constexpr int LT_CONV = 8, LT_EPI = 8, LT_CONV0 = 3, LT_EPI0 = LT_CONV0 + LT_CONV;
+constexpr int LT_THREADS = 32 * (LT_EPI0 + LT_EPI);
+constexpr int LT_SMEM = LT_CTRL + 1024 + 512;
+static_assert(LT_SMEM <= 227 * 1024, "shared memory");
+
+// position in a ring: slot and the parity of its current phase
+template <int N>
+struct LtRing {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == N) { s = 0; ph ^= 1u; }
+    }
+};
 
 // ------------------------------------------------------------------ cluster and tcgen05
 __device__ __forceinline__ uint32_t lt_rank() {
@@ -56,34 +71,12 @@ __device__ __forceinline__ void lt_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// arrive on a barrier of either CTA of the pair (a shared::cluster address)
+// arrive on a barrier of either CTA of the pair (a shared::cluster address).  What it announces
+// is read by the tensor core (after fence.proxy.async) or was read from tensor memory (after
+// tcgen05.wait), so no cluster-scope fence is asked for.
 __device__ __forceinline__ void lt_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
-}
-// mbar_wait for barriers on which the other CTA's threads arrive
-__device__ __forceinline__ bool lt_wait(uint64_t* bar, uint32_t parity, int* status,
-                                        volatile int* abort_flag) {
-    const unsigned long long t0 = globaltimer_ns();
-    for (uint32_t i = 1;; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSleepNs)
-            : "memory");
-        if (ok) return true;
-        if ((i & 7u) == 0) {
-            if (*abort_flag) return false;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) {
-                *abort_flag = 1;
-                atomicExch(status, kStatusWaitTimeout);
-                return false;
-            }
-        }
-    }
 }
 // TMA load into this CTA's shared memory, completion on a barrier of the pair's first CTA
 __device__ __forceinline__ void lt_tma_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1,
@@ -172,24 +165,29 @@ __device__ __forceinline__ uint32_t bf16_bits_rn(float v) {
 }
 
 // What a converter thread multiplies its codes by: nothing (forward), s_w as the bf16 pair
-// hi + lo (hi * q + lo * q is rounded once, to bf16), or a power of two.
+// hi + lo (hi * q + lo * q is rounded once, to bf16), or a power of two.  Loaded a turn ahead as
+// raw bits, so that nothing waits on the load before its turn.
+template <int MODE>
+__device__ __forceinline__ uint32_t lt_scale_bits(const LoraGemm& a, int c, int p) {
+    if (MODE == LORA_DGRAD && c < a.C) return __float_as_uint(__ldg(a.s_w + c));
+    if (MODE == LORA_WGRAD && c < a.C && p < a.P)
+        return __ldg(a.exps + (int64_t)c * (a.P >> a.gshift) + (p >> a.gshift));
+    return 0u;
+}
 struct LtScale {
     uint32_t hi, lo;
 };
 template <int MODE>
-__device__ __forceinline__ LtScale lt_scale(const LoraGemm& a, int c, int p) {
+__device__ __forceinline__ LtScale lt_scale(uint32_t bits) {
     LtScale s = {0u, 0u};
-    if (MODE == LORA_DGRAD && c < a.C) {
-        const float v = __ldg(a.s_w + c);
+    if (MODE == LORA_DGRAD) {
+        const float v = __uint_as_float(bits);
         const uint32_t h = bf16_bits_rn(v);
         const uint32_t l = bf16_bits_rn(v - __uint_as_float(h << 16));
         s.hi = h | h << 16;
         s.lo = l | l << 16;
     }
-    if (MODE == LORA_WGRAD && c < a.C && p < a.P) {
-        const uint32_t b = __ldg(a.exps + (int64_t)c * (a.P >> a.gshift) + (p >> a.gshift));
-        s.hi = b << 7 | b << 23;
-    }
+    if (MODE == LORA_WGRAD) s.hi = bits << 7 | bits << 23;
     return s;
 }
 template <int MODE>
@@ -211,11 +209,13 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
     constexpr bool B_MN = MODE == LORA_WGRAD;           // bf16 operand with t contiguous
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint64_t* rawfull = reinterpret_cast<uint64_t*>(smem + LT_STAGES * LT_STAGE);
-    uint64_t* bfull = rawfull + LT_STAGES;              // first CTA: both halves of T landed
-    uint64_t* aready = bfull + LT_STAGES;               // first CTA: both CTAs converted
-    uint64_t* empty = aready + LT_STAGES;
-    uint64_t* tfull = empty + LT_STAGES;
+    uint64_t* rfull = reinterpret_cast<uint64_t*>(smem + LT_CTRL);
+    uint64_t* rempty = rfull + LT_NR;
+    uint64_t* bfull = rempty + LT_NR;                   // first CTA: both halves of T landed
+    uint64_t* bempty = bfull + LT_NB;
+    uint64_t* aready = bempty + LT_NB;                  // first CTA: both CTAs converted
+    uint64_t* aempty = aready + LT_NA;
+    uint64_t* tfull = aempty + LT_NA;
     uint64_t* tempty = tfull + 2;                       // first CTA
     uint64_t* mma_done = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -242,11 +242,17 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
     };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < LT_STAGES; ++s) {
-            mbar_init(&rawfull[s], 1);
-            mbar_init(&bfull[s], 1);
-            mbar_init(&aready[s], 8);
-            mbar_init(&empty[s], 1);
+        for (int i = 0; i < LT_NR; ++i) {
+            mbar_init(&rfull[i], 1);
+            mbar_init(&rempty[i], LT_CONV / 2);
+        }
+        for (int i = 0; i < LT_NB; ++i) {
+            mbar_init(&bfull[i], 1);
+            mbar_init(&bempty[i], 1);
+        }
+        for (int i = 0; i < LT_NA; ++i) {
+            mbar_init(&aready[i], LT_CONV);             // a group of either CTA
+            mbar_init(&aempty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
@@ -272,61 +278,79 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == 0) {
-        // ---------------------------------------------------------------- producer
-        if (lane == 0) {
-            tma_prefetch_desc(&pmap);
-            tma_prefetch_desc(&tmap);
+        // ---------------------------------------------------------------- int8 producer
+        if (lane == 0) tma_prefetch_desc(&pmap);
+        LtRing<LT_NR> r;
+        int it = 0;
+        bool ok = true;
+        for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
+            int p0, t0;
+            tile_of(u, p0, t0);
+            for (int kb = 0; kb < nk; ++kb) {
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(&rempty[r.s], r.ph ^ 1u, status, abort_flag));
+                if (!ok) break;
+                if (lane == 0) {
+                    const int c0 = kb * LT_BK;
+                    uint8_t* dst = smem + LT_RT + r.s * LT_RAW;
+                    mbar_expect_tx(&rfull[r.s], LT_RAW);
+                    if (A_MN)
+                        tma_load_2d(dst, &pmap, p0, c0, &rfull[r.s]);
+                    else
+                        tma_load_2d(dst, &pmap, c0, p0, &rfull[r.s]);
+                }
+                ++it;
+                r.next();
+            }
         }
+        // copies issued here have landed before the CTA leaves
+        for (int i = max(0, it - LT_NR); i < it; ++i)
+            mbar_drain(&rfull[i % LT_NR], (uint32_t)(i / LT_NR) & 1u, status);
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- bf16 producer
+        if (lane == 0) tma_prefetch_desc(&tmap);
         const uint32_t bfull0 = lt_map(smem_u32(bfull), 0);
-        int s = 0, it = 0;
-        uint32_t ph = 0;
+        LtRing<LT_NB> r;
+        int it = 0;
         bool ok = true;
         for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
             int p0, t0;
             tile_of(u, p0, t0);
             const int total = nk + low_stages(t0);
+            const int tr = t0 + (int)rank * half;
             for (int kb = 0; kb < total; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, status, abort_flag));
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(&bempty[r.s], r.ph ^ 1u, status, abort_flag));
                 if (!ok) break;
                 if (lane == 0) {
-                    uint8_t* st = smem + (size_t)s * LT_STAGE;
                     if (kb < nk) {
                         const int c0 = kb * LT_BK;
-                        mbar_expect_tx(&rawfull[s], LT_RAW);
-                        if (A_MN)
-                            tma_load_2d(st + LT_A + LT_B, &pmap, p0, c0, &rawfull[s]);
-                        else
-                            tma_load_2d(st + LT_A + LT_B, &pmap, c0, p0, &rawfull[s]);
-                        if (rank == 0) mbar_expect_tx(&bfull[s], (uint32_t)BN * 128u);
-                        const uint32_t bt = smem_u32(st + LT_A);
-                        const int tr = t0 + (int)rank * half;
+                        const uint32_t bt = smem_u32(smem + LT_BT + r.s * LT_B);
+                        if (rank == 0) mbar_expect_tx(&bfull[r.s], (uint32_t)BN * 128u);
                         if (B_MN)
                             for (int b = 0; b < half / 64; ++b)
                                 lt_tma_pair(bt + b * 8192, &tmap, (tr + b * 64) * 2, c0,
-                                            bfull0 + s * 8);
+                                            bfull0 + r.s * 8);
                         else
-                            lt_tma_pair(bt, &tmap, c0 * 2, tr, bfull0 + s * 8);
-                    } else {                            // written by the converters alone
-                        mbar_arrive(&rawfull[s]);
-                        if (rank == 0) mbar_arrive(&bfull[s]);
+                            lt_tma_pair(bt, &tmap, c0 * 2, tr, bfull0 + r.s * 8);
+                    } else if (rank == 0) {             // written by the converters
+                        mbar_arrive(&bfull[r.s]);
                     }
                 }
                 ++it;
-                if (++s == LT_STAGES) { s = 0; ph ^= 1u; }
+                r.next();
             }
         }
-        // copies issued here have landed before the CTA leaves
-        for (int i = max(0, it - LT_STAGES); i < it; ++i) {
-            mbar_drain(&rawfull[i % LT_STAGES], (uint32_t)(i / LT_STAGES) & 1u, status);
-            if (rank == 0)
-                mbar_drain(&bfull[i % LT_STAGES], (uint32_t)(i / LT_STAGES) & 1u, status);
-        }
+        if (rank == 0)
+            for (int i = max(0, it - LT_NB); i < it; ++i)
+                mbar_drain(&bfull[i % LT_NB], (uint32_t)(i / LT_NB) & 1u, status);
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         if (rank == 0) {
             const uint32_t idesc = lt_idesc(BN, A_MN, B_MN);
-            int s = 0, buf = 0;
-            uint32_t ph = 0, bph = 0;
+            LtRing<LT_NA> ra;
+            LtRing<LT_NB> rb;
+            LtRing<2> rt;
             bool ok = true;
             for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
                 int p0, t0;
@@ -336,99 +360,87 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                     const bool fresh = kb == 0 || (MODE == LORA_FWD && kb == nk);
                     if (fresh) {
                         if (kb) {                       // base sum complete
-                            lt_commit(&tfull[buf]);
-                            if (++buf == 2) { buf = 0; bph ^= 1u; }
+                            lt_commit(&tfull[rt.s]);
+                            rt.next();
                         }
                         ok = __all_sync(0xffffffffu,
-                                        lt_wait(&tempty[buf], bph ^ 1u, status, abort_flag));
+                                        mbar_wait(&tempty[rt.s], rt.ph ^ 1u, status, abort_flag));
                         if (!ok) break;
                     }
-                    ok = __all_sync(0xffffffffu, lt_wait(&aready[s], ph, status, abort_flag) &&
-                                                     lt_wait(&bfull[s], ph, status, abort_flag));
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&bfull[rb.s], rb.ph, status, abort_flag) &&
+                                        mbar_wait(&aready[ra.s], ra.ph, status, abort_flag));
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t st = smem_u32(smem + (size_t)s * LT_STAGE);
-                    const uint64_t ad = lt_desc(st, A_MN), bd = lt_desc(st + LT_A, B_MN);
-                    const uint32_t d = tmem + (uint32_t)(buf * 256);
+                    const uint64_t ad = lt_desc(smem_u32(smem + LT_AT + ra.s * LT_A), A_MN);
+                    const uint64_t bd = lt_desc(smem_u32(smem + LT_BT + rb.s * LT_B), B_MN);
+                    const uint32_t d = tmem + (uint32_t)(rt.s * 256);
 #pragma unroll
                     for (int k = 0; k < LT_BK / 16; ++k)
                         lt_mma(d, ad + (A_MN ? 128 : 2) * k, bd + (B_MN ? 128 : 2) * k, idesc,
                                !(fresh && k == 0));
-                    lt_commit(&empty[s]);
-                    if (++s == LT_STAGES) { s = 0; ph ^= 1u; }
+                    lt_commit(&aempty[ra.s]);
+                    lt_commit(&bempty[rb.s]);
+                    ra.next();
+                    rb.next();
                 }
                 if (!ok) break;
-                lt_commit(&tfull[buf]);
-                if (++buf == 2) { buf = 0; bph ^= 1u; }
+                lt_commit(&tfull[rt.s]);
+                rt.next();
             }
             lt_commit(mma_done);                        // before tensor memory is released
             mbar_drain(mma_done, 0, status);
         }
         __syncwarp();
-    } else if (warp < 2 + LT_CONV) {
+    } else if (warp < LT_EPI0) {
         // ---------------------------------------------------------------- converters
-        const int grp = (warp - 2) >> 2;
-        const int tid = threadIdx.x - 64 - grp * 128;
+        const int grp = (warp - LT_CONV0) >> 2;
+        const int tid = threadIdx.x - 32 * LT_CONV0 - grp * 128;
         const uint32_t aready0 = lt_map(smem_u32(aready), 0);
-        int s = 0, it = 0;
-        uint32_t ph = 0;
+        LtRing<LT_NR> rr;
+        LtRing<LT_NA> ra;
+        LtRing<LT_NB> rb;
+        int it = 0;
         bool live = true;
         for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
             int p0, t0;
             tile_of(u, p0, t0);
             const int total = nk + low_stages(t0);
-            // the next stage's scales, loaded a turn ahead
-            LtScale nxt[4];
+            const int sc = tid >> 3, sp = p0 + (tid & 7) * 16;     // this thread's first c, its p
+            uint32_t nxt[4];                            // the next turn's scales
             if (A_MN) {
                 const int kb = (it & 1) == grp ? 0 : 1;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    nxt[i] = lt_scale<MODE>(a, kb * LT_BK + i * 16 + (tid >> 3),
-                                            p0 + (tid & 7) * 16);
+                    nxt[i] = lt_scale_bits<MODE>(a, kb * LT_BK + i * 16 + sc, sp);
             }
             for (int kb = 0; kb < total; ++kb) {
                 if ((it & 1) == grp) {
-                    const bool okw = mbar_wait(&rawfull[s], ph, status, abort_flag);
-                    live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
-                    const uint32_t at = smem_u32(smem + (size_t)s * LT_STAGE);
-                    if (live && kb < nk) {
-                        const uint32_t raw = at + LT_A + LT_B;
-                        if (!A_MN) {
-                            // thread: row tid, 64 codes (16-byte pieces swizzled over 64)
-                            uint4 w[4];
+                    const uint32_t at = smem_u32(smem + LT_AT + ra.s * LT_A);
+                    if (kb < nk) {
+                        const uint32_t raw = smem_u32(smem + LT_RT + rr.s * LT_RAW);
+                        bool okw = mbar_wait(&rfull[rr.s], rr.ph, status, abort_flag);
+                        live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
+                        uint4 w[4];
 #pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                w[c] = lds128(raw + tid * 64 + ((c ^ ((tid >> 1) & 3)) << 4));
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = A_MN ? lds128(raw + (i * 16 + sc) * 128 + (tid & 7) * 16)
+                                        : lds128(raw + tid * 64 + ((i ^ ((tid >> 1) & 3)) << 4));
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&rempty[rr.s]);      // codes in registers
+                        uint32_t cur[4];
+                        if (A_MN) {
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t o[8];
-                                s8x4_to_bf16x2_seq(w[c].x, o[0], o[1]);
-                                s8x4_to_bf16x2_seq(w[c].y, o[2], o[3]);
-                                s8x4_to_bf16x2_seq(w[c].z, o[4], o[5]);
-                                s8x4_to_bf16x2_seq(w[c].w, o[6], o[7]);
-                                const uint32_t row = at + tid * 128;
-                                sts128(row + (((2 * c) ^ (tid & 7)) << 4), o[0], o[1], o[2], o[3]);
-                                sts128(row + (((2 * c + 1) ^ (tid & 7)) << 4), o[4], o[5], o[6],
-                                       o[7]);
-                            }
-                        } else {
-                            // thread: 16 codes of p in each of 4 rows of c; the two 16-byte
-                            // pieces are written in an order that keeps the 64-p blocks of a
-                            // row on different banks
-                            LtScale cur[4];
-                            uint4 w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                cur[i] = nxt[i];
-                                w[i] = lds128(raw + (i * 16 + (tid >> 3)) * 128 + (tid & 7) * 16);
-                            }
+                            for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
                             if (kb + 2 < nk)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
-                                    nxt[i] = lt_scale<MODE>(
-                                        a, (kb + 2) * LT_BK + i * 16 + (tid >> 3),
-                                        p0 + (tid & 7) * 16);
-                            const int ch = tid & 7, odd = ch >> 2;
+                                    nxt[i] =
+                                        lt_scale_bits<MODE>(a, (kb + 2) * LT_BK + i * 16 + sc, sp);
+                        }
+                        okw = mbar_wait(&aempty[ra.s], ra.ph ^ 1u, status, abort_flag);
+                        live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
+                        if (live) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 uint32_t o[8];
@@ -436,24 +448,43 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                                 s8x4_to_bf16x2_seq(w[i].y, o[2], o[3]);
                                 s8x4_to_bf16x2_seq(w[i].z, o[4], o[5]);
                                 s8x4_to_bf16x2_seq(w[i].w, o[6], o[7]);
+                                if (!A_MN) {
+                                    // thread: row tid, 64 codes
+                                    const uint32_t row = at + tid * 128;
+                                    sts128(row + (((2 * i) ^ (tid & 7)) << 4), o[0], o[1], o[2],
+                                           o[3]);
+                                    sts128(row + (((2 * i + 1) ^ (tid & 7)) << 4), o[4], o[5],
+                                           o[6], o[7]);
+                                } else {
+                                    // thread: 16 codes of p in each of 4 rows of c; the two
+                                    // 16-byte pieces are written in an order that keeps the
+                                    // 64-p blocks of a row on different banks
+                                    const LtScale f = lt_scale<MODE>(cur[i]);
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) o[j] = lt_apply<MODE>(o[j], cur[i]);
-                                const int c = i * 16 + (tid >> 3);
-                                const uint32_t row = at + odd * 8192 + c * 128;
-                                const int j0 = (ch & 3) * 2;
-                                const uint32_t e0 = odd ? o[4] : o[0], e1 = odd ? o[5] : o[1];
-                                const uint32_t e2 = odd ? o[6] : o[2], e3 = odd ? o[7] : o[3];
-                                const uint32_t f0 = odd ? o[0] : o[4], f1 = odd ? o[1] : o[5];
-                                const uint32_t f2 = odd ? o[2] : o[6], f3 = odd ? o[3] : o[7];
-                                sts128(row + (((j0 + odd) ^ (c & 7)) << 4), e0, e1, e2, e3);
-                                sts128(row + (((j0 + 1 - odd) ^ (c & 7)) << 4), f0, f1, f2, f3);
+                                    for (int j = 0; j < 8; ++j) o[j] = lt_apply<MODE>(o[j], f);
+                                    const int ch = tid & 7, odd = ch >> 2, c = i * 16 + sc;
+                                    const uint32_t row = at + odd * 8192 + c * 128;
+                                    const int j0 = (ch & 3) * 2;
+                                    sts128(row + (((j0 + odd) ^ (c & 7)) << 4),
+                                           odd ? o[4] : o[0], odd ? o[5] : o[1],
+                                           odd ? o[6] : o[2], odd ? o[7] : o[3]);
+                                    sts128(row + (((j0 + 1 - odd) ^ (c & 7)) << 4),
+                                           odd ? o[0] : o[4], odd ? o[1] : o[5],
+                                           odd ? o[2] : o[6], odd ? o[3] : o[7]);
+                                }
                             }
                         }
+                    } else {
+                        // the T tile is written here too
+                        bool okw = mbar_wait(&aempty[ra.s], ra.ph ^ 1u, status, abort_flag) &&
+                                   mbar_wait(&bempty[rb.s], rb.ph ^ 1u, status, abort_flag);
+                        live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
                     }
                     if (MODE != LORA_WGRAD && live && kb >= nk) {
                         // Columns (kb - nk) * 64 .. +64 of the adapter term, in pieces of 8:
                         // per adapter of the list R / 8 pieces against the high parts and
                         // R / 8 against the rest.
+                        const uint32_t bt = smem_u32(smem + LT_BT + rb.s * LT_B);
                         const int rc = a.R >> 3;
                         const int* list = a.lists + (int64_t)(t0 / BN) * LT_LIST;
                         const int cnt = __ldg(list);
@@ -502,24 +533,26 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                                         o[j >> 1] |= b << (16 * (j & 1));
                                     }
                                 }
-                                sts128(at + LT_A + tid * 128 + ((c ^ (tid & 7)) << 4), o[0], o[1],
-                                       o[2], o[3]);
+                                sts128(bt + tid * 128 + ((c ^ (tid & 7)) << 4), o[0], o[1], o[2],
+                                       o[3]);
                             }
                         }
                     }
                     // make the generic-proxy writes visible to the tensor core, then hand over
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) lt_arrive(aready0 + s * 8);
+                    if (lane == 0) lt_arrive(aready0 + ra.s * 8);
                 }
                 ++it;
-                if (++s == LT_STAGES) { s = 0; ph ^= 1u; }
+                if (kb < nk) rr.next();
+                ra.next();
+                rb.next();
             }
         }
     } else {
         // ---------------------------------------------------------------- epilogue
         // warp w: lane quarter w % 4 of the CTA's 128 p, every other chunk of 32 t
-        const int q = warp & 3, par = (warp - 2 - LT_CONV) >> 2;
+        const int q = warp & 3, par = (warp - LT_EPI0) >> 2;
         const uint32_t tempty0 = lt_map(smem_u32(tempty), 0);
         int buf = 0;
         uint32_t bph = 0;
