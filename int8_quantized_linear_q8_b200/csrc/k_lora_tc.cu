@@ -26,20 +26,20 @@
 //
 // Roles (19 warps): 0 and 2 TMA producers of the int8 and the bf16 operand; 1 tensor-memory
 // allocator and, in the pair's first CTA, MMA issuer; 3-10 converters, two groups of four
-// that take every other stage; 11-18 epilogue.  A stage is 64 of c.  Its int8 box (8 KB), its
-// converted P tile (16 KB) and its T tile (16 KB) live in rings of their own depth: the int8
-// path is the longest (copy, conversion, MMA) and its boxes the smallest, so it gets the
-// deepest ring and runs ahead; a converted tile only waits for the tensor core.  With one
-// ring of five whole stages the copies could not run ahead far enough (wgrad 4096 x 11008 x
-// 4096: 571 us).  Every wait is bounded.
+// that take every other stage; 11-18 epilogue.  A stage is 64 of c.  Its int8 box (8 KB) has
+// a ring of its own, eight deep: that path is the longest (copy, conversion, MMA) and runs
+// ahead.  Its converted P tile and its T tile (16 KB each) share a slot of a ring of five, so
+// that the issuing warp, whose own steps bound the main loop, has one barrier to wait for
+// and one commit to make per stage; it tests the next stage's barrier before it issues this
+// stage's MMAs, which hides the test.  Every wait is bounded.
 #include "q8_kernels.cuh"
 
 namespace q8 {
 
 constexpr int LT_BK = 64;
 constexpr int LT_A = 128 * 128, LT_B = 128 * 128, LT_RAW = 128 * 64;
-constexpr int LT_NA = 3, LT_NB = 7, LT_NR = 8;          // ring depths
-constexpr int LT_AT = 0, LT_BT = LT_AT + LT_NA * LT_A, LT_RT = LT_BT + LT_NB * LT_B;
+constexpr int LT_N = 5, LT_NR = 8;                      // ring depths
+constexpr int LT_SLOT = LT_A + LT_B, LT_RT = LT_N * LT_SLOT;
 constexpr int LT_CTRL = LT_RT + LT_NR * LT_RAW;
 constexpr int LT_CONV = 8, LT_EPI = 8, LT_CONV0 = 3, LT_EPI0 = LT_CONV0 + LT_CONV;
 constexpr int LT_THREADS = 32 * (LT_EPI0 + LT_EPI);
@@ -98,23 +98,31 @@ __device__ __forceinline__ uint32_t lt_idesc(int bn, bool a_mn, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
            ((uint32_t)(bn >> 3) << 17) | (16u << 24);
 }
+// one lane of a converged warp
+__device__ __forceinline__ bool lt_elect() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
+// the next two are called by the elected lane
 __device__ __forceinline__ void lt_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // arrives on the barrier at the same offset in both CTAs once the MMAs issued so far are done
 __device__ __forceinline__ void lt_commit(uint64_t* bar) {
     asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
-        ".b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+        ".b64 [%0], %1;" ::"r"(smem_u32(bar)),
         "h"((uint16_t)3)
         : "memory");
 }
@@ -211,11 +219,9 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
     uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t* rfull = reinterpret_cast<uint64_t*>(smem + LT_CTRL);
     uint64_t* rempty = rfull + LT_NR;
-    uint64_t* bfull = rempty + LT_NR;                   // first CTA: both halves of T landed
-    uint64_t* bempty = bfull + LT_NB;
-    uint64_t* aready = bempty + LT_NB;                  // first CTA: both CTAs converted
-    uint64_t* aempty = aready + LT_NA;
-    uint64_t* tfull = aempty + LT_NA;
+    uint64_t* full = rempty + LT_NR;        // first CTA: both CTAs' P and T tiles are there
+    uint64_t* empty = full + LT_N;
+    uint64_t* tfull = empty + LT_N;
     uint64_t* tempty = tfull + 2;                       // first CTA
     uint64_t* mma_done = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -246,13 +252,9 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
             mbar_init(&rfull[i], 1);
             mbar_init(&rempty[i], LT_CONV / 2);
         }
-        for (int i = 0; i < LT_NB; ++i) {
-            mbar_init(&bfull[i], 1);
-            mbar_init(&bempty[i], 1);
-        }
-        for (int i = 0; i < LT_NA; ++i) {
-            mbar_init(&aready[i], LT_CONV);             // a group of either CTA
-            mbar_init(&aempty[i], 1);
+        for (int i = 0; i < LT_N; ++i) {
+            mbar_init(&full[i], LT_CONV + 1);           // a group of either CTA, the T copies
+            mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
@@ -309,8 +311,8 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
     } else if (warp == 2) {
         // ---------------------------------------------------------------- bf16 producer
         if (lane == 0) tma_prefetch_desc(&tmap);
-        const uint32_t bfull0 = lt_map(smem_u32(bfull), 0);
-        LtRing<LT_NB> r;
+        const uint32_t full0 = lt_map(smem_u32(full), 0);
+        LtRing<LT_N> r;
         int it = 0;
         bool ok = true;
         for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
@@ -320,21 +322,21 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
             const int tr = t0 + (int)rank * half;
             for (int kb = 0; kb < total; ++kb) {
                 ok = __all_sync(0xffffffffu,
-                                mbar_wait(&bempty[r.s], r.ph ^ 1u, status, abort_flag));
+                                mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag));
                 if (!ok) break;
                 if (lane == 0) {
                     if (kb < nk) {
                         const int c0 = kb * LT_BK;
-                        const uint32_t bt = smem_u32(smem + LT_BT + r.s * LT_B);
-                        if (rank == 0) mbar_expect_tx(&bfull[r.s], (uint32_t)BN * 128u);
+                        const uint32_t bt = smem_u32(smem + r.s * LT_SLOT + LT_A);
+                        if (rank == 0) mbar_expect_tx(&full[r.s], (uint32_t)BN * 128u);
                         if (B_MN)
                             for (int b = 0; b < half / 64; ++b)
                                 lt_tma_pair(bt + b * 8192, &tmap, (tr + b * 64) * 2, c0,
-                                            bfull0 + r.s * 8);
+                                            full0 + r.s * 8);
                         else
-                            lt_tma_pair(bt, &tmap, c0 * 2, tr, bfull0 + r.s * 8);
+                            lt_tma_pair(bt, &tmap, c0 * 2, tr, full0 + r.s * 8);
                     } else if (rank == 0) {             // written by the converters
-                        mbar_arrive(&bfull[r.s]);
+                        mbar_arrive(&full[r.s]);
                     }
                 }
                 ++it;
@@ -342,16 +344,15 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
             }
         }
         if (rank == 0)
-            for (int i = max(0, it - LT_NB); i < it; ++i)
-                mbar_drain(&bfull[i % LT_NB], (uint32_t)(i / LT_NB) & 1u, status);
+            for (int i = max(0, it - LT_N); i < it; ++i)
+                mbar_drain(&full[i % LT_N], (uint32_t)(i / LT_N) & 1u, status);
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         if (rank == 0) {
             const uint32_t idesc = lt_idesc(BN, A_MN, B_MN);
-            LtRing<LT_NA> ra;
-            LtRing<LT_NB> rb;
+            LtRing<LT_N> r;
             LtRing<2> rt;
-            bool ok = true;
+            bool ok = true, here = false;
             for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
                 int p0, t0;
                 tile_of(u, p0, t0);
@@ -360,35 +361,42 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                     const bool fresh = kb == 0 || (MODE == LORA_FWD && kb == nk);
                     if (fresh) {
                         if (kb) {                       // base sum complete
-                            lt_commit(&tfull[rt.s]);
+                            if (lt_elect()) lt_commit(&tfull[rt.s]);
+                            __syncwarp();
                             rt.next();
                         }
                         ok = __all_sync(0xffffffffu,
                                         mbar_wait(&tempty[rt.s], rt.ph ^ 1u, status, abort_flag));
                         if (!ok) break;
                     }
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait(&bfull[rb.s], rb.ph, status, abort_flag) &&
-                                        mbar_wait(&aready[ra.s], ra.ph, status, abort_flag));
-                    if (!ok) break;
+                    if (!here) {
+                        ok = __all_sync(0xffffffffu,
+                                        mbar_wait(&full[r.s], r.ph, status, abort_flag));
+                        if (!ok) break;
+                    }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint64_t ad = lt_desc(smem_u32(smem + LT_AT + ra.s * LT_A), A_MN);
-                    const uint64_t bd = lt_desc(smem_u32(smem + LT_BT + rb.s * LT_B), B_MN);
-                    const uint32_t d = tmem + (uint32_t)(rt.s * 256);
+                    const int cur = r.s;
+                    r.next();
+                    here = mbar_test_wait(&full[r.s], r.ph);
+                    if (lt_elect()) {
+                        const uint32_t at = smem_u32(smem + cur * LT_SLOT);
+                        const uint64_t ad = lt_desc(at, A_MN), bd = lt_desc(at + LT_A, B_MN);
+                        const uint32_t d = tmem + (uint32_t)(rt.s * 256);
 #pragma unroll
-                    for (int k = 0; k < LT_BK / 16; ++k)
-                        lt_mma(d, ad + (A_MN ? 128 : 2) * k, bd + (B_MN ? 128 : 2) * k, idesc,
-                               !(fresh && k == 0));
-                    lt_commit(&aempty[ra.s]);
-                    lt_commit(&bempty[rb.s]);
-                    ra.next();
-                    rb.next();
+                        for (int k = 0; k < LT_BK / 16; ++k)
+                            lt_mma(d, ad + (A_MN ? 128 : 2) * k, bd + (B_MN ? 128 : 2) * k, idesc,
+                                   !(fresh && k == 0));
+                        lt_commit(&empty[cur]);
+                    }
+                    here = __all_sync(0xffffffffu, here);
                 }
                 if (!ok) break;
-                lt_commit(&tfull[rt.s]);
+                if (lt_elect()) lt_commit(&tfull[rt.s]);
+                __syncwarp();
                 rt.next();
             }
-            lt_commit(mma_done);                        // before tensor memory is released
+            if (lt_elect()) lt_commit(mma_done);        // before tensor memory is released
+            __syncwarp();
             mbar_drain(mma_done, 0, status);
         }
         __syncwarp();
@@ -396,10 +404,9 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
         // ---------------------------------------------------------------- converters
         const int grp = (warp - LT_CONV0) >> 2;
         const int tid = threadIdx.x - 32 * LT_CONV0 - grp * 128;
-        const uint32_t aready0 = lt_map(smem_u32(aready), 0);
+        const uint32_t full0 = lt_map(smem_u32(full), 0);
         LtRing<LT_NR> rr;
-        LtRing<LT_NA> ra;
-        LtRing<LT_NB> rb;
+        LtRing<LT_N> r;
         int it = 0;
         bool live = true;
         for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
@@ -416,7 +423,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
             }
             for (int kb = 0; kb < total; ++kb) {
                 if ((it & 1) == grp) {
-                    const uint32_t at = smem_u32(smem + LT_AT + ra.s * LT_A);
+                    const uint32_t at = smem_u32(smem + r.s * LT_SLOT);
                     if (kb < nk) {
                         const uint32_t raw = smem_u32(smem + LT_RT + rr.s * LT_RAW);
                         bool okw = mbar_wait(&rfull[rr.s], rr.ph, status, abort_flag);
@@ -438,53 +445,59 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                                     nxt[i] =
                                         lt_scale_bits<MODE>(a, (kb + 2) * LT_BK + i * 16 + sc, sp);
                         }
-                        okw = mbar_wait(&aempty[ra.s], ra.ph ^ 1u, status, abort_flag);
+                        // converted in registers first: what lies between a free tile and
+                        // its hand-over is on the ring's critical path
+                        uint32_t o[4][8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            s8x4_to_bf16x2_seq(w[i].x, o[i][0], o[i][1]);
+                            s8x4_to_bf16x2_seq(w[i].y, o[i][2], o[i][3]);
+                            s8x4_to_bf16x2_seq(w[i].z, o[i][4], o[i][5]);
+                            s8x4_to_bf16x2_seq(w[i].w, o[i][6], o[i][7]);
+                            if (A_MN) {
+                                const LtScale f = lt_scale<MODE>(cur[i]);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) o[i][j] = lt_apply<MODE>(o[i][j], f);
+                            }
+                        }
+                        okw = mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag);
                         live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
                         if (live) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                uint32_t o[8];
-                                s8x4_to_bf16x2_seq(w[i].x, o[0], o[1]);
-                                s8x4_to_bf16x2_seq(w[i].y, o[2], o[3]);
-                                s8x4_to_bf16x2_seq(w[i].z, o[4], o[5]);
-                                s8x4_to_bf16x2_seq(w[i].w, o[6], o[7]);
                                 if (!A_MN) {
                                     // thread: row tid, 64 codes
                                     const uint32_t row = at + tid * 128;
-                                    sts128(row + (((2 * i) ^ (tid & 7)) << 4), o[0], o[1], o[2],
-                                           o[3]);
-                                    sts128(row + (((2 * i + 1) ^ (tid & 7)) << 4), o[4], o[5],
-                                           o[6], o[7]);
+                                    sts128(row + (((2 * i) ^ (tid & 7)) << 4), o[i][0], o[i][1],
+                                           o[i][2], o[i][3]);
+                                    sts128(row + (((2 * i + 1) ^ (tid & 7)) << 4), o[i][4],
+                                           o[i][5], o[i][6], o[i][7]);
                                 } else {
-                                    // thread: 16 codes of p in each of 4 rows of c; the two
-                                    // 16-byte pieces are written in an order that keeps the
-                                    // 64-p blocks of a row on different banks
-                                    const LtScale f = lt_scale<MODE>(cur[i]);
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) o[j] = lt_apply<MODE>(o[j], f);
+                                    // thread: 16 codes of p in each of 4 rows of c, two 16-byte
+                                    // pieces; lanes of the second 64-p block write theirs in the
+                                    // other order, which keeps a row's lanes on different banks
                                     const int ch = tid & 7, odd = ch >> 2, c = i * 16 + sc;
                                     const uint32_t row = at + odd * 8192 + c * 128;
                                     const int j0 = (ch & 3) * 2;
                                     sts128(row + (((j0 + odd) ^ (c & 7)) << 4),
-                                           odd ? o[4] : o[0], odd ? o[5] : o[1],
-                                           odd ? o[6] : o[2], odd ? o[7] : o[3]);
+                                           odd ? o[i][4] : o[i][0], odd ? o[i][5] : o[i][1],
+                                           odd ? o[i][6] : o[i][2], odd ? o[i][7] : o[i][3]);
                                     sts128(row + (((j0 + 1 - odd) ^ (c & 7)) << 4),
-                                           odd ? o[0] : o[4], odd ? o[1] : o[5],
-                                           odd ? o[2] : o[6], odd ? o[3] : o[7]);
+                                           odd ? o[i][0] : o[i][4], odd ? o[i][1] : o[i][5],
+                                           odd ? o[i][2] : o[i][6], odd ? o[i][3] : o[i][7]);
                                 }
                             }
                         }
                     } else {
                         // the T tile is written here too
-                        bool okw = mbar_wait(&aempty[ra.s], ra.ph ^ 1u, status, abort_flag) &&
-                                   mbar_wait(&bempty[rb.s], rb.ph ^ 1u, status, abort_flag);
+                        const bool okw = mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag);
                         live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
                     }
                     if (MODE != LORA_WGRAD && live && kb >= nk) {
                         // Columns (kb - nk) * 64 .. +64 of the adapter term, in pieces of 8:
                         // per adapter of the list R / 8 pieces against the high parts and
                         // R / 8 against the rest.
-                        const uint32_t bt = smem_u32(smem + LT_BT + rb.s * LT_B);
+                        const uint32_t bt = at + LT_A;
                         const int rc = a.R >> 3;
                         const int* list = a.lists + (int64_t)(t0 / BN) * LT_LIST;
                         const int cnt = __ldg(list);
@@ -541,12 +554,11 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                     // make the generic-proxy writes visible to the tensor core, then hand over
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) lt_arrive(aready0 + ra.s * 8);
+                    if (lane == 0) lt_arrive(full0 + r.s * 8);
                 }
                 ++it;
                 if (kb < nk) rr.next();
-                ra.next();
-                rb.next();
+                r.next();
             }
         }
     } else {
