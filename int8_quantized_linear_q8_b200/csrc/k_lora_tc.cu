@@ -150,28 +150,6 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 }
 
 // ------------------------------------------------------------------------- conversion
-// Four int8 codes -> bf16 (b0, b1), (b2, b3), exact: as s8x4_to_bf16x2_eo, in order.
-__device__ __forceinline__ void s8x4_to_bf16x2_seq(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const uint32_t l = __byte_perm(w, 0, 0x4140), h = __byte_perm(w, 0, 0x4342);
-    lo = bf16x2_sub(lop_and_or(l, 0x007F007Fu, 0x43004300u),
-                    lop_and_or(l, 0x00800080u, 0x43004300u));
-    hi = bf16x2_sub(lop_and_or(h, 0x007F007Fu, 0x43004300u),
-                    lop_and_or(h, 0x00800080u, 0x43004300u));
-}
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-__device__ __forceinline__ uint32_t bf16_bits_rn(float v) {
-    return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
 // What a converter thread multiplies its codes by: nothing (forward), s_w as the bf16 pair
 // hi + lo (hi * q + lo * q is rounded once, to bf16), or a power of two.  Loaded a turn ahead as
 // raw bits, so that nothing waits on the load before its turn.
@@ -200,13 +178,10 @@ __device__ __forceinline__ LtScale lt_scale(uint32_t bits) {
 }
 template <int MODE>
 __device__ __forceinline__ uint32_t lt_apply(uint32_t v, const LtScale& s) {
-    if (MODE == LORA_DGRAD) return bf16x2_fma(v, s.hi, bf16x2_mul(v, s.lo));
-    if (MODE == LORA_WGRAD) return bf16x2_mul(v, s.hi);
+    if (MODE == LORA_DGRAD) return bf16x2_fma(v, s.hi, bf16x2_mulrn(v, s.lo));
+    if (MODE == LORA_WGRAD) return bf16x2_mulrn(v, s.hi);
     return v;
 }
-
-// the tile's adapter list: [0] their number, then their ids in ascending order
-constexpr int LT_LIST = 260;
 
 // ------------------------------------------------------------------------- the kernel
 template <int MODE>
@@ -661,39 +636,6 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                      : "memory");
 }
 
-// The adapters that the tokens of each tile use, ascending; a CTA per tile.
-__global__ __launch_bounds__(256) void k_lora_lists(const int32_t* __restrict__ ids, int64_t T,
-                                                    int BN, int L, int* __restrict__ lists) {
-    __shared__ uint32_t seen[32];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (threadIdx.x < 32) seen[threadIdx.x] = 0;
-    __syncthreads();
-    const int64_t t = (int64_t)blockIdx.x * BN + threadIdx.x;
-    if ((int)threadIdx.x < BN && t < T) {
-        const int id = __ldg(ids + t);
-        if (id >= 0 && id < L) atomicOr(&seen[id >> 5], 1u << (id & 31));
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        int* out = lists + (int64_t)blockIdx.x * LT_LIST;
-        uint32_t w = seen[threadIdx.x];
-        int n = __popc(w), before = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, before, o);
-            if ((int)threadIdx.x >= o) before += v;
-        }
-        if (threadIdx.x == 31) out[0] = before;
-        before -= n;
-        while (w) {
-            const int b = __ffs(w) - 1;
-            w &= w - 1;
-            out[1 + before++] = (int)threadIdx.x * 32 + b;
-        }
-    }
-}
-
 // ----------------------------------------------------------------------- host side
 int lora_tc_tile(int mode, int64_t T) {
     const int64_t tiles = (T + 255) / 256;
@@ -705,12 +647,6 @@ size_t lora_list_bytes(int64_t T) {
     const int64_t BN = lora_tc_tile(LORA_FWD, T);
     return (size_t)((T + BN - 1) / BN) * LT_LIST * sizeof(int);
 }
-cudaError_t launch_lora_lists(const int32_t* ids, int64_t T, int L, int* lists, cudaStream_t st) {
-    const int BN = lora_tc_tile(LORA_FWD, T);
-    k_lora_lists<<<(unsigned)((T + BN - 1) / BN), 256, 0, st>>>(ids, T, BN, L, lists);
-    return cudaGetLastError();
-}
-
 template <int MODE>
 static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, int* status) {
     const int BN = lora_tc_tile(MODE, a.T);

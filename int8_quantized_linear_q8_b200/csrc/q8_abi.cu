@@ -222,8 +222,8 @@ static q8_status check_adapter_pointers(const q8_adapters* ad, const int32_t* id
     return Q8_OK;
 }
 
-// Workspaces: the tiles' adapter lists; backward, g fp32 [M, R] before them.
-static size_t lora_fwd_bytes(int64_t M) { return M > 0 ? align_up(lora_list_bytes(M), 256) : 0; }
+// Workspaces: the plan of the rows' adapters; backward, g fp32 [M, R] before it.
+static size_t lora_fwd_bytes(int64_t M) { return M > 0 ? lora_plan_bytes(M) : 0; }
 static size_t lora_bwd_g_bytes(int64_t M, int64_t R) { return align_up((size_t)M * R * 4, 256); }
 static size_t lora_bwd_bytes(int64_t M, int64_t R) {
     return lora_bwd_g_bytes(M, R) + lora_fwd_bytes(M);
@@ -446,10 +446,9 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     Q8_TRY(current_device(sms, &status));
     cudaStream_t st = (cudaStream_t)stream;
     const int R = (int)ad->rank, L = (int)ad->count;
-    int* lists = (int*)workspace;
-    Q8_TRY(launched(launch_lora_lists(ids, M, L, lists, st)));
+    Q8_TRY(launched(launch_lora_plan(ids, M, L, workspace, st)));
     Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
-                                       ad->scale, ids, h, M, (int)K, R, L, st)));
+                                       ad->scale, workspace, h, M, (int)K, R, L, st, sms)));
     LoraGemm a = {};
     a.q = q;
     a.t = (const uint16_t*)x;
@@ -464,7 +463,7 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     a.low = (const uint16_t*)ad->b;
     a.h = h;
     a.scale = ad->scale;
-    a.lists = lists;
+    a.lists = lora_plan_lists(workspace);
     a.R = R;
     a.L = L;
     return launched(launch_lora_tc(LORA_FWD, a, st, sms, status));
@@ -509,11 +508,11 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
     if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     Q8_TRY(current_device(sms, &status));
     float* g = (float*)workspace;
-    int* lists = (int*)((uint8_t*)workspace + lora_bwd_g_bytes(M, R));
-    if (dx) Q8_TRY(launched(launch_lora_lists(ids, M, L, lists, st)));
+    void* plan = (uint8_t*)workspace + lora_bwd_g_bytes(M, R);
+    Q8_TRY(launched(launch_lora_plan(ids, M, L, plan, st)));
     if (dx || da)
         Q8_TRY(launched(launch_lora_shrink(true, (const uint16_t*)dy, (const uint16_t*)ad->b,
-                                           ad->scale, ids, g, M, (int)N, R, L, st)));
+                                           ad->scale, plan, g, M, (int)N, R, L, st, sms)));
     if (dx) {
         LoraGemm a = {};
         a.q = q;
@@ -528,17 +527,18 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
         a.low = (const uint16_t*)ad->a;
         a.h = g;
         a.scale = ad->scale;
-        a.lists = lists;
+        a.lists = lora_plan_lists(plan);
         a.R = R;
         a.L = L;
         Q8_TRY(launched(launch_lora_tc(LORA_DGRAD, a, st, sms, status)));
     }
     if (da)
-        Q8_TRY(launched(launch_lora_wgrad(false, input->x, input->exps, input->group, g,
-                                          ad->scale, ids, da, accumulate, M, (int)K, R, L, st)));
+        Q8_TRY(launched(launch_lora_wgrad(false, input->x, input->group ? input->exps : nullptr,
+                                          log2_of(input->group), g, ad->scale, plan, da,
+                                          accumulate, M, (int)K, R, L, st, sms)));
     if (db)
-        Q8_TRY(launched(launch_lora_wgrad(true, dy, nullptr, 0, h, ad->scale, ids, db, accumulate,
-                                          M, (int)N, R, L, st)));
+        Q8_TRY(launched(launch_lora_wgrad(true, dy, nullptr, 0, h, ad->scale, plan, db, accumulate,
+                                          M, (int)N, R, L, st, sms)));
     return Q8_OK;
 }
 

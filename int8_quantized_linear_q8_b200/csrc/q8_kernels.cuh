@@ -36,6 +36,28 @@ __device__ __forceinline__ void static_codes16(const float (&v)[16], float s1, f
     }
 }
 
+// Four int8 codes -> bf16 (b0, b1), (b2, b3), exact: as s8x4_to_bf16x2_eo, in order.
+__device__ __forceinline__ void s8x4_to_bf16x2_seq(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t l = __byte_perm(w, 0, 0x4140), h = __byte_perm(w, 0, 0x4342);
+    lo = bf16x2_sub(lop_and_or(l, 0x007F007Fu, 0x43004300u),
+                    lop_and_or(l, 0x00800080u, 0x43004300u));
+    hi = bf16x2_sub(lop_and_or(h, 0x007F007Fu, 0x43004300u),
+                    lop_and_or(h, 0x00800080u, 0x43004300u));
+}
+__device__ __forceinline__ uint32_t bf16x2_mulrn(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16_bits_rn(float v) {
+    return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
 // q8_abi.cu: host checks shared with the allocation-free entry point
 q8_status w8a8_check_args(const float* x, const q8_qparams& first, const q8_qparams* second,
                           const int8_t* q, const int32_t* wsum, const float* s_w,
@@ -149,19 +171,27 @@ struct LoraGemm {
     const uint16_t* low;
     const float* h;             // [T, R]; LORA_DGRAD: g, scale included
     const float* scale;
-    const int* lists;           // launch_lora_lists
+    const int* lists;           // lora_plan_lists
     int R, L;
 };
+size_t lora_plan_bytes(int64_t M);               // workspace of the plan
+const int* lora_plan_lists(const void* ws);
+cudaError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, void* ws, cudaStream_t st);
+// h (or, backward, g) of every row; ws: the plan of its ids
 cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, const float* scale,
-                               const int32_t* ids, float* h, int64_t M, int C, int R, int L,
-                               cudaStream_t st);
-cudaError_t launch_lora_wgrad(bool db, const void* x, const uint8_t* exps, int G, const float* low,
-                              const float* scale, const int32_t* ids, float* out, int accumulate,
-                              int64_t M, int P, int R, int L, cudaStream_t st);
+                               const void* ws, float* h, int64_t M, int C, int R, int L,
+                               cudaStream_t st, int num_sms);
+// dB (db: x = dy, low = h) or dA (x: the layer's input, bf16, or codes with exps; low = g)
+cudaError_t launch_lora_wgrad(bool db, const void* x, const uint8_t* exps, int gshift,
+                              const float* low, const float* scale, const void* ws, float* out,
+                              int accumulate, int64_t M, int P, int R, int L, cudaStream_t st,
+                              int num_sms);
 
 // k_lora_tc.cu
+// adapter list of a token tile: [0] their number, then their ids in ascending order
+constexpr int LT_LIST = 260;
+int lora_tc_tile(int mode, int64_t T);          // tokens per tile
 size_t lora_list_bytes(int64_t T);
-cudaError_t launch_lora_lists(const int32_t* ids, int64_t T, int L, int* lists, cudaStream_t st);
 cudaError_t launch_lora_tc(int mode, const LoraGemm& a, cudaStream_t st, int num_sms,
                            int* status);
 
