@@ -124,7 +124,10 @@ __device__ __forceinline__ void tmem_wait_ld_x8(uint32_t (&v)[8]) {
 
 // PF: the producer prefetches the first l2pf stages into L2 before the dependency wait (a
 // separate instantiation, so the kernels of short streams are unchanged by it).
-template <int MT, bool XT, int SL, bool BIAS, bool PF>
+// LOW: `bias` is a term of every output, fp32 [M, N], that the kernel before this one writes
+// (k_lora_decode.cu).  x and the weight are older than that kernel (its own predecessor waits
+// for the stream before it lets others start), so only the epilogue waits for it.
+template <int MT, bool XT, int SL, bool BIAS, bool PF, bool LOW = false>
 __global__ __launch_bounds__(WT_THREADS, 1) void k_w8a16_tma(
     const __grid_constant__ CUtensorMap wmap, const uint16_t* __restrict__ x,
     const float* __restrict__ s_w, const float* __restrict__ bias, void* __restrict__ y,
@@ -197,7 +200,7 @@ __global__ __launch_bounds__(WT_THREADS, 1) void k_w8a16_tma(
             if (++st == nst) { st = 0; ++rg; }
         }
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!LOW) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == WT_CONSUMERS) {
         // ------------------------------------------------------------- producer
@@ -348,7 +351,20 @@ __global__ __launch_bounds__(WT_THREADS, 1) void k_w8a16_tma(
     // Independent accumulator chains: consecutive MMAs of a warp go to different
     // accumulators, so they do not wait on each other's results.
     constexpr int CH = WT_SPW == 2 && MT == 1 ? 8 : 4;
+    float term[MT][4];                  // LOW: this lane's terms of the row group
+    auto load_terms = [&](int rg) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = mt * 8 + 2 * t + (i & 1), n = rg * 16 + g + 8 * (i >> 1);
+                term[mt][i] = m < M && n < N ? ld_after(bias + (int64_t)m * N + n) : 0.0f;
+            }
+    };
     for (int rg = rg0; rg < rg1; ++rg) {
+        // loaded ahead of their use, but for the first row group's: those are waited for
+        // when its sums are done
+        if (LOW && rg > rg0) load_terms(rg);
         float acc[CH][MT][4];
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -424,6 +440,10 @@ __global__ __launch_bounds__(WT_THREADS, 1) void k_w8a16_tma(
         // the WT_CONSUMERS partials in warp order (no float atomics, so the sum is the same
         // on every run), scales and writes y.  Slots rotate, so no barrier is needed: a
         // warp can run at most `stages` stages (nslots - 2 groups) ahead of the slowest one.
+        if (LOW && rg == rg0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            load_terms(rg);
+        }
         float* sl = slots + (size_t)slot * WT_CONSUMERS * MT * 128;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -468,8 +488,9 @@ __global__ __launch_bounds__(WT_THREADS, 1) void k_w8a16_tma(
                     const int n = n0 + g + 8 * (i >> 1);
                     if (m < M && n < N) {
                         const float sv = sws[n - rg0 * 16];
-                        const float r = BIAS ? fmaf(vv[mt][i], sv, sbias[n - rg0 * 16])
-                                             : vv[mt][i] * sv;
+                        const float r = LOW    ? fmaf(vv[mt][i], sv, term[mt][i])
+                                        : BIAS ? fmaf(vv[mt][i], sv, sbias[n - rg0 * 16])
+                                               : vv[mt][i] * sv;
                         if (y_bf16)
                             reinterpret_cast<__nv_bfloat16*>(y)[(int64_t)m * N + n] =
                                 __float2bfloat16_rn(r);
@@ -577,12 +598,12 @@ bool w8a16_tma_fits(int64_t M, int64_t K, bool bias) {
            wt_layout<16>((int)M, (int)K, 1, 4, false, bias).total <= (size_t)WT_MAX_SMEM;
 }
 
-template <int MT, bool XT, int SL, bool BIAS, bool PF>
+template <int MT, bool XT, int SL, bool BIAS, bool PF, bool LOW = false>
 static cudaError_t launch_wt_pf(const CUtensorMap& map, const uint16_t* x, const float* s_w,
                                 const float* bias, void* y, int y_bf16, int M, int N, int K,
                                 cudaStream_t st, int grid, int stages, size_t smem,
                                 int* status) {
-    cudaError_t e = ensure_dyn_smem<k_w8a16_tma<MT, XT, SL, BIAS, PF>>((int)smem);
+    cudaError_t e = ensure_dyn_smem<k_w8a16_tma<MT, XT, SL, BIAS, PF, LOW>>((int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -594,11 +615,11 @@ static cudaError_t launch_wt_pf(const CUtensorMap& map, const uint16_t* x, const
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_w8a16_tma<MT, XT, SL, BIAS, PF>, map, x, s_w, bias, y,
+    return cudaLaunchKernelEx(&cfg, k_w8a16_tma<MT, XT, SL, BIAS, PF, LOW>, map, x, s_w, bias, y,
                               y_bf16, M, N, K, stages, PF ? stages : 0, status);
 }
 
-template <int MT, bool XT, int SL, bool BIAS>
+template <int MT, bool XT, int SL, bool BIAS, bool LOW = false>
 static cudaError_t launch_wt(const CUtensorMap& map, const uint16_t* x, const float* s_w,
                              const float* bias, void* y, int y_bf16, int M, int N, int K,
                              cudaStream_t st, int num_sms, int* status) {
@@ -615,6 +636,9 @@ static cudaError_t launch_wt(const CUtensorMap& map, const uint16_t* x, const fl
     // CTAs that stream at least 512 KB (measured on the decode sweep: K = 4096 x N = 32000
     // -0.6 to -1.2 us per call; on shorter streams it only added latency)
     const int64_t cta_bytes = (int64_t)((RG + grid - 1) / grid) * 16 * K;
+    if (LOW)            // it does not wait before its stream: nothing to prefetch ahead of
+        return launch_wt_pf<MT, XT, SL, BIAS, false, LOW>(map, x, s_w, bias, y, y_bf16, M, N, K,
+                                                          st, grid, stages, L.total, status);
     if (cta_bytes >= ((int64_t)512 << 10))
         return launch_wt_pf<MT, XT, SL, BIAS, true>(map, x, s_w, bias, y, y_bf16, M, N, K, st,
                                                     grid, stages, L.total, status);
@@ -624,15 +648,17 @@ static cudaError_t launch_wt(const CUtensorMap& map, const uint16_t* x, const fl
 
 cudaError_t launch_w8a16_tma(const uint16_t* x, const int8_t* q, const float* s_w,
                              const float* bias, void* y, int y_bf16, int64_t M, int64_t N, int K,
-                             cudaStream_t st, int num_sms, int* status) {
+                             cudaStream_t st, int num_sms, int* status, bool low) {
     CUtensorMap map;
     if (!make_tmap_u8_2d(&map, q, N, K, WT_BOX, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     const int m = (int)M, n = (int)N;
 #define WT_LAUNCH(MT_, XT_, SL_)                                                            \
-    (bias ? launch_wt<MT_, XT_, SL_, true>(map, x, s_w, bias, y, y_bf16, m, n, K, st, num_sms, \
-                                           status)                                         \
-          : launch_wt<MT_, XT_, SL_, false>(map, x, s_w, bias, y, y_bf16, m, n, K, st,        \
+    (low    ? launch_wt<MT_, XT_, SL_, false, true>(map, x, s_w, bias, y, y_bf16, m, n, K, st,  \
+                                                    num_sms, status)                       \
+     : bias ? launch_wt<MT_, XT_, SL_, true>(map, x, s_w, bias, y, y_bf16, m, n, K, st, num_sms, \
+                                             status)                                       \
+            : launch_wt<MT_, XT_, SL_, false>(map, x, s_w, bias, y, y_bf16, m, n, K, st,        \
                                             num_sms, status))
     if (wt_use_wide(m, K, N, num_sms))
         return M <= 8 ? WT_LAUNCH(1, true, 32) : WT_LAUNCH(2, true, 32);

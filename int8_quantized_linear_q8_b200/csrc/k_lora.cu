@@ -243,16 +243,16 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tile = blockIdx.x / S;
-    if (tile >= __ldg(off + LP_KEYS + 1)) return;               // uniform over the cluster
+    if (tile >= ld_after(off + LP_KEYS + 1)) return;               // uniform over the cluster
     const int part = S > 1 ? (int)cluster_rank() : 0;
-    const int key = __ldg(tiles + 3 * tile), start = __ldg(tiles + 3 * tile + 1);
-    const int rows = __ldg(tiles + 3 * tile + 2);
+    const int key = ld_after(tiles + 3 * tile), start = ld_after(tiles + 3 * tile + 1);
+    const int rows = ld_after(tiles + 3 * tile + 2);
     const int r0 = blockIdx.y * (8 * NT), rn = min(8 * NT, R - r0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (key < 0) {                                              // rows without an adapter
         if (part == 0)
             for (int u = tid; u < rows * rn; u += 128)
-                h[(int64_t)__ldg(perm + start + u / rn) * R + r0 + u % rn] = 0.0f;
+                h[(int64_t)ld_after(perm + start + u / rn) * R + r0 + u % rn] = 0.0f;
         return;
     }
     const int steps = (C + 63) / 64;
@@ -261,7 +261,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
     // copies: thread -> row tid >> 1, four 16-byte pieces from 4 * (tid & 1)
     const int crow = tid >> 1, cp0 = (tid & 1) * 4;
     const uint16_t* xrow =
-        x + (int64_t)__ldg(perm + start + (crow < rows ? crow : 0)) * C;
+        x + (int64_t)ld_after(perm + start + (crow < rows ? crow : 0)) * C;
     const uint16_t* wmat = W + (int64_t)key * R * C;
     auto load = [&](int st, int slot) {
         const uint32_t xs = base + slot * 16384, wsm = xs + 8192;
@@ -334,7 +334,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
             for (int i = 0; i < 4; ++i) {
                 const int row = warp * 16 + g + 8 * (i >> 1), r = n * 8 + 2 * t + (i & 1);
                 if (row < rows && r < rn)
-                    h[(int64_t)__ldg(perm + start + row) * R + r0 + r] = acc[n][i] * f;
+                    h[(int64_t)ld_after(perm + start + row) * R + r0 + r] = acc[n][i] * f;
             }
         return;
     }
@@ -354,7 +354,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
         const int row = lo + u / rn, r = u % rn;
         float v = 0.0f;
         for (int q = 0; q < S; ++q) v += ld_peer(base + (row * LD + r) * 4, q);
-        h[(int64_t)__ldg(perm + start + row) * R + r0 + r] = v * f;
+        h[(int64_t)ld_after(perm + start + row) * R + r0 + r] = v * f;
     }
     cluster_sync_all();                             // nobody leaves while its part is read
 }
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(128) void k_lora_wgrad(
     const int p0 = blockIdx.x / S * 128, r0 = blockIdx.y * (8 * NT), rn = min(8 * NT, R - r0);
     const int key = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int first = __ldg(off + key), total = __ldg(off + key + 1) - first;
+    const int first = ld_after(off + key), total = ld_after(off + key + 1) - first;
     const int steps = (total + LW_ROWS - 1) / LW_ROWS;
     const int s0 = (int)((int64_t)steps * part / S), s1 = (int)((int64_t)steps * (part + 1) / S);
     const uint32_t base = smem_u32(sm);
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(128) void k_lora_wgrad(
     auto fetch = [&](int st) {
         const int at = st * LW_ROWS + xr;
         const bool live = at < total;
-        const int64_t m = live ? __ldg(perm + first + at) : 0;
+        const int64_t m = live ? ld_after(perm + first + at) : 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) xv[j] = make_uint4(0, 0, 0, 0);
         if (KIND == 1) {
@@ -419,7 +419,7 @@ __global__ __launch_bounds__(128) void k_lora_wgrad(
 #pragma unroll
         for (int j = 0; j < 2 * NT; ++j) {
             const int r = (tid & 3) * 2 * NT + j;
-            lv[j] = live && r < rn ? __ldg(low + m * R + r0 + r) * f : 0.0f;
+            lv[j] = live && r < rn ? ld_after(low + m * R + r0 + r) * f : 0.0f;
         }
     };
     auto place = [&](int buf) {

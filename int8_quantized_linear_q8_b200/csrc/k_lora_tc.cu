@@ -218,7 +218,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
     // stages of adapter columns after the tile's nk base stages
     auto low_stages = [&](int t0) {
         if (MODE == LORA_WGRAD || !a.ids) return 0;
-        const int cnt = __ldg(a.lists + (int64_t)(t0 / BN) * LT_LIST);
+        const int cnt = ld_after(a.lists + (int64_t)(t0 / BN) * LT_LIST);
         return (cnt * 2 * a.R + LT_BK - 1) / LT_BK;
     };
 
@@ -475,56 +475,58 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                         const uint32_t bt = at + LT_A;
                         const int rc = a.R >> 3;
                         const int* list = a.lists + (int64_t)(t0 / BN) * LT_LIST;
-                        const int cnt = __ldg(list);
+                        const int cnt = ld_after(list);
                         const int t = t0 + (int)rank * half + tid;
                         const bool row_t = tid < half;
                         const int id = row_t && t < a.T ? __ldg(a.ids + t) : -1;
-#pragma unroll 2
+                        int ad[8], col[8];              // adapter (-1: none) and its first column
+                        bool rest[8];
+#pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             const int piece = (kb - nk) * 8 + c;
-                            const int e = piece / (2 * rc);
-                            const int in = piece - e * 2 * rc;
-                            const int low = in >= rc, r0 = (in - low * rc) * 8;
-                            const int i = e < cnt ? __ldg(list + 1 + e) : -1;
-                            if (!A_MN) {
-                                uint4 w = make_uint4(0, 0, 0, 0);
-                                const int p = p0 + tid;
-                                if (i >= 0 && p < a.P)
-                                    w = ldg_keep(a.low + ((int64_t)i * a.P + p) * a.R + r0);
-                                sts128(at + tid * 128 + ((c ^ (tid & 7)) << 4), w.x, w.y, w.z,
-                                       w.w);
-                            } else {
-                                // row 8 c + (tid >> 4) of the 64, piece tid & 15 of 128 p
-                                const int r = tid >> 4, pc = tid & 15;
-                                const int p = p0 + pc * 8;
-                                uint4 w = make_uint4(0, 0, 0, 0);
-                                if (i >= 0 && p < a.P)
-                                    w = ldg_keep(a.low + ((int64_t)i * a.R + r0 + r) * a.P + p);
-                                sts128(at + (pc >> 3) * 8192 + (8 * c + r) * 128 +
-                                           (((pc & 7) ^ r) << 4),
-                                       w.x, w.y, w.z, w.w);
-                            }
-                            if (row_t) {
-                                uint32_t o[4] = {0, 0, 0, 0};
-                                if (i >= 0 && id == i) {
-                                    const float sc = MODE == LORA_FWD ? __ldg(a.scale + i) : 1.0f;
-                                    const float4* hp = reinterpret_cast<const float4*>(
-                                        a.h + (int64_t)t * a.R + r0);
-                                    const float4 h0 = hp[0], h1 = hp[1];
-                                    const float v[8] = {h0.x * sc, h0.y * sc, h0.z * sc,
-                                                        h0.w * sc, h1.x * sc, h1.y * sc,
-                                                        h1.z * sc, h1.w * sc};
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) {
-                                        uint32_t b = bf16_bits_rn(v[j]);
-                                        if (low) b = bf16_bits_rn(v[j] - __uint_as_float(b << 16));
-                                        o[j >> 1] |= b << (16 * (j & 1));
-                                    }
-                                }
-                                sts128(bt + tid * 128 + ((c ^ (tid & 7)) << 4), o[0], o[1], o[2],
-                                       o[3]);
-                            }
+                            const int e = piece / (2 * rc), in = piece - e * 2 * rc;
+                            rest[c] = in >= rc;
+                            col[c] = (rest[c] ? in - rc : in) * 8;
+                            ad[c] = e < cnt ? ld_after(list + 1 + e) : -1;
                         }
+                        // all loads of the P tile before the first use of one
+                        uint4 w[8];
+                        const int pr = tid >> 4, pc = tid & 15;     // A_MN: row and 8 p of a piece
+                        const int p = A_MN ? p0 + pc * 8 : p0 + tid;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            w[c] = make_uint4(0, 0, 0, 0);
+                            if (ad[c] >= 0 && p < a.P)
+                                w[c] = ldg_keep(
+                                    A_MN ? a.low + ((int64_t)ad[c] * a.R + col[c] + pr) * a.P + p
+                                         : a.low + ((int64_t)ad[c] * a.P + p) * a.R + col[c]);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            if (!row_t) break;
+                            uint32_t o[4] = {0, 0, 0, 0};
+                            if (ad[c] >= 0 && id == ad[c]) {
+                                const float f = MODE == LORA_FWD ? __ldg(a.scale + id) : 1.0f;
+                                const float* hp = a.h + (int64_t)t * a.R + col[c];
+                                const float4 h0 = ld_after4(hp), h1 = ld_after4(hp + 4);
+                                const float v[8] = {h0.x * f, h0.y * f, h0.z * f, h0.w * f,
+                                                    h1.x * f, h1.y * f, h1.z * f, h1.w * f};
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    uint32_t b = bf16_bits_rn(v[j]);
+                                    if (rest[c]) b = bf16_bits_rn(v[j] - __uint_as_float(b << 16));
+                                    o[j >> 1] |= b << (16 * (j & 1));
+                                }
+                            }
+                            sts128(bt + tid * 128 + ((c ^ (tid & 7)) << 4), o[0], o[1], o[2],
+                                   o[3]);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            sts128(A_MN ? at + (pc >> 3) * 8192 + (8 * c + pr) * 128 +
+                                              (((pc & 7) ^ pr) << 4)
+                                        : at + tid * 128 + ((c ^ (tid & 7)) << 4),
+                                   w[c].x, w[c].y, w[c].z, w[c].w);
                     }
                     // make the generic-proxy writes visible to the tensor core, then hand over
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

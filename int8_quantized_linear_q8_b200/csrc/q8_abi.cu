@@ -223,10 +223,15 @@ static q8_status check_adapter_pointers(const q8_adapters* ad, const int32_t* id
 }
 
 // Workspaces: the plan of the rows' adapters; backward, g fp32 [M, R] before it.
-static size_t lora_fwd_bytes(int64_t M) { return M > 0 ? lora_plan_bytes(M) : 0; }
+// Up to 16 rows run the decode GEMV where it takes the shape; it needs the term [M, N].
+static inline bool lora_decodes(int64_t M, int64_t K) { return M <= 16 && w8a16_tma_fits(M, K); }
+static size_t lora_fwd_bytes(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0) return 0;
+    return lora_decodes(M, K) ? align_up((size_t)M * (size_t)N * 4, 256) : lora_plan_bytes(M);
+}
 static size_t lora_bwd_g_bytes(int64_t M, int64_t R) { return align_up((size_t)M * R * 4, 256); }
 static size_t lora_bwd_bytes(int64_t M, int64_t R) {
-    return lora_bwd_g_bytes(M, R) + lora_fwd_bytes(M);
+    return M > 0 ? lora_bwd_g_bytes(M, R) + lora_plan_bytes(M) : 0;
 }
 static inline int log2_of(int g) { return g == 32 ? 5 : g == 64 ? 6 : g == 128 ? 7 : 8; }
 
@@ -410,7 +415,7 @@ size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K, int extra) 
             return plan_gptq(N, K).bytes;
         case Q8_OP_LINEAR_W8A16_LORA:
             if (M > 0x7fffffff || !valid_rank(extra)) return 0;
-            return lora_fwd_bytes(M);
+            return lora_fwd_bytes(M, N, K);
         case Q8_OP_LINEAR_W8A16_LORA_BACKWARD:
             if (M > 0x7fffffff || !valid_rank(extra)) return 0;
             return lora_bwd_bytes(M, extra);
@@ -438,7 +443,7 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     if (!aligned16(x) || !aligned16(q) || !aligned16(y) || !aligned16(h) || !aligned4(s_w) ||
         !aligned4(bias))
         return Q8_ERR_ALIGN;
-    const size_t need = lora_fwd_bytes(M);
+    const size_t need = lora_fwd_bytes(M, N, K);
     if (!workspace || ws_bytes < need) return Q8_ERR_WORKSPACE;
     if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     int sms = 0;
@@ -446,6 +451,14 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     Q8_TRY(current_device(sms, &status));
     cudaStream_t st = (cudaStream_t)stream;
     const int R = (int)ad->rank, L = (int)ad->count;
+    if (lora_decodes(M, K)) {
+        float* t = (float*)workspace;
+        Q8_TRY(launched(launch_lora_decode((const uint16_t*)x, (const uint16_t*)ad->a,
+                                           (const uint16_t*)ad->b, ad->scale, bias, ids, h, t,
+                                           (int)M, N, (int)K, R, L, st)));
+        return launched(launch_w8a16_tma((const uint16_t*)x, q, s_w, t, y, yt == Q8_BF16, M, N,
+                                         (int)K, st, sms, status, true));
+    }
     Q8_TRY(launched(launch_lora_plan(ids, M, L, workspace, st)));
     Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
                                        ad->scale, workspace, h, M, (int)K, R, L, st, sms)));

@@ -58,6 +58,28 @@ __device__ __forceinline__ uint32_t bf16_bits_rn(float v) {
     return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Loads of what an earlier kernel of a chain of programmatic dependent launches wrote: volatile,
+// so that none is moved ahead of the griddepcontrol.wait before it (a __ldg is taken to read
+// memory that never changes).
+__device__ __forceinline__ int ld_after(const int* p) {
+    int v;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_after(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_after4(const float* p) {
+    float4 v;
+    asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // q8_abi.cu: host checks shared with the allocation-free entry point
 q8_status w8a8_check_args(const float* x, const q8_qparams& first, const q8_qparams* second,
                           const int8_t* q, const int32_t* wsum, const float* s_w,
@@ -97,7 +119,14 @@ bool w8a16_tma_fits(int64_t M, int64_t K, bool bias = false);
 // bias (nullable, fp32 [N]) is added after the scale in every linear launcher below
 cudaError_t launch_w8a16_tma(const uint16_t* x, const int8_t* q, const float* s_w,
                              const float* bias, void* y, int y_bf16, int64_t M, int64_t N, int K,
-                             cudaStream_t st, int num_sms, int* status);
+                             cudaStream_t st, int num_sms, int* status, bool low = false);
+// low: `bias` is an fp32 [M, N] term that the stream's last kernel writes
+// (launch_lora_decode, and only that: see k_w8a16_tma)
+
+// k_lora_decode.cu: h [M, R] and the term t [M, N] of up to 16 rows
+cudaError_t launch_lora_decode(const uint16_t* x, const uint16_t* A, const uint16_t* B,
+                               const float* scale, const float* bias, const int32_t* ids, float* h,
+                               float* t, int M, int64_t N, int K, int R, int L, cudaStream_t st);
 
 // k_gemm_tc.cu
 cudaError_t launch_gemm_s8s8_s32_tc(const int8_t* a, const int8_t* b, int32_t* acc, int64_t M,
