@@ -88,7 +88,8 @@ typedef enum {
     Q8_OP_LINEAR_DQ8CA_Q4GSW = 1,
     Q8_OP_GPTQ_INT8 = 3,            /* q8_gptq_int8 (M unused, extra = block) */
     Q8_OP_LINEAR_W8A16_LORA = 4,           /* q8_linear_w8a16_lora (extra = rank)          */
-    Q8_OP_LINEAR_W8A16_LORA_BACKWARD = 5   /* q8_linear_w8a16_lora_backward (extra = rank) */
+    Q8_OP_LINEAR_W8A16_LORA_BACKWARD = 5,  /* q8_linear_w8a16_lora_backward (extra = rank) */
+    Q8_OP_CHECKPOINT_WGRAD = 6             /* q8_checkpoint_wgrad (extra unused)           */
 } q8_op;
 
 /* Host.  Human-readable name of a status code (static string). */
@@ -405,10 +406,12 @@ q8_status q8_checkpoint_load(const int8_t* codes, const uint8_t* exps, int group
  * exact products, fp32 accumulation.
  *   dy device bf16 [M, N] (N % 8 == 0, Q8_ERR_SHAPE otherwise); codes, exps, group as
  *   written by q8_checkpoint_save; dw device fp32 [N, K]: overwritten, or added to when
- *   accumulate != 0.  M == 0 sets dw to 0 (leaves it when accumulating). */
+ *   accumulate != 0.  M == 0 sets dw to 0 (leaves it when accumulating).
+ *   workspace: at least q8_workspace_bytes(Q8_OP_CHECKPOINT_WGRAD, M, N, K, 0) bytes (may be
+ *   NULL when that is 0), with the rules of q8_linear_w8a16_lora. */
 q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t* exps,
                               int group, float* dw, int accumulate, int64_t M, int64_t N,
-                              int64_t K, void* stream);
+                              int64_t K, void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------- GPTQ (offline) */
 

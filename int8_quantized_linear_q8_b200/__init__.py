@@ -26,7 +26,7 @@ Q8_ERR_UNSUPPORTED_ARCH, Q8_ERR_LAUNCH, Q8_ERR_WORKSPACE, Q8_ERR_DEVICE = 5, 6, 
 Q8_F32, Q8_BF16 = 0, 1
 Q8_OP_LINEAR_W8A8, Q8_OP_LINEAR_DQ8CA_Q4GSW = 0, 1
 Q8_OP_GPTQ_INT8 = 3
-Q8_OP_LINEAR_W8A16_LORA, Q8_OP_LINEAR_W8A16_LORA_BACKWARD = 4, 5
+Q8_OP_LINEAR_W8A16_LORA, Q8_OP_LINEAR_W8A16_LORA_BACKWARD, Q8_OP_CHECKPOINT_WGRAD = 4, 5, 6
 Q8_GRID_SYM127, Q8_GRID_FULL128 = 0, 1
 _GRIDS = {"sym127": Q8_GRID_SYM127, "full128": Q8_GRID_FULL128}
 
@@ -146,7 +146,8 @@ def _lib() -> ctypes.CDLL:
     L.q8_checkpoint_load.restype = st
     L.q8_checkpoint_load.argtypes = [_vp, _vp, st, _vp, st, _i64, _i64, _vp]
     L.q8_checkpoint_wgrad.restype = st
-    L.q8_checkpoint_wgrad.argtypes = [_vp, _vp, _vp, st, _vp, st, _i64, _i64, _i64, _vp]
+    L.q8_checkpoint_wgrad.argtypes = [_vp, _vp, _vp, st, _vp, st, _i64, _i64, _i64, _vp, _sz,
+                                      _vp]
     _LIB = L
     return L
 
@@ -603,7 +604,7 @@ def q8_checkpoint_load(codes: torch.Tensor, exps: torch.Tensor, y=None,
 
 
 def q8_checkpoint_wgrad(dy: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor, dw=None,
-                        accumulate: bool = False, stream=None) -> torch.Tensor:
+                        accumulate: bool = False, workspace=None, stream=None) -> torch.Tensor:
     """dw [N, K] (= or, with accumulate, +=) dy^T x of a bf16 [M, N] gradient and the
     checkpoint of the layer's input x [M, K]; fp32."""
     M, N = dy.shape
@@ -613,9 +614,14 @@ def q8_checkpoint_wgrad(dy: torch.Tensor, codes: torch.Tensor, exps: torch.Tenso
     if accumulate and dw is None:
         raise ValueError("accumulate adds to dw: pass it")
     dw = _result(dw, "dw", torch.float32, (N, K), dy.device, stream)
-    _same_device(dy, codes, exps, dw)
+    _same_device(dy, codes, exps, dw, workspace)
+    nbytes = _lib().q8_workspace_bytes(Q8_OP_CHECKPOINT_WGRAD, M, N, K, 0)
+    if nbytes and workspace is None:
+        workspace = _empty((nbytes,), torch.uint8, dy.device, stream)
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib().q8_checkpoint_wgrad(_ptr(dy), _ptr(codes), _ptr(exps), saved.group, _ptr(dw),
-                                      int(bool(accumulate)), M, N, K, _stream(stream)),
+                                      int(bool(accumulate)), M, N, K, _ptr(workspace), wsb,
+                                      _stream(stream)),
            "q8_checkpoint_wgrad")
     return dw
 

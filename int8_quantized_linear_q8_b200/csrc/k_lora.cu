@@ -190,16 +190,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(live ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -238,7 +228,8 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
                                                      const int* __restrict__ perm,
                                                      const int* __restrict__ off,
                                                      const int* __restrict__ tiles, int C, int R,
-                                                     int S, float* __restrict__ h) {
+                                                     int S, float* __restrict__ h,
+                                                     uint16_t* __restrict__ hp) {
     extern __shared__ __align__(1024) uint8_t sm[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -325,7 +316,16 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
         }
         slot = (slot + 1) % LSH_STAGES;
     }
-    const float f = BWD ? __ldg(scale + key) : 1.0f;
+    // h (or g) in fp32, and times the scale in two bf16 parts, [M, 2 R]: high, rest
+    const float f = __ldg(scale + key);
+    auto put = [&](int row, int r, float v) {
+        const int64_t m = ld_after(perm + start + row);
+        const float sv = v * f;
+        h[m * R + r0 + r] = BWD ? sv : v;
+        const uint32_t hi = bf16_bits_rn(sv);
+        hp[m * 2 * R + r0 + r] = (uint16_t)hi;
+        hp[m * 2 * R + R + r0 + r] = (uint16_t)bf16_bits_rn(sv - __uint_as_float(hi << 16));
+    };
     const int g = lane >> 2, t = lane & 3;
     if (S == 1) {
 #pragma unroll
@@ -333,8 +333,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int row = warp * 16 + g + 8 * (i >> 1), r = n * 8 + 2 * t + (i & 1);
-                if (row < rows && r < rn)
-                    h[(int64_t)ld_after(perm + start + row) * R + r0 + r] = acc[n][i] * f;
+                if (row < rows && r < rn) put(row, r, acc[n][i]);
             }
         return;
     }
@@ -354,7 +353,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
         const int row = lo + u / rn, r = u % rn;
         float v = 0.0f;
         for (int q = 0; q < S; ++q) v += ld_peer(base + (row * LD + r) * 4, q);
-        h[(int64_t)ld_after(perm + start + row) * R + r0 + r] = v * f;
+        put(row, r, v);
     }
     cluster_sync_all();                             // nobody leaves while its part is read
 }
@@ -571,8 +570,8 @@ static cudaError_t launch_clustered(void (*k)(KArgs...), dim3 grid, int S, size_
 static int rank_tiles(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : R <= 32 ? 4 : 8; }
 
 cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, const float* scale,
-                               const void* ws, float* h, int64_t M, int C, int R, int L,
-                               cudaStream_t st, int num_sms) {
+                               const void* ws, float* h, uint16_t* hp, int64_t M, int C, int R,
+                               int L, cudaStream_t st, int num_sms) {
     const LoraPlan p = plan_of(M);
     const uint8_t* wsb = (const uint8_t*)ws;
     const int* perm = (const int*)(wsb + p.perm);
@@ -589,7 +588,7 @@ cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, c
         cudaError_t e = ensure_dyn_smem<k_lora_shrink<NT_, B_>>(LSH_BYTES);                   \
         if (e != cudaSuccess) return e;                                                       \
         return launch_clustered(k_lora_shrink<NT_, B_>, grid, S, LSH_BYTES, st, x, w, scale,  \
-                                perm, off, tl, C, R, S, h);                                   \
+                                perm, off, tl, C, R, S, h, hp);                                   \
     } while (0)
 #define LORA_SHRINK_NT(NT_)              \
     do {                                 \

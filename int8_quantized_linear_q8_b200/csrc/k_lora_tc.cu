@@ -20,15 +20,24 @@
 //
 // The adapter term is more of the same contraction: for the adapters that the tile's tokens
 // use (a list made per tile beforehand), the rank's columns of b (or a) on the P side and of
-// scale * h (or g) on the T side, zero for tokens of other adapters.  h is split into two bf16
-// parts (high and the rest: off by at most 2^-17), so an adapter takes 2 * rank columns.  Forward
-// it goes to the other accumulator buffer, since s_w applies to the base sum alone.
+// scale * h (or g) on the T side, zero for tokens of other adapters.  h comes as two bf16 parts
+// (high and rest: off by at most 2^-17), so an adapter takes 2 * rank columns.  Forward it goes
+// to the other accumulator buffer, since s_w applies to the base sum alone.
 //
-// Roles (19 warps): 0 and 2 TMA producers of the int8 and the bf16 operand; 1 tensor-memory
+// Two variants.  PRE: the int8 operand was expanded to bf16 in the workspace beforehand
+// (k_lora_expand) and both operands come by TMA.  Otherwise it stays int8 in HBM and L2 and the
+// kernel converts it, which costs nothing extra to read but adds 24 KB of shared-memory traffic
+// to the 64 KB that a stage and CTA move anyway, more than the port carries in the MMAs' time.
+//
+// Few tiles (fewer than half the CTA pairs): S = 2 or 4 pairs of one cluster split a tile's
+// stages; each owns 1 / S of the tile's columns and adds the other pairs' parts, which they
+// store in its shared memory (free by then), in pair order.
+//
+// Roles (19 warps): 0 and 2 TMA producers of the int8 and the bf16 operands; 1 tensor-memory
 // allocator and, in the pair's first CTA, MMA issuer; 3-10 converters, two groups of four
 // that take every other stage; 11-18 epilogue.  A stage is 64 of c.  Its int8 box (8 KB) has
 // a ring of its own, eight deep: that path is the longest (copy, conversion, MMA) and runs
-// ahead.  Its converted P tile and its T tile (16 KB each) share a slot of a ring of five, so
+// ahead.  Its P tile and its T tile (16 KB each) share a slot of a ring of five (PRE: seven), so
 // that the issuing warp, whose own steps bound the main loop, has one barrier to wait for
 // and one commit to make per stage; it tests the next stage's barrier before it issues this
 // stage's MMAs, which hides the test.  Every wait is bounded.
@@ -38,9 +47,11 @@ namespace q8 {
 
 constexpr int LT_BK = 64;
 constexpr int LT_A = 128 * 128, LT_B = 128 * 128, LT_RAW = 128 * 64;
-constexpr int LT_N = 5, LT_NR = 8;                      // ring depths
-constexpr int LT_SLOT = LT_A + LT_B, LT_RT = LT_N * LT_SLOT;
+constexpr int LT_N_MAX = 7, LT_NR = 8;                  // ring depths
+__host__ __device__ constexpr int lt_slots(bool pre) { return pre ? 7 : 5; }
+constexpr int LT_SLOT = LT_A + LT_B, LT_RT = 5 * LT_SLOT;
 constexpr int LT_CTRL = LT_RT + LT_NR * LT_RAW;
+static_assert(LT_CTRL >= LT_N_MAX * LT_SLOT, "PRE uses the whole region for its slots");
 constexpr int LT_CONV = 8, LT_EPI = 8, LT_CONV0 = 3, LT_EPI0 = LT_CONV0 + LT_CONV;
 constexpr int LT_THREADS = 32 * (LT_EPI0 + LT_EPI);
 constexpr int LT_SMEM = LT_CTRL + 1024 + 512;
@@ -118,12 +129,12 @@ __device__ __forceinline__ void lt_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// arrives on the barrier at the same offset in both CTAs once the MMAs issued so far are done
-__device__ __forceinline__ void lt_commit(uint64_t* bar) {
+// arrives on the barrier at the same offset in the pair's CTAs once the MMAs issued so far are done
+__device__ __forceinline__ void lt_commit(uint64_t* bar, uint16_t ctas) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
         ".b64 [%0], %1;" ::"r"(smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"(ctas)
         : "memory");
 }
 __device__ __forceinline__ void lt_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -184,12 +195,52 @@ __device__ __forceinline__ uint32_t lt_apply(uint32_t v, const LtScale& s) {
 }
 
 // ------------------------------------------------------------------------- the kernel
+// Writes 32 columns (t0 + j) of this lane's p: v + bias.  All lanes of the warp call it.
 template <int MODE>
-__global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
+__device__ __forceinline__ void lt_store(const LoraGemm& a, int t0, int p, float bs,
+                                         float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+    if (MODE == LORA_FWD)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += bs;
+    if (MODE != LORA_WGRAD && a.out_bf16 && (a.P & 1) == 0) {
+        // neighbouring lanes exchange, so that each stores two p of one t
+        uint32_t* out = reinterpret_cast<uint32_t*>(a.out);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            const bool od = lane & 1;
+            const float got = __shfl_xor_sync(0xffffffffu, od ? v[j] : v[j + 1], 1);
+            const uint32_t lo = bf16_bits_rn(od ? got : v[j]);
+            const uint32_t hi = bf16_bits_rn(od ? v[j + 1] : got);
+            const int64_t t = t0 + j + (od ? 1 : 0);
+            if (t < a.T && p < a.P) out[(t * a.P + (p & ~1)) >> 1] = lo | hi << 16;
+        }
+    } else if (MODE != LORA_WGRAD && a.out_bf16) {
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (t0 + j < a.T && p < a.P)
+                out[(int64_t)(t0 + j) * a.P + p] = __float2bfloat16_rn(v[j]);
+    } else {
+        float* out = reinterpret_cast<float*>(a.out) + (int64_t)t0 * a.P + p;
+        if (MODE == LORA_WGRAD && a.accumulate) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (t0 + j < a.T && p < a.P) v[j] += out[(int64_t)j * a.P];
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (t0 + j < a.T && p < a.P) out[(int64_t)j * a.P] = v[j];
+    }
+}
+
+template <int MODE, bool PRE>
+__global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
     const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap tmap,
-    const LoraGemm a, int BN, int num_p, int num_t, int* status) {
+    const LoraGemm a, int BN, int num_p, int num_t, int S, int* status) {
     constexpr bool A_MN = MODE != LORA_FWD;             // int8 operand with p contiguous
     constexpr bool B_MN = MODE == LORA_WGRAD;           // bf16 operand with t contiguous
+    constexpr int LT_N = lt_slots(PRE);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t* rfull = reinterpret_cast<uint64_t*>(smem + LT_CTRL);
@@ -203,8 +254,12 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = lt_rank();
+    // pair of the cluster, CTA of the pair, and the cluster rank of the pair's first CTA
+    const uint32_t crank = lt_rank(), rank = crank & 1u, lead = crank & ~1u;
+    const int pair = (int)(crank >> 1);
+    const uint16_t both = (uint16_t)(3u << lead);
     const int units = num_p * num_t;
+    const int u0 = blockIdx.x / (2 * S), ustep = gridDim.x / (2 * S);
     const int nk = (a.C + LT_BK - 1) / LT_BK;
     const int half = BN >> 1;
     // Tiles run over t first, in blocks of 16 t tiles: the pairs that run at once share both
@@ -215,11 +270,16 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
         p0 = rem / tb * 256 + (int)rank * 128;
         t0 = (blk * 16 + rem % tb) * BN;
     };
-    // stages of adapter columns after the tile's nk base stages
-    auto low_stages = [&](int t0) {
-        if (MODE == LORA_WGRAD || !a.ids) return 0;
-        const int cnt = ld_after(a.lists + (int64_t)(t0 / BN) * LT_LIST);
-        return (cnt * 2 * a.R + LT_BK - 1) / LT_BK;
+    // A tile's stages: nk of the base sum, then those of its adapters' columns; this pair
+    // takes [k0, k1).
+    auto stages_of = [&](int t0, int& k0, int& k1) {
+        int total = nk;
+        if (MODE != LORA_WGRAD) {
+            const int cnt = ld_after(a.lists + (int64_t)(t0 / BN) * LT_LIST);
+            total += (cnt * 2 * a.R + LT_BK - 1) / LT_BK;
+        }
+        k0 = total * pair / S;
+        k1 = total * (pair + 1) / S;
     };
 
     if (threadIdx.x == 0) {
@@ -228,7 +288,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
             mbar_init(&rempty[i], LT_CONV / 2);
         }
         for (int i = 0; i < LT_N; ++i) {
-            mbar_init(&full[i], LT_CONV + 1);           // a group of either CTA, the T copies
+            mbar_init(&full[i], LT_CONV + 1);           // a group of either CTA, the copies
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -260,10 +320,11 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
         LtRing<LT_NR> r;
         int it = 0;
         bool ok = true;
-        for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
-            int p0, t0;
+        for (int u = u0; u < units && ok && !PRE; u += ustep) {
+            int p0, t0, k0, k1;
             tile_of(u, p0, t0);
-            for (int kb = 0; kb < nk; ++kb) {
+            stages_of(t0, k0, k1);
+            for (int kb = k0; kb < min(nk, k1); ++kb) {
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(&rempty[r.s], r.ph ^ 1u, status, abort_flag));
                 if (!ok) break;
@@ -286,24 +347,31 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
     } else if (warp == 2) {
         // ---------------------------------------------------------------- bf16 producer
         if (lane == 0) tma_prefetch_desc(&tmap);
-        const uint32_t full0 = lt_map(smem_u32(full), 0);
+        const uint32_t full0 = lt_map(smem_u32(full), lead);
         LtRing<LT_N> r;
         int it = 0;
         bool ok = true;
-        for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
-            int p0, t0;
+        for (int u = u0; u < units && ok; u += ustep) {
+            int p0, t0, k0, k1;
             tile_of(u, p0, t0);
-            const int total = nk + low_stages(t0);
+            stages_of(t0, k0, k1);
             const int tr = t0 + (int)rank * half;
-            for (int kb = 0; kb < total; ++kb) {
+            for (int kb = k0; kb < k1; ++kb) {
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag));
                 if (!ok) break;
                 if (lane == 0) {
                     if (kb < nk) {
                         const int c0 = kb * LT_BK;
-                        const uint32_t bt = smem_u32(smem + r.s * LT_SLOT + LT_A);
-                        if (rank == 0) mbar_expect_tx(&full[r.s], (uint32_t)BN * 128u);
+                        const uint32_t at = smem_u32(smem + r.s * LT_SLOT), bt = at + LT_A;
+                        if (rank == 0)
+                            mbar_expect_tx(&full[r.s], (uint32_t)BN * 128u + (PRE ? 2 * LT_A : 0));
+                        if (PRE && A_MN) {
+                            lt_tma_pair(at, &pmap, p0 * 2, c0, full0 + r.s * 8);
+                            lt_tma_pair(at + 8192, &pmap, (p0 + 64) * 2, c0, full0 + r.s * 8);
+                        } else if (PRE) {
+                            lt_tma_pair(at, &pmap, c0 * 2, p0, full0 + r.s * 8);
+                        }
                         if (B_MN)
                             for (int b = 0; b < half / 64; ++b)
                                 lt_tma_pair(bt + b * 8192, &tmap, (tr + b * 64) * 2, c0,
@@ -328,15 +396,15 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
             LtRing<LT_N> r;
             LtRing<2> rt;
             bool ok = true, here = false;
-            for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
-                int p0, t0;
+            for (int u = u0; u < units && ok; u += ustep) {
+                int p0, t0, k0, k1;
                 tile_of(u, p0, t0);
-                const int total = nk + low_stages(t0);
-                for (int kb = 0; kb < total && ok; ++kb) {
-                    const bool fresh = kb == 0 || (MODE == LORA_FWD && kb == nk);
+                stages_of(t0, k0, k1);
+                for (int kb = k0; kb < k1 && ok; ++kb) {
+                    const bool fresh = kb == k0 || (MODE == LORA_FWD && kb == nk);
                     if (fresh) {
-                        if (kb) {                       // base sum complete
-                            if (lt_elect()) lt_commit(&tfull[rt.s]);
+                        if (kb > k0) {                  // base sum complete
+                            if (lt_elect()) lt_commit(&tfull[rt.s], both);
                             __syncwarp();
                             rt.next();
                         }
@@ -361,16 +429,16 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                         for (int k = 0; k < LT_BK / 16; ++k)
                             lt_mma(d, ad + (A_MN ? 128 : 2) * k, bd + (B_MN ? 128 : 2) * k, idesc,
                                    !(fresh && k == 0));
-                        lt_commit(&empty[cur]);
+                        lt_commit(&empty[cur], both);
                     }
                     here = __all_sync(0xffffffffu, here);
                 }
                 if (!ok) break;
-                if (lt_elect()) lt_commit(&tfull[rt.s]);
+                if (lt_elect()) lt_commit(&tfull[rt.s], both);
                 __syncwarp();
                 rt.next();
             }
-            if (lt_elect()) lt_commit(mma_done);        // before tensor memory is released
+            if (lt_elect()) lt_commit(mma_done, both);  // before tensor memory is released
             __syncwarp();
             mbar_drain(mma_done, 0, status);
         }
@@ -379,27 +447,27 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
         // ---------------------------------------------------------------- converters
         const int grp = (warp - LT_CONV0) >> 2;
         const int tid = threadIdx.x - 32 * LT_CONV0 - grp * 128;
-        const uint32_t full0 = lt_map(smem_u32(full), 0);
+        const uint32_t full0 = lt_map(smem_u32(full), lead);
         LtRing<LT_NR> rr;
         LtRing<LT_N> r;
         int it = 0;
         bool live = true;
-        for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
-            int p0, t0;
+        for (int u = u0; u < units; u += ustep) {
+            int p0, t0, k0, k1;
             tile_of(u, p0, t0);
-            const int total = nk + low_stages(t0);
+            stages_of(t0, k0, k1);
             const int sc = tid >> 3, sp = p0 + (tid & 7) * 16;     // this thread's first c, its p
             uint32_t nxt[4];                            // the next turn's scales
-            if (A_MN) {
-                const int kb = (it & 1) == grp ? 0 : 1;
+            if (A_MN && !PRE) {
+                const int kb = k0 + ((it & 1) == grp ? 0 : 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     nxt[i] = lt_scale_bits<MODE>(a, kb * LT_BK + i * 16 + sc, sp);
             }
-            for (int kb = 0; kb < total; ++kb) {
+            for (int kb = k0; kb < k1; ++kb) {
                 if ((it & 1) == grp) {
                     const uint32_t at = smem_u32(smem + r.s * LT_SLOT);
-                    if (kb < nk) {
+                    if (!PRE && kb < nk) {
                         const uint32_t raw = smem_u32(smem + LT_RT + rr.s * LT_RAW);
                         bool okw = mbar_wait(&rfull[rr.s], rr.ph, status, abort_flag);
                         live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
@@ -464,7 +532,9 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                             }
                         }
                     } else {
-                        // the T tile is written here too
+                        // PRE base stages: nothing to write, but the arrival is counted, so it
+                        // must not come before the slot is free; adapter columns: both tiles
+                        // are written here
                         const bool okw = mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag);
                         live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
                     }
@@ -477,56 +547,33 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                         const int* list = a.lists + (int64_t)(t0 / BN) * LT_LIST;
                         const int cnt = ld_after(list);
                         const int t = t0 + (int)rank * half + tid;
-                        const bool row_t = tid < half;
-                        const int id = row_t && t < a.T ? __ldg(a.ids + t) : -1;
-                        int ad[8], col[8];              // adapter (-1: none) and its first column
-                        bool rest[8];
+                        const int id = tid < half && t < a.T ? __ldg(a.ids + t) : -1;
+                        const int pr = tid >> 4, pc = tid & 15;     // A_MN: row and 8 p of a piece
+                        const int p = A_MN ? p0 + pc * 8 : p0 + tid;
+                        int ad[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            ad[c] = ld_after(list + 1 + min(((kb - nk) * 8 + c) / (2 * rc), 255));
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             const int piece = (kb - nk) * 8 + c;
                             const int e = piece / (2 * rc), in = piece - e * 2 * rc;
-                            rest[c] = in >= rc;
-                            col[c] = (rest[c] ? in - rc : in) * 8;
-                            ad[c] = e < cnt ? ld_after(list + 1 + e) : -1;
+                            const int col = (in >= rc ? in - rc : in) * 8;
+                            const bool there = e < cnt;
+                            const bool pl = there && p < a.P, tl = there && id == ad[c];
+                            const uint16_t* ps =
+                                A_MN ? a.low + ((int64_t)ad[c] * a.R + col + pr) * a.P + p
+                                     : a.low + ((int64_t)ad[c] * a.P + p) * a.R + col;
+                            cp_async16(A_MN ? at + (pc >> 3) * 8192 + (8 * c + pr) * 128 +
+                                                  (((pc & 7) ^ pr) << 4)
+                                            : at + tid * 128 + ((c ^ (tid & 7)) << 4),
+                                       pl ? ps : a.low, pl);
+                            if (tid < half)
+                                cp_async16(bt + tid * 128 + ((c ^ (tid & 7)) << 4),
+                                           tl ? a.hp + (int64_t)t * 2 * a.R + in * 8 : a.hp, tl);
                         }
-                        // all loads of the P tile before the first use of one
-                        uint4 w[8];
-                        const int pr = tid >> 4, pc = tid & 15;     // A_MN: row and 8 p of a piece
-                        const int p = A_MN ? p0 + pc * 8 : p0 + tid;
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            w[c] = make_uint4(0, 0, 0, 0);
-                            if (ad[c] >= 0 && p < a.P)
-                                w[c] = ldg_keep(
-                                    A_MN ? a.low + ((int64_t)ad[c] * a.R + col[c] + pr) * a.P + p
-                                         : a.low + ((int64_t)ad[c] * a.P + p) * a.R + col[c]);
-                        }
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            if (!row_t) break;
-                            uint32_t o[4] = {0, 0, 0, 0};
-                            if (ad[c] >= 0 && id == ad[c]) {
-                                const float f = MODE == LORA_FWD ? __ldg(a.scale + id) : 1.0f;
-                                const float* hp = a.h + (int64_t)t * a.R + col[c];
-                                const float4 h0 = ld_after4(hp), h1 = ld_after4(hp + 4);
-                                const float v[8] = {h0.x * f, h0.y * f, h0.z * f, h0.w * f,
-                                                    h1.x * f, h1.y * f, h1.z * f, h1.w * f};
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    uint32_t b = bf16_bits_rn(v[j]);
-                                    if (rest[c]) b = bf16_bits_rn(v[j] - __uint_as_float(b << 16));
-                                    o[j >> 1] |= b << (16 * (j & 1));
-                                }
-                            }
-                            sts128(bt + tid * 128 + ((c ^ (tid & 7)) << 4), o[0], o[1], o[2],
-                                   o[3]);
-                        }
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            sts128(A_MN ? at + (pc >> 3) * 8192 + (8 * c + pr) * 128 +
-                                              (((pc & 7) ^ pr) << 4)
-                                        : at + tid * 128 + ((c ^ (tid & 7)) << 4),
-                                   w[c].x, w[c].y, w[c].z, w[c].w);
+                        cp_commit();
+                        cp_wait<0>();
                     }
                     // make the generic-proxy writes visible to the tensor core, then hand over
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -534,7 +581,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
                     if (lane == 0) lt_arrive(full0 + r.s * 8);
                 }
                 ++it;
-                if (kb < nk) rr.next();
+                if (!PRE && kb < nk) rr.next();
                 r.next();
             }
         }
@@ -542,91 +589,117 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1) void k_lor
         // ---------------------------------------------------------------- epilogue
         // warp w: lane quarter w % 4 of the CTA's 128 p, every other chunk of 32 t
         const int q = warp & 3, par = (warp - LT_EPI0) >> 2;
-        const uint32_t tempty0 = lt_map(smem_u32(tempty), 0);
-        int buf = 0;
-        uint32_t bph = 0;
+        const uint32_t tempty0 = lt_map(smem_u32(tempty), lead);
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        LtRing<2> rt;
         bool live = true;
-        for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1) {
-            int p0, t0;
+        for (int u = u0; u < units; u += ustep) {
+            int p0, t0, k0, k1;
             tile_of(u, p0, t0);
+            stages_of(t0, k0, k1);
             const int p = p0 + q * 32 + lane;
-            const bool low = MODE == LORA_FWD && low_stages(t0) > 0;
+            // forward: which of the two sums this pair has
+            const bool base = MODE != LORA_FWD || k0 < nk, low = MODE == LORA_FWD && k1 > nk;
             float sw = 1.0f, bs = 0.0f;
             if (MODE == LORA_FWD && p < a.P) {
                 sw = __ldg(a.s_w + p);
                 if (a.bias) bs = __ldg(a.bias + p);
             }
-            const int buf2 = buf ^ 1;
-            const uint32_t bph2 = buf == 1 ? bph ^ 1u : bph;
-            bool okw = mbar_wait(&tfull[buf], bph, status, abort_flag);
-            if (low) okw = mbar_wait(&tfull[buf2], bph2, status, abort_flag) && okw;
+            const LtRing<2> r1 = rt;
+            if (base) rt.next();
+            const LtRing<2> r2 = rt;
+            if (low) rt.next();
+            bool okw = true;
+            if (base) okw = mbar_wait(&tfull[r1.s], r1.ph, status, abort_flag);
+            if (low) okw = mbar_wait(&tfull[r2.s], r2.ph, status, abort_flag) && okw;
             live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-#pragma unroll 1
-            for (int c = par; live && c < BN / 32; c += 2) {
+            // this pair's part of 32 columns
+            auto part = [&](int c, float (&v)[32]) {
                 uint32_t r[32];
-                lt_ld32(lanes + (uint32_t)(buf * 256 + c * 32), r);
-                float v[32];
-                if (low) {
-                    uint32_t r2[32];
-                    lt_ld32(lanes + (uint32_t)(buf2 * 256 + c * 32), r2);
+                if (base) {
+                    lt_ld32(lanes + (uint32_t)(r1.s * 256 + c * 32), r);
                     lt_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        v[j] = fmaf(__uint_as_float(r[j]), sw, bs) + __uint_as_float(r2[j]);
-                } else {
-                    lt_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = MODE == LORA_FWD ? fmaf(__uint_as_float(r[j]), sw, bs)
+                        v[j] = MODE == LORA_FWD ? __uint_as_float(r[j]) * sw
                                                 : __uint_as_float(r[j]);
-                }
-                const int tc = t0 + c * 32;
-                if (MODE != LORA_WGRAD && a.out_bf16 && (a.P & 1) == 0) {
-                    // neighbouring lanes exchange, so that each stores two p of one t
-                    uint32_t* out = reinterpret_cast<uint32_t*>(a.out);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const bool od = lane & 1;
-                        const float got =
-                            __shfl_xor_sync(0xffffffffu, od ? v[j] : v[j + 1], 1);
-                        const uint32_t lo = bf16_bits_rn(od ? got : v[j]);
-                        const uint32_t hi = bf16_bits_rn(od ? v[j + 1] : got);
-                        const int64_t t = tc + j + (od ? 1 : 0);
-                        if (t < a.T && p < a.P)
-                            out[(t * a.P + (p & ~1)) >> 1] = lo | hi << 16;
-                    }
-                } else if (MODE != LORA_WGRAD && a.out_bf16) {
-                    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (tc + j < a.T && p < a.P)
-                            out[(int64_t)(tc + j) * a.P + p] = __float2bfloat16_rn(v[j]);
                 } else {
-                    float* out = reinterpret_cast<float*>(a.out) + (int64_t)tc * a.P + p;
-                    if (MODE == LORA_WGRAD && a.accumulate) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (tc + j < a.T && p < a.P) v[j] += out[(int64_t)j * a.P];
-                    }
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                }
+                if (low) {
+                    lt_ld32(lanes + (uint32_t)(r2.s * 256 + c * 32), r);
+                    lt_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
+                }
+            };
+            if (S == 1) {
+#pragma unroll 1
+                for (int c = par; live && c < BN / 32; c += 2) {
+                    float v[32];
+                    part(c, v);
+                    lt_store<MODE>(a, t0 + c * 32, p, bs, v);
+                }
+            } else {
+                // chunk c belongs to pair (c >> 1) % S; a sender's parts of an owner's chunks
+                // lie at [sender][(c >> 1) / S * 2 + (c & 1)][column][128 p] of its ring region
+                const int own = ((BN + 63) / 64 + S - 1) / S * 2;  // chunks an owner has, at most
+                const uint32_t ring = smem_u32(smem) + (uint32_t)((q * 32 + lane) * 4);
+                lt_cluster_sync();      // every pair's MMAs and copies are done: rings are free
+#pragma unroll 1
+                for (int c = par; live && c < BN / 32; c += 2) {
+                    const int o = (c >> 1) % S;
+                    if (o == pair) continue;
+                    float v[32];
+                    part(c, v);
+                    const uint32_t to =
+                        lt_map(ring + (uint32_t)((pair * own + (c >> 1) / S * 2 + (c & 1)) * 16384),
+                               (uint32_t)o * 2 + rank);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (tc + j < a.T && p < a.P) out[(int64_t)j * a.P] = v[j];
+                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + j * 512),
+                                     "f"(v[j])
+                                     : "memory");
+                }
+                lt_cluster_sync();      // all parts are there
+#pragma unroll 1
+                for (int c = par; live && c < BN / 32; c += 2) {
+                    if ((c >> 1) % S != pair) continue;
+                    float v[32], mine[32];
+                    part(c, mine);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    for (int o = 0; o < S; ++o) {
+                        const uint32_t from =
+                            ring + (uint32_t)((o * own + (c >> 1) / S * 2 + (c & 1)) * 16384);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            float w = mine[j];
+                            if (o != pair)
+                                asm volatile("ld.shared.f32 %0, [%1];"
+                                             : "=f"(w)
+                                             : "r"(from + j * 512)
+                                             : "memory");
+                            v[j] += w;
+                        }
+                    }
+                    lt_store<MODE>(a, t0 + c * 32, p, bs, v);
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-                lt_arrive(tempty0 + buf * 8);
-                if (low) lt_arrive(tempty0 + buf2 * 8);
-            }
-            if (!low) {
-                if (++buf == 2) { buf = 0; bph ^= 1u; }
-            } else {
-                bph ^= 1u;                              // two buffers further: the same one
+                if (base) lt_arrive(tempty0 + r1.s * 8);
+                if (low) lt_arrive(tempty0 + r2.s * 8);
             }
         }
+    }
+    if (S > 1 && warp < LT_EPI0) {      // the epilogue's two barriers, for the other roles
+        __syncwarp();
+        lt_cluster_sync();
+        lt_cluster_sync();
     }
 
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -649,44 +722,117 @@ size_t lora_list_bytes(int64_t T) {
     const int64_t BN = lora_tc_tile(LORA_FWD, T);
     return (size_t)((T + BN - 1) / BN) * LT_LIST * sizeof(int);
 }
-template <int MODE>
+// Pairs that split a tile's stages (a cluster): while the tiles would leave more than half of
+// the pairs idle, and each part keeps at least 4 stages.
+static int lora_tc_split(int64_t tiles, int64_t C, int num_sms) {
+    int S = 1;
+    while (S < 4 && tiles * 2 * S <= num_sms / 2 && C / LT_BK >= 4 * 2 * S) S *= 2;
+    return S;
+}
+
+template <int MODE, bool PRE>
 static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, int* status) {
     const int BN = lora_tc_tile(MODE, a.T);
     CUtensorMap pm, tm;
-    const bool okp = MODE == LORA_FWD
-                         ? make_tmap_u8_2d(&pm, a.q, a.P, a.C, LT_BK, 128, CU_TENSOR_MAP_SWIZZLE_64B)
-                         : make_tmap_u8_2d(&pm, a.q, a.C, a.P, 128, LT_BK,
-                                           CU_TENSOR_MAP_SWIZZLE_NONE);
+    bool okp;
+    if (PRE)
+        okp = MODE == LORA_FWD ? make_tmap_u8_2d(&pm, a.pre, a.P, (int64_t)a.C * 2, 128, 128,
+                                                 CU_TENSOR_MAP_SWIZZLE_128B)
+                               : make_tmap_u8_2d(&pm, a.pre, a.C, (int64_t)a.P * 2, 128, LT_BK,
+                                                 CU_TENSOR_MAP_SWIZZLE_128B);
+    else
+        okp = MODE == LORA_FWD
+                  ? make_tmap_u8_2d(&pm, a.q, a.P, a.C, LT_BK, 128, CU_TENSOR_MAP_SWIZZLE_64B)
+                  : make_tmap_u8_2d(&pm, a.q, a.C, a.P, 128, LT_BK, CU_TENSOR_MAP_SWIZZLE_NONE);
     const bool okt = MODE == LORA_WGRAD
                          ? make_tmap_u8_2d(&tm, a.t, a.C, a.T * 2, 128, LT_BK,
                                            CU_TENSOR_MAP_SWIZZLE_128B)
                          : make_tmap_u8_2d(&tm, a.t, a.T, (int64_t)a.C * 2, 128, BN / 2,
                                            CU_TENSOR_MAP_SWIZZLE_128B);
     if (!okp || !okt) return cudaErrorInvalidValue;
-    cudaError_t e = ensure_dyn_smem<k_lora_tc<MODE>>(LT_SMEM);
+    cudaError_t e = ensure_dyn_smem<k_lora_tc<MODE, PRE>>(LT_SMEM);
     if (e != cudaSuccess) return e;
-    const int64_t num_p = (a.P + 255) / 256, num_t = (a.T + BN - 1) / BN;
-    if (num_p * num_t > 0x3fffffff) return cudaErrorInvalidValue;
-    const int64_t pairs = num_p * num_t < num_sms / 2 ? num_p * num_t : num_sms / 2;
+    const int64_t num_p = (a.P + 255) / 256, num_t = (a.T + BN - 1) / BN, tiles = num_p * num_t;
+    if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
+    const int S = lora_tc_split(tiles, a.C, num_sms);
+    const int64_t clusters = S > 1 || tiles < num_sms / 2 ? tiles : num_sms / 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.gridDim = dim3((unsigned)(2 * S * clusters));
     cfg.blockDim = dim3(LT_THREADS);
     cfg.dynamicSmemBytes = LT_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2 * S;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_lora_tc<MODE, PRE>, pm, tm, a, BN, (int)num_p, (int)num_t,
+                              S, status);
+}
+
+cudaError_t launch_lora_tc(int mode, const LoraGemm& a, cudaStream_t st, int num_sms,
+                           int* status) {
+#define LT_MODE(M_) \
+    (a.pre ? launch_tc<M_, true>(a, st, num_sms, status) : launch_tc<M_, false>(a, st, num_sms, status))
+    if (mode == LORA_FWD) return LT_MODE(LORA_FWD);
+    if (mode == LORA_DGRAD) return LT_MODE(LORA_DGRAD);
+    return LT_MODE(LORA_WGRAD);
+#undef LT_MODE
+}
+
+// ------------------------------------------------------------------------- expansion
+// The int8 operand in bf16 for PRE, 16 values a thread: q (forward), s_w[c] * q rounded once
+// (dgrad), or code * 2^e.
+template <int MODE>
+__global__ __launch_bounds__(256) void k_lora_expand(const LoraGemm a, int64_t n16, int row16,
+                                                     uint16_t* __restrict__ out) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n16) return;
+    const uint4 w = ldg_stream(reinterpret_cast<const uint4*>(a.q) + i);
+    uint32_t o[8];
+    s8x4_to_bf16x2_seq(w.x, o[0], o[1]);
+    s8x4_to_bf16x2_seq(w.y, o[2], o[3]);
+    s8x4_to_bf16x2_seq(w.z, o[4], o[5]);
+    s8x4_to_bf16x2_seq(w.w, o[6], o[7]);
+    if (MODE != LORA_FWD) {
+        const int64_t c = i / row16;
+        const LtScale f = lt_scale<MODE>(lt_scale_bits<MODE>(a, (int)c, (int)(i - c * row16) * 16));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = lt_apply<MODE>(o[j], f);
+    }
+    uint4* to = reinterpret_cast<uint4*>(out) + 2 * i;
+    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// The expansion moves 3 bytes a value, the conversion inside the GEMM costs it about a fifth of
+// its time, which grows with T.
+constexpr int64_t LT_PRE_T = 1024;
+size_t lora_pre_bytes(int64_t P, int64_t C, int64_t T) {
+    return T >= LT_PRE_T ? (size_t)P * (size_t)C * 2 : 0;
+}
+cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, cudaStream_t st) {
+    const int64_t n16 = (int64_t)a.P * a.C / 16;
+    const int row16 = (mode == LORA_FWD ? a.C : a.P) / 16;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((n16 + 255) / 256));
+    cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_lora_tc<MODE>, pm, tm, a, BN, (int)num_p, (int)num_t,
-                              status);
-}
-
-cudaError_t launch_lora_tc(int mode, const LoraGemm& a, cudaStream_t st, int num_sms,
-                           int* status) {
-    if (mode == LORA_FWD) return launch_tc<LORA_FWD>(a, st, num_sms, status);
-    if (mode == LORA_DGRAD) return launch_tc<LORA_DGRAD>(a, st, num_sms, status);
-    return launch_tc<LORA_WGRAD>(a, st, num_sms, status);
+    if (mode == LORA_FWD) return cudaLaunchKernelEx(&cfg, k_lora_expand<LORA_FWD>, a, n16, row16, out);
+    if (mode == LORA_DGRAD)
+        return cudaLaunchKernelEx(&cfg, k_lora_expand<LORA_DGRAD>, a, n16, row16, out);
+    return cudaLaunchKernelEx(&cfg, k_lora_expand<LORA_WGRAD>, a, n16, row16, out);
 }
 
 }  // namespace q8

@@ -222,16 +222,26 @@ static q8_status check_adapter_pointers(const q8_adapters* ad, const int32_t* id
     return Q8_OK;
 }
 
-// Workspaces: the plan of the rows' adapters; backward, g fp32 [M, R] before it.
 // Up to 16 rows run the decode GEMV where it takes the shape; it needs the term [M, N].
 static inline bool lora_decodes(int64_t M, int64_t K) { return M <= 16 && w8a16_tma_fits(M, K); }
-static size_t lora_fwd_bytes(int64_t M, int64_t N, int64_t K) {
-    if (M <= 0) return 0;
-    return lora_decodes(M, K) ? align_up((size_t)M * (size_t)N * 4, 256) : lora_plan_bytes(M);
+// Workspaces of the GEMM forms (byte offsets): backward g fp32 [M, R]; h (or g) in two bf16
+// parts [M, 2 R]; the plan of the rows' adapters; the int8 weight in bf16, where it is expanded.
+struct LoraWs {
+    size_t g = 0, hp = 0, plan = 0, pre = 0, pre_bytes = 0, bytes = 0;
+};
+static LoraWs plan_lora(bool bwd, int64_t M, int64_t N, int64_t K, int64_t R) {
+    LoraWs w;
+    if (M <= 0) return w;
+    w.hp = bwd ? align_up((size_t)M * R * 4, 256) : 0;
+    w.plan = w.hp + align_up((size_t)M * R * 4, 256);
+    w.pre = w.plan + align_up(lora_plan_bytes(M), 256);
+    w.pre_bytes = lora_pre_bytes(N, K, M);
+    w.bytes = w.pre + w.pre_bytes;
+    return w;
 }
-static size_t lora_bwd_g_bytes(int64_t M, int64_t R) { return align_up((size_t)M * R * 4, 256); }
-static size_t lora_bwd_bytes(int64_t M, int64_t R) {
-    return M > 0 ? lora_bwd_g_bytes(M, R) + lora_plan_bytes(M) : 0;
+static size_t lora_fwd_bytes(int64_t M, int64_t N, int64_t K, int64_t R) {
+    if (M > 0 && lora_decodes(M, K)) return align_up((size_t)M * (size_t)N * 4, 256);
+    return plan_lora(false, M, N, K, R).bytes;
 }
 static inline int log2_of(int g) { return g == 32 ? 5 : g == 64 ? 6 : g == 128 ? 7 : 8; }
 
@@ -413,12 +423,13 @@ size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K, int extra) 
         case Q8_OP_GPTQ_INT8:
             if (K > kGptqMaxK || !gptq_block_ok(extra)) return 0;
             return plan_gptq(N, K).bytes;
+        case Q8_OP_CHECKPOINT_WGRAD: return M > 0 ? lora_pre_bytes(K, M, N) : 0;
         case Q8_OP_LINEAR_W8A16_LORA:
             if (M > 0x7fffffff || !valid_rank(extra)) return 0;
-            return lora_fwd_bytes(M, N, K);
+            return lora_fwd_bytes(M, N, K, extra);
         case Q8_OP_LINEAR_W8A16_LORA_BACKWARD:
             if (M > 0x7fffffff || !valid_rank(extra)) return 0;
-            return lora_bwd_bytes(M, extra);
+            return plan_lora(true, M, N, K, extra).bytes;
         case Q8_OP_LINEAR_DQ8CA_Q4GSW: {
             if (!valid_group(extra) || K % 128 != 0 || K % extra != 0) return 0;
             int sms = 0;
@@ -443,7 +454,7 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     if (!aligned16(x) || !aligned16(q) || !aligned16(y) || !aligned16(h) || !aligned4(s_w) ||
         !aligned4(bias))
         return Q8_ERR_ALIGN;
-    const size_t need = lora_fwd_bytes(M, N, K);
+    const size_t need = lora_fwd_bytes(M, N, K, ad->rank);
     if (!workspace || ws_bytes < need) return Q8_ERR_WORKSPACE;
     if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     int sms = 0;
@@ -459,9 +470,9 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
         return launched(launch_w8a16_tma((const uint16_t*)x, q, s_w, t, y, yt == Q8_BF16, M, N,
                                          (int)K, st, sms, status, true));
     }
-    Q8_TRY(launched(launch_lora_plan(ids, M, L, workspace, st)));
-    Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
-                                       ad->scale, workspace, h, M, (int)K, R, L, st, sms)));
+    const LoraWs w = plan_lora(false, M, N, K, R);
+    uint8_t* ws = (uint8_t*)workspace;
+    uint16_t* hp = (uint16_t*)(ws + w.hp);
     LoraGemm a = {};
     a.q = q;
     a.t = (const uint16_t*)x;
@@ -474,11 +485,17 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     a.T = M;
     a.ids = ids;
     a.low = (const uint16_t*)ad->b;
-    a.h = h;
-    a.scale = ad->scale;
-    a.lists = lora_plan_lists(workspace);
+    a.hp = hp;
+    a.lists = lora_plan_lists(ws + w.plan);
     a.R = R;
     a.L = L;
+    Q8_TRY(launched(launch_lora_plan(ids, M, L, ws + w.plan, st)));
+    Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
+                                       ad->scale, ws + w.plan, h, hp, M, (int)K, R, L, st, sms)));
+    if (w.pre_bytes) {
+        Q8_TRY(launched(launch_lora_expand(LORA_FWD, a, (uint16_t*)(ws + w.pre), st)));
+        a.pre = (const uint16_t*)(ws + w.pre);
+    }
     return launched(launch_lora_tc(LORA_FWD, a, st, sms, status));
 }
 
@@ -516,16 +533,18 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
     Q8_TRY(check_adapter_pointers(ad, ids));
     if (!aligned16(dy) || !aligned16(q) || !aligned16(dx) || !aligned16(h) || !aligned4(s_w))
         return Q8_ERR_ALIGN;
-    const size_t need = lora_bwd_bytes(M, R);
-    if (!workspace || ws_bytes < need) return Q8_ERR_WORKSPACE;
+    const LoraWs w = plan_lora(true, M, N, K, R);
+    if (!workspace || ws_bytes < w.bytes) return Q8_ERR_WORKSPACE;
     if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     Q8_TRY(current_device(sms, &status));
-    float* g = (float*)workspace;
-    void* plan = (uint8_t*)workspace + lora_bwd_g_bytes(M, R);
+    uint8_t* ws = (uint8_t*)workspace;
+    float* g = (float*)(ws + w.g);
+    uint16_t* hp = (uint16_t*)(ws + w.hp);
+    void* plan = ws + w.plan;
     Q8_TRY(launched(launch_lora_plan(ids, M, L, plan, st)));
     if (dx || da)
         Q8_TRY(launched(launch_lora_shrink(true, (const uint16_t*)dy, (const uint16_t*)ad->b,
-                                           ad->scale, plan, g, M, (int)N, R, L, st, sms)));
+                                           ad->scale, plan, g, hp, M, (int)N, R, L, st, sms)));
     if (dx) {
         LoraGemm a = {};
         a.q = q;
@@ -538,11 +557,14 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
         a.T = M;
         a.ids = ids;
         a.low = (const uint16_t*)ad->a;
-        a.h = g;
-        a.scale = ad->scale;
+        a.hp = hp;
         a.lists = lora_plan_lists(plan);
         a.R = R;
         a.L = L;
+        if (w.pre_bytes) {
+            Q8_TRY(launched(launch_lora_expand(LORA_DGRAD, a, (uint16_t*)(ws + w.pre), st)));
+            a.pre = (const uint16_t*)(ws + w.pre);
+        }
         Q8_TRY(launched(launch_lora_tc(LORA_DGRAD, a, st, sms, status)));
     }
     if (da)
@@ -587,7 +609,7 @@ q8_status q8_checkpoint_load(const int8_t* codes, const uint8_t* exps, int group
 
 q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t* exps, int group,
                               float* dw, int accumulate, int64_t M, int64_t N, int64_t K,
-                              void* stream) {
+                              void* workspace, size_t ws_bytes, void* stream) {
     if (!valid_group(group)) return Q8_ERR_ARG;
     if (M < 0 || M > 0x7fffffff || N < 1 || N > 0x7fffffff || N % 8) return Q8_ERR_SHAPE;
     Q8_TRY(check_k(K));
@@ -595,6 +617,9 @@ q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t
     if (M == 0 && accumulate) return Q8_OK;
     if (!dw || (M > 0 && (!dy || !codes || !exps))) return Q8_ERR_NULL;
     if (!aligned16(dw) || !aligned16(dy) || !aligned16(codes)) return Q8_ERR_ALIGN;
+    const size_t need = M > 0 ? lora_pre_bytes(K, M, N) : 0;
+    if (need && (!workspace || ws_bytes < need)) return Q8_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     int sms = 0;
     int* status = nullptr;
     Q8_TRY(current_device(sms, &status));
@@ -610,6 +635,10 @@ q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t
     a.P = (int)K;
     a.C = (int)M;
     a.T = N;
+    if (need) {
+        Q8_TRY(launched(launch_lora_expand(LORA_WGRAD, a, (uint16_t*)workspace, st)));
+        a.pre = (const uint16_t*)workspace;
+    }
     return launched(launch_lora_tc(LORA_WGRAD, a, st, sms, status));
 }
 

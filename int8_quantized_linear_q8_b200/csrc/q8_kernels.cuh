@@ -58,6 +58,17 @@ __device__ __forceinline__ uint32_t bf16_bits_rn(float v) {
     return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Loads of what an earlier kernel of a chain of programmatic dependent launches wrote: volatile,
 // so that none is moved ahead of the griddepcontrol.wait before it (a __ldg is taken to read
 // memory that never changes).
@@ -186,6 +197,7 @@ cudaError_t launch_checkpoint_load(const int8_t* codes, const uint8_t* exps, int
 enum { LORA_FWD = 0, LORA_DGRAD = 1, LORA_WGRAD = 2 };
 struct LoraGemm {
     const int8_t* q;            // int8 operand
+    const uint16_t* pre;        // its bf16 expansion (launch_lora_expand), or nullptr
     const uint16_t* t;          // bf16 operand
     const float* s_w;
     const float* bias;          // nullable
@@ -195,21 +207,20 @@ struct LoraGemm {
     int out_bf16, accumulate;
     int P, C;
     int64_t T;
-    // adapter term (ids == nullptr: none): low = b (LORA_FWD) or a (LORA_DGRAD)
+    // adapter term (LORA_WGRAD: none): low = b (LORA_FWD) or a (LORA_DGRAD)
     const int32_t* ids;
     const uint16_t* low;
-    const float* h;             // [T, R]; LORA_DGRAD: g, scale included
-    const float* scale;
+    const uint16_t* hp;         // [T, 2 R]: scale * h (LORA_DGRAD: g) in two bf16 parts
     const int* lists;           // lora_plan_lists
     int R, L;
 };
 size_t lora_plan_bytes(int64_t M);               // workspace of the plan
 const int* lora_plan_lists(const void* ws);
 cudaError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, void* ws, cudaStream_t st);
-// h (or, backward, g) of every row; ws: the plan of its ids
+// h (or, backward, g) of every row, and its two bf16 parts hp [M, 2 R]; ws: the plan of its ids
 cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, const float* scale,
-                               const void* ws, float* h, int64_t M, int C, int R, int L,
-                               cudaStream_t st, int num_sms);
+                               const void* ws, float* h, uint16_t* hp, int64_t M, int C, int R,
+                               int L, cudaStream_t st, int num_sms);
 // dB (db: x = dy, low = h) or dA (x: the layer's input, bf16, or codes with exps; low = g)
 cudaError_t launch_lora_wgrad(bool db, const void* x, const uint8_t* exps, int gshift,
                               const float* low, const float* scale, const void* ws, float* out,
@@ -220,6 +231,8 @@ cudaError_t launch_lora_wgrad(bool db, const void* x, const uint8_t* exps, int g
 // adapter list of a token tile: [0] their number, then their ids in ascending order
 constexpr int LT_LIST = 260;
 int lora_tc_tile(int mode, int64_t T);          // tokens per tile
+size_t lora_pre_bytes(int64_t P, int64_t C, int64_t T);     // of the expansion; 0: none
+cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, cudaStream_t st);
 size_t lora_list_bytes(int64_t T);
 cudaError_t launch_lora_tc(int mode, const LoraGemm& a, cudaStream_t st, int num_sms,
                            int* status);

@@ -61,6 +61,11 @@ def test_forward_refusals(L):
         assert _fwd(L, **{name: ODD4}) == q8.Q8_ERR_ALIGN, name
     for ad in (_ad(a=ODD), _ad(b=ODD), _ad(scale=ODD4)):
         assert _fwd(L, ad=ad) == q8.Q8_ERR_ALIGN
+    need = q8.q8_workspace_bytes(FWD, 40, 32, 64, 16)
+    assert need > 0
+    assert _fwd(L, M=40, wsb=need - 1) == q8.Q8_ERR_WORKSPACE
+    assert _fwd(L, M=40, ws=None) == q8.Q8_ERR_WORKSPACE
+    assert _fwd(L, M=40, ws=ODD) == q8.Q8_ERR_ALIGN
     assert _fwd(L, M=0, x=None, y=None, h=None, ids=None) == q8.Q8_OK
 
 
@@ -114,8 +119,10 @@ def test_checkpoint_refusals(L):
             assert f(**{name: ODD}) == q8.Q8_ERR_ALIGN
         assert f(M=0, **{p: None}) == q8.Q8_OK
     wg = lambda **k: (lambda c: L.q8_checkpoint_wgrad(                           # noqa: E731
-        c["dy"], c["c"], c["e"], c["G"], c["dw"], c["acc"], c["M"], c["N"], c["K"], None))(
-            dict(dict(dy=GOOD, c=GOOD, e=GOOD, G=32, dw=GOOD, acc=0, M=4, N=32, K=64), **k))
+        c["dy"], c["c"], c["e"], c["G"], c["dw"], c["acc"], c["M"], c["N"], c["K"], c["ws"],
+        c["wsb"], None))(
+            dict(dict(dy=GOOD, c=GOOD, e=GOOD, G=32, dw=GOOD, acc=0, M=4, N=32, K=64, ws=None,
+                      wsb=0), **k))
     assert wg(G=8) == q8.Q8_ERR_ARG
     for bad in (dict(N=12), dict(N=0), dict(M=-1), dict(K=48), dict(G=256)):
         assert wg(**bad) == q8.Q8_ERR_SHAPE, bad
@@ -124,6 +131,11 @@ def test_checkpoint_refusals(L):
     for name in ("dy", "c", "dw"):
         assert wg(**{name: ODD}) == q8.Q8_ERR_ALIGN
     assert wg(M=0, acc=1, dy=None) == q8.Q8_OK
+    need = q8.q8_workspace_bytes(q8.Q8_OP_CHECKPOINT_WGRAD, 256, 8192, 64)
+    assert need > 0
+    assert wg(M=256, N=8192) == q8.Q8_ERR_WORKSPACE
+    assert wg(M=256, N=8192, ws=GOOD, wsb=need - 1) == q8.Q8_ERR_WORKSPACE
+    assert wg(M=256, N=8192, ws=ODD, wsb=need) == q8.Q8_ERR_ALIGN
 
 
 def test_binding_refuses_cpu_tensors():
