@@ -12,6 +12,7 @@ Function names are the C ABI's.  Errors raise ``Q8Error`` carrying the q8_status
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -430,43 +431,73 @@ def q8_linear_w8a8_noalloc(x: torch.Tensor, first, q: torch.Tensor, wsum: torch.
 
 
 # ------------------------------------------------- low-rank adapters and 8-bit checkpoints
+# A decode call's GPU time is a few microseconds, so these wrappers keep the host's part short: one
+# test per tensor (the messages are made when it fails), addresses passed as integers, and the
+# workspace formula asked once per size.
 
 
-def _same_device(first: torch.Tensor, *tensors) -> None:
-    """Every tensor on the current device: its stream is the one the call is enqueued on."""
-    dev = first.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors are on {dev} and {t.device}")
+def _is(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], dev: int) -> int:
+    """The address of a contiguous tensor of this type and shape on the current device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return t.data_ptr()
 
 
-def _empty(shape, dtype, device, stream):
+def _device(t: torch.Tensor) -> int:
+    """Index of the current CUDA device, on which every tensor of a call has to be."""
+    return torch.cuda.current_device() if isinstance(t, torch.Tensor) and t.is_cuda else -1
+
+
+def _new(shape, dtype, dev: int, stream):
     """A new tensor that belongs to the stream the call runs on (the caching allocator
     may hand its memory on in that stream's order only)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _result(t, name, dtype, shape, device, stream):
-    if t is None:
-        return _empty(shape, dtype, device, stream)
-    _need(t, name, dtype, shape)
-    return t
+def _on(stream, dev: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(dev)
+    return torch.cuda.current_stream().cuda_stream
 
 
-def _adapters(a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, N: int, K: int):
+@functools.lru_cache(maxsize=4096)
+def _scratch_bytes(op: int, M: int, N: int, K: int, extra: int) -> int:
+    return _lib().q8_workspace_bytes(op, M, N, K, extra)
+
+
+def _scratch(ws, op: int, M: int, N: int, K: int, extra: int, dev: int, stream):
+    """(the workspace, its address, its bytes)"""
+    if ws is not None:
+        if not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the current device")
+        return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+    nbytes = _scratch_bytes(op, M, N, K, extra)
+    if nbytes == 0:
+        return None, None, 0
+    ws = _new((nbytes,), torch.uint8, dev, stream)
+    return ws, ws.data_ptr(), nbytes
+
+
+def _adapters(a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, N: int, K: int, dev: int):
     if not isinstance(a, torch.Tensor) or a.dim() != 3:
         raise ValueError("a must be 3-D [count, rank, K]")
     L, R, _ = a.shape
-    _need(a, "a", torch.bfloat16, (L, R, K))
-    _need(b, "b", torch.bfloat16, (L, N, R))
-    _need(scale, "scale", torch.float32, (L,))
-    return q8_adapters(a.data_ptr(), b.data_ptr(), scale.data_ptr(), L, R)
+    return q8_adapters(_is(a, "a", torch.bfloat16, (L, R, K), dev),
+                       _is(b, "b", torch.bfloat16, (L, N, R), dev),
+                       _is(scale, "scale", torch.float32, (L,), dev), L, R)
+
+
+def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return t.shape
 
 
 def q8_linear_w8a16_lora(x: torch.Tensor, q: torch.Tensor, s_w: torch.Tensor, a: torch.Tensor,
@@ -476,29 +507,28 @@ def q8_linear_w8a16_lora(x: torch.Tensor, q: torch.Tensor, s_w: torch.Tensor, a:
     """q8_linear_w8a16 plus each row's own low-rank adapter -> (y [M,N], h fp32 [M,rank]);
     a bf16 [count,rank,K], b bf16 [count,N,rank], scale fp32 [count], ids int32 [M] (a row
     whose id is outside [0, count) has no adapter)."""
-    M, K = x.shape
-    N = q.shape[0]
-    _need(x, "x", torch.bfloat16, (M, K))
-    _need(q, "q", torch.int8, (N, K))
-    _need(s_w, "s_w", torch.float32, (N,))
-    ad = _adapters(a, b, scale, N, K)
-    _need(ids, "ids", torch.int32, (M,))
-    if bias is not None:
-        _need(bias, "bias", torch.float32, (N,))
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    M, K = _rows(x, "x")
+    N = _rows(q, "q")[0]
+    dev = _device(x)
+    xp = _is(x, "x", torch.bfloat16, (M, K), dev)
+    qp = _is(q, "q", torch.int8, (N, K), dev)
+    sp = _is(s_w, "s_w", torch.float32, (N,), dev)
+    ad = _adapters(a, b, scale, N, K, dev)
+    ip = _is(ids, "ids", torch.int32, (M,), dev)
+    bp = None if bias is None else _is(bias, "bias", torch.float32, (N,), dev)
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    y = _result(y, "y", out_dtype, (M, N), x.device, stream)
-    h = _result(h, "h", torch.float32, (M, ad.rank), x.device, stream)
-    _same_device(x, q, s_w, a, b, scale, ids, bias, y, h, workspace)
-    nbytes = _lib().q8_workspace_bytes(Q8_OP_LINEAR_W8A16_LORA, M, N, K, ad.rank)
-    if nbytes and workspace is None:
-        workspace = _empty((nbytes,), torch.uint8, x.device, stream)
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib().q8_linear_w8a16_lora(_ptr(x), _ptr(q), _ptr(s_w), _ptr(bias), ctypes.byref(ad),
-                                       _ptr(ids), _ptr(y),
-                                       Q8_BF16 if out_dtype == torch.bfloat16 else Q8_F32,
-                                       _ptr(h), M, N, K, _ptr(workspace), wsb, _stream(stream)),
-           "q8_linear_w8a16_lora")
+    R = a.shape[1]
+    if y is None:
+        y = _new((M, N), out_dtype, dev, stream)
+    if h is None:
+        h = _new((M, R), torch.float32, dev, stream)
+    yp = _is(y, "y", out_dtype, (M, N), dev)
+    hp = _is(h, "h", torch.float32, (M, R), dev)
+    ws, wp, wsb = _scratch(workspace, Q8_OP_LINEAR_W8A16_LORA, M, N, K, R, dev, stream)
+    _check(_lib().q8_linear_w8a16_lora(xp, qp, sp, bp, ad, ip, yp,
+                                       Q8_BF16 if out_dtype is torch.bfloat16 else Q8_F32, hp, M,
+                                       N, K, wp, wsb, _on(stream, dev)), "q8_linear_w8a16_lora")
     return y, h
 
 
@@ -513,14 +543,15 @@ def q8_linear_w8a16_lora_backward(dy: torch.Tensor, q: torch.Tensor, s_w: torch.
     db fp32 [count,N,rank]), None for those not wanted.  The layer's input is x (bf16) or its
     checkpoint (codes, exps of q8_checkpoint_save); h is the forward call's.  accumulate adds
     to the given da and db."""
-    M, N = dy.shape
-    K = q.shape[1]
-    _need(dy, "dy", torch.bfloat16, (M, N))
-    _need(q, "q", torch.int8, (N, K))
-    _need(s_w, "s_w", torch.float32, (N,))
-    ad = _adapters(a, b, scale, N, K)
-    L, R = int(ad.count), int(ad.rank)
-    _need(ids, "ids", torch.int32, (M,))
+    M, N = _rows(dy, "dy")
+    K = _rows(q, "q")[1]
+    dev = _device(dy)
+    dyp = _is(dy, "dy", torch.bfloat16, (M, N), dev)
+    qp = _is(q, "q", torch.int8, (N, K), dev)
+    sp = _is(s_w, "s_w", torch.float32, (N,), dev)
+    ad = _adapters(a, b, scale, N, K, dev)
+    L, R = a.shape[0], a.shape[1]
+    ip = _is(ids, "ids", torch.int32, (M,), dev)
     want_dx, want_da, want_db = (want_dx or dx is not None, want_da or da is not None,
                                  want_db or db is not None)
     if accumulate and ((want_da and da is None) or (want_db and db is None)):
@@ -530,76 +561,75 @@ def q8_linear_w8a16_lora_backward(dy: torch.Tensor, q: torch.Tensor, s_w: torch.
         if (x is None) == (codes is None) or (codes is None) != (exps is None):
             raise ValueError("pass x, or codes and exps")
         if x is not None:
-            _need(x, "x", torch.bfloat16, (M, K))
-            saved = q8_saved_input(x.data_ptr(), None, 0)
+            saved = q8_saved_input(_is(x, "x", torch.bfloat16, (M, K), dev), None, 0)
         else:
-            saved = _saved(codes, exps, M, K)
+            saved = _saved(codes, exps, M, K, dev)
+    hp = None
     if want_db:
         if h is None:
             raise ValueError("db needs h, the forward call's second result")
-        _need(h, "h", torch.float32, (M, R))
-    dev = dy.device
-    dx = _result(dx, "dx", torch.bfloat16, (M, K), dev, stream) if want_dx else None
-    da = _result(da, "da", torch.float32, (L, R, K), dev, stream) if want_da else None
-    db = _result(db, "db", torch.float32, (L, N, R), dev, stream) if want_db else None
-    _same_device(dy, q, s_w, a, b, scale, ids, h, x, codes, exps, dx, da, db, workspace)
-    nbytes = _lib().q8_workspace_bytes(Q8_OP_LINEAR_W8A16_LORA_BACKWARD, M, N, K, R)
-    if nbytes and workspace is None:
-        workspace = _empty((nbytes,), torch.uint8, dev, stream)
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib().q8_linear_w8a16_lora_backward(
-        _ptr(dy), _ptr(q), _ptr(s_w), ctypes.byref(ad), _ptr(ids), _ptr(h), ctypes.byref(saved),
-        _ptr(dx), _ptr(da), _ptr(db), int(bool(accumulate)), M, N, K, _ptr(workspace), wsb,
-        _stream(stream)), "q8_linear_w8a16_lora_backward")
+        hp = _is(h, "h", torch.float32, (M, R), dev)
+    if want_dx and dx is None:
+        dx = _new((M, K), torch.bfloat16, dev, stream)
+    if want_da and da is None:
+        da = _new((L, R, K), torch.float32, dev, stream)
+    if want_db and db is None:
+        db = _new((L, N, R), torch.float32, dev, stream)
+    dxp = _is(dx, "dx", torch.bfloat16, (M, K), dev) if want_dx else None
+    dap = _is(da, "da", torch.float32, (L, R, K), dev) if want_da else None
+    dbp = _is(db, "db", torch.float32, (L, N, R), dev) if want_db else None
+    ws, wp, wsb = _scratch(workspace, Q8_OP_LINEAR_W8A16_LORA_BACKWARD, M, N, K, R, dev, stream)
+    _check(_lib().q8_linear_w8a16_lora_backward(dyp, qp, sp, ad, ip, hp, saved, dxp, dap, dbp,
+                                                1 if accumulate else 0, M, N, K, wp, wsb,
+                                                _on(stream, dev)),
+           "q8_linear_w8a16_lora_backward")
     return dx, da, db
 
 
-def _saved(codes: torch.Tensor, exps: torch.Tensor, M: int, K: int) -> q8_saved_input:
-    _need(codes, "codes", torch.int8, (M, K))
-    G = _group_of(exps, K)
-    _need(exps, "exps", torch.uint8, (M, K // G))
-    return q8_saved_input(codes.data_ptr(), exps.data_ptr(), G)
-
-
-def _group_of(exps: torch.Tensor, K: int) -> int:
-    if not isinstance(exps, torch.Tensor) or exps.dim() != 2 or exps.shape[1] < 1 or \
-            K % exps.shape[1]:
-        raise ValueError("exps must be 2-D [M, K / group]")
-    return K // exps.shape[1]
+def _saved(codes: torch.Tensor, exps: torch.Tensor, M: int, K: int, dev: int) -> q8_saved_input:
+    groups = _rows(exps, "exps")[1]
+    if groups < 1 or K % groups:
+        raise ValueError("exps must be [M, K / group]")
+    return q8_saved_input(_is(codes, "codes", torch.int8, (M, K), dev),
+                          _is(exps, "exps", torch.uint8, (M, groups), dev), K // groups)
 
 
 def q8_checkpoint_save(x: torch.Tensor, group: int = 128, codes=None, exps=None, stream=None):
     """8-bit checkpoint of a bf16 or fp32 [M, K] activation -> (codes int8 [M,K], exponent
     bytes uint8 [M, K/group]); a code counts steps of 2^(byte - 127)."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError("x must be 2-D [M, K]")
-    M, K = x.shape
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    M, K = _rows(x, "x")
+    dev = _device(x)
+    bf16 = x.dtype is torch.bfloat16
+    if not bf16 and x.dtype is not torch.float32:
         raise ValueError("x must be bfloat16 or float32")
-    _need(x, "x", x.dtype, (M, K))
+    xp = _is(x, "x", x.dtype, (M, K), dev)
     if group not in (32, 64, 128, 256) or K % group:
         raise ValueError("group must be 32, 64, 128 or 256 and divide K")
-    codes = _result(codes, "codes", torch.int8, (M, K), x.device, stream)
-    exps = _result(exps, "exps", torch.uint8, (M, K // group), x.device, stream)
-    _same_device(x, codes, exps)
-    _check(_lib().q8_checkpoint_save(_ptr(x), Q8_BF16 if x.dtype == torch.bfloat16 else Q8_F32,
-                                     M, K, int(group), _ptr(codes), _ptr(exps),
-                                     _stream(stream)), "q8_checkpoint_save")
+    if codes is None:
+        codes = _new((M, K), torch.int8, dev, stream)
+    if exps is None:
+        exps = _new((M, K // group), torch.uint8, dev, stream)
+    cp = _is(codes, "codes", torch.int8, (M, K), dev)
+    ep = _is(exps, "exps", torch.uint8, (M, K // group), dev)
+    _check(_lib().q8_checkpoint_save(xp, Q8_BF16 if bf16 else Q8_F32, M, K, group, cp, ep,
+                                     _on(stream, dev)), "q8_checkpoint_save")
     return codes, exps
 
 
 def q8_checkpoint_load(codes: torch.Tensor, exps: torch.Tensor, y=None,
                        out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """The values a checkpoint stands for, bf16 or fp32 [M, K] (exact in both)."""
-    M, K = codes.shape
-    saved = _saved(codes, exps, M, K)
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    M, K = _rows(codes, "codes")
+    dev = _device(codes)
+    saved = _saved(codes, exps, M, K, dev)
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    y = _result(y, "y", out_dtype, (M, K), codes.device, stream)
-    _same_device(codes, exps, y)
-    _check(_lib().q8_checkpoint_load(_ptr(codes), _ptr(exps), saved.group, _ptr(y),
-                                     Q8_BF16 if out_dtype == torch.bfloat16 else Q8_F32, M, K,
-                                     _stream(stream)), "q8_checkpoint_load")
+    if y is None:
+        y = _new((M, K), out_dtype, dev, stream)
+    yp = _is(y, "y", out_dtype, (M, K), dev)
+    _check(_lib().q8_checkpoint_load(saved.x, saved.exps, saved.group, yp,
+                                     Q8_BF16 if out_dtype is torch.bfloat16 else Q8_F32, M, K,
+                                     _on(stream, dev)), "q8_checkpoint_load")
     return y
 
 
@@ -607,21 +637,19 @@ def q8_checkpoint_wgrad(dy: torch.Tensor, codes: torch.Tensor, exps: torch.Tenso
                         accumulate: bool = False, workspace=None, stream=None) -> torch.Tensor:
     """dw [N, K] (= or, with accumulate, +=) dy^T x of a bf16 [M, N] gradient and the
     checkpoint of the layer's input x [M, K]; fp32."""
-    M, N = dy.shape
-    K = codes.shape[1]
-    _need(dy, "dy", torch.bfloat16, (M, N))
-    saved = _saved(codes, exps, M, K)
-    if accumulate and dw is None:
-        raise ValueError("accumulate adds to dw: pass it")
-    dw = _result(dw, "dw", torch.float32, (N, K), dy.device, stream)
-    _same_device(dy, codes, exps, dw, workspace)
-    nbytes = _lib().q8_workspace_bytes(Q8_OP_CHECKPOINT_WGRAD, M, N, K, 0)
-    if nbytes and workspace is None:
-        workspace = _empty((nbytes,), torch.uint8, dy.device, stream)
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib().q8_checkpoint_wgrad(_ptr(dy), _ptr(codes), _ptr(exps), saved.group, _ptr(dw),
-                                      int(bool(accumulate)), M, N, K, _ptr(workspace), wsb,
-                                      _stream(stream)),
+    M, N = _rows(dy, "dy")
+    K = _rows(codes, "codes")[1]
+    dev = _device(dy)
+    dyp = _is(dy, "dy", torch.bfloat16, (M, N), dev)
+    saved = _saved(codes, exps, M, K, dev)
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate adds to dw: pass it")
+        dw = _new((N, K), torch.float32, dev, stream)
+    dwp = _is(dw, "dw", torch.float32, (N, K), dev)
+    ws, wp, wsb = _scratch(workspace, Q8_OP_CHECKPOINT_WGRAD, M, N, K, 0, dev, stream)
+    _check(_lib().q8_checkpoint_wgrad(dyp, saved.x, saved.exps, saved.group, dwp,
+                                      1 if accumulate else 0, M, N, K, wp, wsb, _on(stream, dev)),
            "q8_checkpoint_wgrad")
     return dw
 

@@ -86,17 +86,30 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
     for (int i = tid; i <= L; i += 1024) cnt[i] = 0;
     for (int i = tid; i < 32 * (LP_KEYS + 3); i += 1024) (&part[0][0])[i] = 0;
     __syncthreads();
-    auto key_of = [&](int m) {
-        if (m >= M) return -1;
-        const int id = __ldg(ids + m);
-        return id >= 0 && id < L ? id : L;
-    };
+    // keys of eight rounds of 1024 rows at a time; they stay in registers for the second pass
+    // when there are no more
     const int rounds = (int)(((int64_t)M + 1023) / 1024);
-    for (int c = 0; c < rounds; ++c) {
-        const int64_t m = (int64_t)c * 1024 + tid;
-        const int key = m < M ? key_of((int)m) : -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, key);
-        if (key >= 0 && lane == __ffs(same) - 1) atomicAdd(&cnt[key], __popc(same));
+    int keys[8];
+    auto load_keys = [&](int c0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t m = (int64_t)(c0 + j) * 1024 + tid;
+            keys[j] = m < M ? __ldg(ids + m) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t m = (int64_t)(c0 + j) * 1024 + tid;
+            keys[j] = m >= M ? -1 : keys[j] >= 0 && keys[j] < L ? keys[j] : L;
+        }
+    };
+    for (int c0 = 0; c0 < rounds; c0 += 8) {
+        load_keys(c0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (c0 + j >= rounds) break;
+            const uint32_t same = __match_any_sync(0xffffffffu, keys[j]);
+            if (keys[j] >= 0 && lane == __ffs(same) - 1) atomicAdd(&cnt[keys[j]], __popc(same));
+        }
     }
     __syncthreads();
     // exclusive sums over the keys of rows and of blocks of rows; key 1024 follows the rest
@@ -147,24 +160,28 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
         tiles[3 * j + 2] = min(LP_ROWS, cnt[lo] - in);
     }
     __syncthreads();
-    for (int c = 0; c < rounds; ++c) {
-        const int64_t m = (int64_t)c * 1024 + tid;
-        const int key = m < M ? key_of((int)m) : -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, key);
-        const bool lead = key >= 0 && lane == __ffs(same) - 1;
-        if (lead) part[warp][key] = (uint8_t)__popc(same);
-        __syncthreads();
-        if (key >= 0) {
-            int at = pos[key] + __popc(same & ((1u << lane) - 1u));
-            for (int w = 0; w < warp; ++w) at += part[w][key];
-            perm[at] = (int)m;
+    for (int c0 = 0; c0 < rounds; c0 += 8) {
+        if (rounds > 8) load_keys(c0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (c0 + j >= rounds) break;
+            const int key = keys[j];
+            const uint32_t same = __match_any_sync(0xffffffffu, key);
+            const bool lead = key >= 0 && lane == __ffs(same) - 1;
+            if (lead) part[warp][key] = (uint8_t)__popc(same);
+            __syncthreads();
+            if (key >= 0) {
+                int at = pos[key] + __popc(same & ((1u << lane) - 1u));
+                for (int w = 0; w < warp; ++w) at += part[w][key];
+                perm[at] = (c0 + j) * 1024 + tid;
+            }
+            __syncthreads();
+            if (lead) {
+                atomicAdd(&pos[key], __popc(same));
+                part[warp][key] = 0;
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        if (lead) {
-            atomicAdd(&pos[key], __popc(same));
-            part[warp][key] = 0;
-        }
-        __syncthreads();
     }
 }
 
@@ -364,7 +381,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
 // of 32 rows: the next step's X pieces and low values wait in registers while this step's
 // MMAs run, then go to the other shared-memory buffer (8-bit codes are expanded on the way,
 // exactly).  X^T is read with transposing ldmatrix.  Clusters split the rows as above.
-//   KIND 0: dA from bf16, 1: dA from codes, 2: dB
+// One launch makes both: CTAs of dA (KIND 0: from bf16, 1: from codes) after those of dB (2).
 constexpr int LW_ROWS = 32;
 constexpr int LW_X = LW_ROWS * 256, LW_LOW = LW_ROWS * 128;    // one part (hi or rest)
 constexpr int LW_STAGE = LW_X + 2 * LW_LOW;
@@ -372,17 +389,28 @@ template <int NT>
 constexpr int lw_smem() {
     return 2 * LW_STAGE > 128 * (8 * NT + 1) * 4 ? 2 * LW_STAGE : 128 * (8 * NT + 1) * 4;
 }
+struct LoraGrad {
+    const void* X;              // [M, P]
+    const float* low;           // [M, R]
+    float* out;
+    int P;
+    int blocks;                 // CTAs along x: P tiles times parts; 0: not wanted
+};
 
 template <int NT, int KIND>
-__global__ __launch_bounds__(128) void k_lora_wgrad(
-    const void* __restrict__ X, const uint8_t* __restrict__ exps, int gshift,
-    const float* __restrict__ low, const float* __restrict__ scale, const int* __restrict__ perm,
-    const int* __restrict__ off, float* __restrict__ out, int accumulate, int P, int R, int S) {
+__device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
+                                               const uint8_t* __restrict__ exps, int gshift,
+                                               const float* __restrict__ scale,
+                                               const int* __restrict__ perm,
+                                               const int* __restrict__ off, int accumulate, int R,
+                                               int S) {
+    const void* X = q.X;
+    const float* low = q.low;
+    float* out = q.out;
+    const int P = q.P;
     extern __shared__ __align__(1024) uint8_t sm[];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int part = S > 1 ? (int)cluster_rank() : 0;
-    const int p0 = blockIdx.x / S * 128, r0 = blockIdx.y * (8 * NT), rn = min(8 * NT, R - r0);
+    const int p0 = bx / S * 128, r0 = blockIdx.y * (8 * NT), rn = min(8 * NT, R - r0);
     const int key = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int first = ld_after(off + key), total = ld_after(off + key + 1) - first;
@@ -396,10 +424,15 @@ __global__ __launch_bounds__(128) void k_lora_wgrad(
     uint4 xv[4];
     uint32_t xe = 0;
     float lv[2 * NT];
-    auto fetch = [&](int st) {
+    int row_next = 0;                               // the row after the one fetched next
+    auto look = [&](int st) {
         const int at = st * LW_ROWS + xr;
-        const bool live = at < total;
-        const int64_t m = live ? ld_after(perm + first + at) : 0;
+        row_next = at < total ? ld_after(perm + first + at) : -1;
+    };
+    auto fetch = [&](int st) {
+        const bool live = row_next >= 0;
+        const int64_t m = live ? row_next : 0;
+        if (st + 1 < s1) look(st + 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) xv[j] = make_uint4(0, 0, 0, 0);
         if (KIND == 1) {
@@ -415,10 +448,27 @@ __global__ __launch_bounds__(128) void k_lora_wgrad(
             for (int j = 0; j < 4; ++j)
                 if (live && p0 + xp + 8 * j < P) xv[j] = ldg_stream(src + 8 * j);
         }
+        // 2 NT columns, in pieces of at most 4 (rn is a multiple of 8)
 #pragma unroll
-        for (int j = 0; j < 2 * NT; ++j) {
-            const int r = (tid & 3) * 2 * NT + j;
-            lv[j] = live && r < rn ? ld_after(low + m * R + r0 + r) * f : 0.0f;
+        for (int j = 0; j < 2 * NT; ++j) lv[j] = 0.0f;
+        const int r = (tid & 3) * 2 * NT;
+        const float* lp = low + m * R + r0 + r;
+        if (NT == 1) {
+            if (live)
+                asm volatile("ld.global.v2.f32 {%0,%1}, [%2];"
+                             : "=f"(lv[0]), "=f"(lv[1])
+                             : "l"(lp)
+                             : "memory");
+        } else {
+#pragma unroll
+            for (int j = 0; j + 3 < 2 * NT; j += 4)
+                if (live && r + j < rn) {
+                    const float4 v = ld_after4(lp + j);
+                    lv[j] = v.x;
+                    lv[j + 1] = v.y;
+                    lv[j + 2] = v.z;
+                    lv[j + 3] = v.w;
+                }
         }
     };
     auto place = [&](int buf) {
@@ -462,9 +512,10 @@ __global__ __launch_bounds__(128) void k_lora_wgrad(
             uint32_t hi = 0, lo = 0;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const uint32_t b = bf16_bits_rn(lv[j + q]);
+                const float v = lv[j + q] * f;
+                const uint32_t b = bf16_bits_rn(v);
                 hi |= b << (16 * q);
-                lo |= bf16_bits_rn(lv[j + q] - __uint_as_float(b << 16)) << (16 * q);
+                lo |= bf16_bits_rn(v - __uint_as_float(b << 16)) << (16 * q);
             }
             const uint32_t at = xs + LW_X + xr * 128 + (((r >> 3) ^ (xr & 7)) << 4) + (r & 7) * 2;
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(hi) : "memory");
@@ -479,6 +530,7 @@ __global__ __launch_bounds__(128) void k_lora_wgrad(
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[a][i][j] = 0.0f;
     if (s0 < s1) {
+        look(s0);
         fetch(s0);
         place(0);
     }
@@ -536,14 +588,31 @@ __global__ __launch_bounds__(128) void k_lora_wgrad(
         const int p = lo + (KIND == 2 ? u / rn : u % wide), r = KIND == 2 ? u % rn : u / wide;
         float v = 0.0f;
         if (S > 1)
-            for (int q = 0; q < S; ++q) v += ld_peer(base + (p * LD + r) * 4, q);
+            for (int o = 0; o < S; ++o) v += ld_peer(base + (p * LD + r) * 4, o);
         else
             v = mine[p * LD + r];
-        float* o = out + (KIND == 2 ? ((int64_t)key * P + p0 + p) * R + r0 + r
+        float* to = out + (KIND == 2 ? ((int64_t)key * P + p0 + p) * R + r0 + r
                                     : ((int64_t)key * R + r0 + r) * P + p0 + p);
-        *o = accumulate ? *o + v : v;
+        *to = accumulate ? *to + v : v;
     }
-    if (S > 1) cluster_sync_all();                  // nobody leaves while its part is read
+    if (S > 1) cluster_sync_all();              // nobody leaves while its part is read
+}
+
+template <int NT, int KIND>
+__global__ __launch_bounds__(128) void k_lora_wgrad(const LoraGrad db, const LoraGrad da,
+                                                    const uint8_t* __restrict__ exps, int gshift,
+                                                    const float* __restrict__ scale,
+                                                    const int* __restrict__ perm,
+                                                    const int* __restrict__ off, int accumulate,
+                                                    int R, int S) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int bx = blockIdx.x;                      // a cluster lies in one of the two ranges
+    if (bx < db.blocks)
+        lora_grad_tile<NT, 2>(db, bx, exps, gshift, scale, perm, off, accumulate, R, S);
+    else
+        lora_grad_tile<NT, KIND>(da, bx - db.blocks, exps, gshift, scale, perm, off, accumulate,
+                                 R, S);
 }
 
 // ----------------------------------------------------------------------- host side
@@ -579,9 +648,9 @@ cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, c
     const int* tl = (const int*)(wsb + p.tiles);
     const int NT = rank_tiles(R), z = (R + 8 * NT - 1) / (8 * NT);
     const int64_t tiles = (M + LP_ROWS - 1) / LP_ROWS + (M < L + 1 ? M : L + 1);
-    // parts of the summed axis: enough CTAs for about two per SM, at least 256 of c each
+    // parts of the summed axis: as many CTAs as run at once (three per SM), at least 256 of c each
     int S = 1;
-    while (S < 8 && (M + LP_ROWS - 1) / LP_ROWS * z * S < 2 * num_sms && C / (2 * S) >= 256) S *= 2;
+    while (S < 8 && tiles * z * 2 * S <= 3 * num_sms && C / (2 * S) >= 256) S *= 2;
     const dim3 grid((unsigned)(tiles * S), z);
 #define LORA_SHRINK(NT_, B_)                                                                  \
     do {                                                                                      \
@@ -603,31 +672,35 @@ cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, c
 #undef LORA_SHRINK_NT
 }
 
-cudaError_t launch_lora_wgrad(bool db, const void* x, const uint8_t* exps, int gshift,
-                              const float* low, const float* scale, const void* ws, float* out,
-                              int accumulate, int64_t M, int P, int R, int L, cudaStream_t st,
-                              int num_sms) {
+cudaError_t launch_lora_wgrad(const void* dy, const float* h, float* db, const void* x,
+                              const uint8_t* exps, int gshift, const float* g, float* da,
+                              const float* scale, const void* ws, int accumulate, int64_t M, int N,
+                              int K, int R, int L, cudaStream_t st, int num_sms) {
     const LoraPlan p = plan_of(M);
     const uint8_t* wsb = (const uint8_t*)ws;
     const int* perm = (const int*)(wsb + p.perm);
     const int* off = (const int*)(wsb + p.off);
     const int NT = rank_tiles(R), z = (R + 8 * NT - 1) / (8 * NT);
-    const int64_t blocks = (int64_t)((P + 127) / 128) * z * L;
-    // parts of an adapter's rows: about four CTAs per SM, at least 128 rows each if the
+    LoraGrad gb = {dy, h, db, N, db ? (N + 127) / 128 : 0};
+    LoraGrad ga = {x, g, da, K, da ? (K + 127) / 128 : 0};
+    // parts of an adapter's rows: until four CTAs per SM, at least 64 rows each if the
     // adapters share the batch evenly
     int S = 1;
-    while (S < 8 && blocks * S < 2 * num_sms && M / L / (2 * S) >= 128) S *= 2;
-    const dim3 grid((P + 127) / 128 * S, z, L);
+    while (S < 8 && (int64_t)(gb.blocks + ga.blocks) * z * L * 2 * S <= 4 * num_sms &&
+           M / L / (2 * S) >= 64)
+        S *= 2;
+    gb.blocks *= S;
+    ga.blocks *= S;
+    const dim3 grid(gb.blocks + ga.blocks, z, L);
 #define LORA_WG(NT_, K_)                                                                      \
     do {                                                                                      \
         cudaError_t e = ensure_dyn_smem<k_lora_wgrad<NT_, K_>>(lw_smem<NT_>());               \
         if (e != cudaSuccess) return e;                                                       \
-        return launch_clustered(k_lora_wgrad<NT_, K_>, grid, S, lw_smem<NT_>(), st, x, exps,  \
-                                gshift, low, scale, perm, off, out, accumulate, P, R, S);     \
+        return launch_clustered(k_lora_wgrad<NT_, K_>, grid, S, lw_smem<NT_>(), st, gb, ga,   \
+                                exps, gshift, scale, perm, off, accumulate, R, S);            \
     } while (0)
 #define LORA_WG_NT(NT_)                    \
     do {                                   \
-        if (db) LORA_WG(NT_, 2);           \
         if (exps) LORA_WG(NT_, 1);         \
         LORA_WG(NT_, 0);                   \
     } while (0)

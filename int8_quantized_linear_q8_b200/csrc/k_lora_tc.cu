@@ -614,6 +614,14 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
             if (low) okw = mbar_wait(&tfull[r2.s], r2.ph, status, abort_flag) && okw;
             live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            auto free_sums = [&]() {
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    if (base) lt_arrive(tempty0 + r1.s * 8);
+                    if (low) lt_arrive(tempty0 + r2.s * 8);
+                }
+            };
             // this pair's part of 32 columns
             auto part = [&](int c, float (&v)[32]) {
                 uint32_t r[32];
@@ -635,7 +643,41 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                     for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
                 }
             };
-            if (S == 1) {
+            bool held = true;
+            if (S == 1 && MODE != LORA_WGRAD && a.out_bf16 && (a.P & 1) == 0) {
+                // all of the warp's columns into registers, rounded and packed in pairs of t,
+                // so that the accumulators are free before the stores
+                uint32_t w[4][16];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = par + 2 * i;
+                    if (live && c < BN / 32) {
+                        float v[32];
+                        part(c, v);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2)
+                            w[i][j >> 1] = bf16_bits_rn(v[j] + bs) | bf16_bits_rn(v[j + 1] + bs) << 16;
+                    }
+                }
+                free_sums();
+                held = false;
+                uint32_t* out = reinterpret_cast<uint32_t*>(a.out);
+                const bool od = lane & 1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = par + 2 * i;
+                    if (!live || c >= BN / 32) continue;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        // neighbouring lanes exchange, so that each stores two p of one t
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, w[i][j], 1);
+                        const uint32_t two = od ? __byte_perm(got, w[i][j], 0x7632)
+                                                : __byte_perm(w[i][j], got, 0x5410);
+                        const int64_t t = t0 + c * 32 + 2 * j + (od ? 1 : 0);
+                        if (t < a.T && p < a.P) out[(t * a.P + (p & ~1)) >> 1] = two;
+                    }
+                }
+            } else if (S == 1) {
 #pragma unroll 1
                 for (int c = par; live && c < BN / 32; c += 2) {
                     float v[32];
@@ -688,12 +730,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                     lt_store<MODE>(a, t0 + c * 32, p, bs, v);
                 }
             }
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                if (base) lt_arrive(tempty0 + r1.s * 8);
-                if (low) lt_arrive(tempty0 + r2.s * 8);
-            }
+            if (held) free_sums();
         }
     }
     if (S > 1 && warp < LT_EPI0) {      // the epilogue's two barriers, for the other roles

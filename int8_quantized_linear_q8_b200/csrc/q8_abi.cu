@@ -567,13 +567,11 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
         }
         Q8_TRY(launched(launch_lora_tc(LORA_DGRAD, a, st, sms, status)));
     }
-    if (da)
-        Q8_TRY(launched(launch_lora_wgrad(false, input->x, input->group ? input->exps : nullptr,
-                                          log2_of(input->group), g, ad->scale, plan, da,
-                                          accumulate, M, (int)K, R, L, st, sms)));
-    if (db)
-        Q8_TRY(launched(launch_lora_wgrad(true, dy, nullptr, 0, h, ad->scale, plan, db, accumulate,
-                                          M, (int)N, R, L, st, sms)));
+    if (da || db)
+        Q8_TRY(launched(launch_lora_wgrad(
+            dy, h, db, da ? input->x : nullptr, da && input->group ? input->exps : nullptr,
+            da ? log2_of(input->group) : 0, g, da, ad->scale, plan, accumulate, M, (int)N, (int)K,
+            R, L, st, sms)));
     return Q8_OK;
 }
 

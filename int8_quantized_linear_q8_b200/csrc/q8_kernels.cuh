@@ -221,11 +221,11 @@ cudaError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, void* ws, cud
 cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, const float* scale,
                                const void* ws, float* h, uint16_t* hp, int64_t M, int C, int R,
                                int L, cudaStream_t st, int num_sms);
-// dB (db: x = dy, low = h) or dA (x: the layer's input, bf16, or codes with exps; low = g)
-cudaError_t launch_lora_wgrad(bool db, const void* x, const uint8_t* exps, int gshift,
-                              const float* low, const float* scale, const void* ws, float* out,
-                              int accumulate, int64_t M, int P, int R, int L, cudaStream_t st,
-                              int num_sms);
+// dB from dy and h, dA from the layer's input (bf16, or codes with exps) and g, each if wanted
+cudaError_t launch_lora_wgrad(const void* dy, const float* h, float* db, const void* x,
+                              const uint8_t* exps, int gshift, const float* g, float* da,
+                              const float* scale, const void* ws, int accumulate, int64_t M, int N,
+                              int K, int R, int L, cudaStream_t st, int num_sms);
 
 // k_lora_tc.cu
 // adapter list of a token tile: [0] their number, then their ids in ascending order
