@@ -447,7 +447,9 @@ def _is(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], dev: int) -> i
 
 def _device(t: torch.Tensor) -> int:
     """Index of the current CUDA device, on which every tensor of a call has to be."""
-    return torch.cuda.current_device() if isinstance(t, torch.Tensor) and t.is_cuda else -1
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
+    return torch.cuda.current_device()
 
 
 def _new(shape, dtype, dev: int, stream):

@@ -49,7 +49,7 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
                                                     int* __restrict__ tiles) {
     __shared__ int cnt[LP_KEYS + 1], pos[LP_KEYS + 1], tpos[LP_KEYS + 1];
     __shared__ int wsum[2][32];
-    __shared__ uint8_t part[32][LP_KEYS + 3];
+    __shared__ __align__(16) uint8_t part[32][LP_KEYS + 3];     // rows of a key in each warp
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -84,7 +84,8 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
         return;
     }
     for (int i = tid; i <= L; i += 1024) cnt[i] = 0;
-    for (int i = tid; i < 32 * (LP_KEYS + 3); i += 1024) (&part[0][0])[i] = 0;
+    for (int i = tid; i < 8 * (LP_KEYS + 3); i += 1024)
+        reinterpret_cast<uint32_t*>(&part[0][0])[i] = 0;
     __syncthreads();
     // keys of eight rounds of 1024 rows at a time; they stay in registers for the second pass
     // when there are no more
@@ -172,6 +173,7 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
             __syncthreads();
             if (key >= 0) {
                 int at = pos[key] + __popc(same & ((1u << lane) - 1u));
+#pragma unroll 8
                 for (int w = 0; w < warp; ++w) at += part[w][key];
                 perm[at] = (c0 + j) * 1024 + tid;
             }
@@ -233,10 +235,15 @@ __device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
 // axis: the CTAs of a cluster split that axis and add their parts in rank order.
 //   BWD == false: long operand x [M, C], adapter rows W[i] = A[i] [R, C] (c contiguous)
 //   BWD == true : long operand dy [M, C], W[i] = B[i] [C, R] (r contiguous), times scale[i]
-// Steps of 64 c through a ring of four shared-memory stages (cp.async, 16-byte pieces placed
-// at piece ^ (row & 7): conflict-free for the copies and for ldmatrix).
-constexpr int LSH_STAGES = 4;
-constexpr int LSH_BYTES = LSH_STAGES * 2 * 64 * 128;
+// Steps of 64 c through a ring of shared-memory stages (cp.async): 64 rows of x (128 bytes, 16-byte
+// pieces at piece ^ (row & 7)) and the adapter's piece: 8 NT rows of 128 bytes placed likewise,
+// or, backward, 64 rows of 16 NT bytes, their pieces rotated so that eight rows fill all banks.
+__host__ __device__ constexpr int lsh_stages(int nt) { return nt == 8 ? 4 : 5; }
+__host__ __device__ constexpr int lsh_stage(int nt) { return 8192 + 1024 * nt; }
+template <int NT>
+__device__ __forceinline__ uint32_t lsh_piece(int row, int pc) {       // backward
+    return (uint32_t)(row * 16 * NT + ((pc ^ ((row * NT >> 3) & (NT - 1))) << 4));
+}
 
 template <int NT, bool BWD>
 __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict__ x,
@@ -247,6 +254,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
                                                      const int* __restrict__ tiles, int C, int R,
                                                      int S, float* __restrict__ h,
                                                      uint16_t* __restrict__ hp) {
+    constexpr int LSH = lsh_stages(NT);
     extern __shared__ __align__(1024) uint8_t sm[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -272,7 +280,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
         x + (int64_t)ld_after(perm + start + (crow < rows ? crow : 0)) * C;
     const uint16_t* wmat = W + (int64_t)key * R * C;
     auto load = [&](int st, int slot) {
-        const uint32_t xs = base + slot * 16384, wsm = xs + 8192;
+        const uint32_t xs = base + slot * lsh_stage(NT), wsm = xs + 8192;
         const int c0 = st * 64;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -288,7 +296,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
             } else if (pc < NT) {
                 const int cc = c0 + crow;
                 const bool lw = cc < C && pc * 8 < rn;
-                cp_async16(wsm + crow * 128 + ((pc ^ (crow & 7)) << 4),
+                cp_async16(wsm + lsh_piece<NT>(crow, pc),
                            lw ? wmat + (int64_t)cc * R + r0 + pc * 8 : W, lw);
             }
         }
@@ -299,17 +307,17 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < LSH_STAGES - 1; ++i) {
+    for (int i = 0; i < LSH - 1; ++i) {
         if (s0 + i < s1) load(s0 + i, i);
         cp_commit();
     }
     int slot = 0;
     for (int st = s0; st < s1; ++st) {
-        cp_wait<LSH_STAGES - 2>();
+        cp_wait<LSH - 2>();
         __syncthreads();
-        if (st + LSH_STAGES - 1 < s1) load(st + LSH_STAGES - 1, (slot + LSH_STAGES - 1) % LSH_STAGES);
+        if (st + LSH - 1 < s1) load(st + LSH - 1, (slot + LSH - 1) % LSH);
         cp_commit();
-        const uint32_t xs = base + slot * 16384, wsm = xs + 8192;
+        const uint32_t xs = base + slot * lsh_stage(NT), wsm = xs + 8192;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             uint32_t a[4];
@@ -325,13 +333,13 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
                 } else {
                     const int br = k * 16 + (lane & 15);
                     const int pc = n + (NT > 1 ? lane >> 4 : 0);
-                    ldsm4_t(wsm + br * 128 + ((pc ^ (br & 7)) << 4), b);
+                    ldsm4_t(wsm + lsh_piece<NT>(br, pc), b);
                 }
                 mma_bf16_16816(acc[n], a[0], a[1], a[2], a[3], b[0], b[1]);
                 if (NT > 1) mma_bf16_16816(acc[n + (NT > 1)], a[0], a[1], a[2], a[3], b[2], b[3]);
             }
         }
-        slot = (slot + 1) % LSH_STAGES;
+        slot = (slot + 1) % LSH;
     }
     // h (or g) in fp32, and times the scale in two bf16 parts, [M, 2 R]: high, rest
     const float f = __ldg(scale + key);
@@ -378,16 +386,19 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
 // ------------------------------------------------------------------------- dA and dB
 // out[p, r] = sum over the rows m of adapter i of X[m, p] * low[m, r], for 128 p and up to
 // 8 * NT columns of the rank; X is dy (dB) or the layer's input in bf16 or 8 bits (dA).  Steps
-// of 32 rows: the next step's X pieces and low values wait in registers while this step's
-// MMAs run, then go to the other shared-memory buffer (8-bit codes are expanded on the way,
-// exactly).  X^T is read with transposing ldmatrix.  Clusters split the rows as above.
+// of 32 rows through a ring of three shared-memory stages (cp.async of the gathered rows: X as it
+// is kept, low in fp32); a step's low values become two bf16 tiles and its codes a bf16 tile
+// (exactly) in shared memory, then X^T and low are read with transposing ldmatrix.  Clusters
+// split the rows as above.
 // One launch makes both: CTAs of dA (KIND 0: from bf16, 1: from codes) after those of dB (2).
-constexpr int LW_ROWS = 32;
-constexpr int LW_X = LW_ROWS * 256, LW_LOW = LW_ROWS * 128;    // one part (hi or rest)
-constexpr int LW_STAGE = LW_X + 2 * LW_LOW;
+constexpr int LW_ROWS = 32, LW_STAGES = 3;
+constexpr int LW_X = LW_ROWS * 256, LW_LOW = LW_ROWS * 128;    // bf16 tiles: X, a part of low
+__host__ __device__ constexpr int lw_stage(int nt) { return LW_X + LW_ROWS * 32 * nt; }
+__host__ __device__ constexpr int lw_work(int nt) { return LW_STAGES * lw_stage(nt); }
 template <int NT>
 constexpr int lw_smem() {
-    return 2 * LW_STAGE > 128 * (8 * NT + 1) * 4 ? 2 * LW_STAGE : 128 * (8 * NT + 1) * 4;
+    constexpr int loop = lw_work(NT) + 2 * LW_LOW + LW_X, tile = 128 * (8 * NT + 1) * 4;
+    return loop > tile ? loop : tile;
 }
 struct LoraGrad {
     const void* X;              // [M, P]
@@ -419,108 +430,52 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
     const uint32_t base = smem_u32(sm);
     const float f = KIND == 2 && total > 0 ? __ldg(scale + key) : 1.0f;
 
-    // X: thread -> row tid >> 2, 32 p from 32 * (tid & 3); low: row tid >> 2, 2 * NT columns
-    const int xr = tid >> 2, xp = (tid & 3) * 32;
-    uint4 xv[4];
-    uint32_t xe = 0;
-    float lv[2 * NT];
-    int row_next = 0;                               // the row after the one fetched next
+    // thread: row tid >> 2 of a step, a quarter of its p, columns 2 NT (tid & 3) of its low
+    const int xr = tid >> 2, xq = tid & 3;
+    const uint32_t work = base + lw_work(NT), xwork = work + 2 * LW_LOW;
+    int row_next = -1;                              // this thread's row in the step loaded next
+    // KIND 1: the exponent bytes of the steps on their way, oldest first (a load is not waited
+    // for before the step after the one that issued it)
+    uint32_t e_in[LW_STAGES - 1];
     auto look = [&](int st) {
         const int at = st * LW_ROWS + xr;
-        row_next = at < total ? ld_after(perm + first + at) : -1;
+        row_next = st < s1 && at < total ? ld_after(perm + first + at) : -1;
     };
-    auto fetch = [&](int st) {
+    auto load = [&](int st, int slot) {             // returns the exponent byte
+        uint32_t e = 0;
+        const uint32_t xs = base + slot * lw_stage(NT), ls = xs + LW_X;
         const bool live = row_next >= 0;
         const int64_t m = live ? row_next : 0;
-        if (st + 1 < s1) look(st + 1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) xv[j] = make_uint4(0, 0, 0, 0);
+        look(st + 1);
         if (KIND == 1) {
-            const int8_t* src = reinterpret_cast<const int8_t*>(X) + m * P + p0 + xp;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (live && p0 + xp + 16 * j < P) xv[j] = ldg_stream(src + 16 * j);
-            xe = live && p0 + xp < P
-                     ? __ldg(exps + m * (P >> gshift) + ((p0 + xp) >> gshift)) : 0u;
-        } else {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(X) + m * P + p0 + xp;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (live && p0 + xp + 8 * j < P) xv[j] = ldg_stream(src + 8 * j);
-        }
-        // 2 NT columns, in pieces of at most 4 (rn is a multiple of 8)
-#pragma unroll
-        for (int j = 0; j < 2 * NT; ++j) lv[j] = 0.0f;
-        const int r = (tid & 3) * 2 * NT;
-        const float* lp = low + m * R + r0 + r;
-        if (NT == 1) {
-            if (live)
-                asm volatile("ld.global.v2.f32 {%0,%1}, [%2];"
-                             : "=f"(lv[0]), "=f"(lv[1])
-                             : "l"(lp)
-                             : "memory");
-        } else {
-#pragma unroll
-            for (int j = 0; j + 3 < 2 * NT; j += 4)
-                if (live && r + j < rn) {
-                    const float4 v = ld_after4(lp + j);
-                    lv[j] = v.x;
-                    lv[j + 1] = v.y;
-                    lv[j + 2] = v.z;
-                    lv[j + 3] = v.w;
-                }
-        }
-    };
-    auto place = [&](int buf) {
-        const uint32_t xs = base + buf * LW_STAGE;
-        // row of 256 bytes, 16-byte pieces at piece ^ (row & 7)
-        if (KIND == 1) {
-            const uint32_t e2 = xe << 7 | xe << 23;             // 2^e twice, as bf16
+            const int8_t* src = reinterpret_cast<const int8_t*>(X) + m * P + p0 + xq * 32;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const uint32_t w[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
-                uint32_t o[8];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    s8x4_to_bf16x2_seq(w[q], o[2 * q], o[2 * q + 1]);
-                    o[2 * q] = bf16x2_mulrn(o[2 * q], e2);
-                    o[2 * q + 1] = bf16x2_mulrn(o[2 * q + 1], e2);
-                }
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int pc = (tid & 3) * 4 + 2 * j + q;
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                     xs + xr * 256 + ((pc ^ (xr & 7)) << 4)),
-                                 "r"(o[4 * q]), "r"(o[4 * q + 1]), "r"(o[4 * q + 2]),
-                                 "r"(o[4 * q + 3])
-                                 : "memory");
-                }
+                const bool in = live && p0 + xq * 32 + 16 * j < P;
+                cp_async16(xs + xr * 128 + (((xq * 2 + j) ^ (xr & 7)) << 4),
+                           in ? (const void*)(src + 16 * j) : X, in);
             }
+            e = live && p0 + xq * 32 < P
+                          ? __ldg(exps + m * (P >> gshift) + ((p0 + xq * 32) >> gshift))
+                          : 0u;
         } else {
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(X) + m * P + p0 + xq * 32;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int pc = (tid & 3) * 4 + j;
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                 xs + xr * 256 + ((pc ^ (xr & 7)) << 4)),
-                             "r"(xv[j].x), "r"(xv[j].y), "r"(xv[j].z), "r"(xv[j].w)
-                             : "memory");
+                const bool in = live && p0 + xq * 32 + 8 * j < P;
+                cp_async16(xs + xr * 256 + (((xq * 4 + j) ^ (xr & 7)) << 4),
+                           in ? (const void*)(src + 8 * j) : X, in);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 2 * NT; j += 2) {
-            const int r = (tid & 3) * 2 * NT + j;
-            uint32_t hi = 0, lo = 0;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float v = lv[j + q] * f;
-                const uint32_t b = bf16_bits_rn(v);
-                hi |= b << (16 * q);
-                lo |= bf16_bits_rn(v - __uint_as_float(b << 16)) << (16 * q);
+        for (int j = 0; j < (NT + 1) / 2; ++j) {
+            const int pc = xq + 4 * j;                          // 4 columns a piece
+            if (pc < 2 * NT) {
+                const bool in = live && pc * 4 < rn;
+                cp_async16(ls + xr * 32 * NT + pc * 16, in ? low + m * R + r0 + pc * 4 : low, in);
             }
-            const uint32_t at = xs + LW_X + xr * 128 + (((r >> 3) ^ (xr & 7)) << 4) + (r & 7) * 2;
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(hi) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + LW_LOW), "r"(lo) : "memory");
         }
+        return e;
     };
     float acc[2][NT][4];
 #pragma unroll
@@ -529,16 +484,68 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[a][i][j] = 0.0f;
-    if (s0 < s1) {
-        look(s0);
-        fetch(s0);
-        place(0);
+    look(s0);
+#pragma unroll
+    for (int i = 0; i < LW_STAGES - 1; ++i) {
+        e_in[i] = s0 + i < s1 ? load(s0 + i, i) : 0u;
+        cp_commit();
     }
-    __syncthreads();
+    int slot = 0;
     for (int st = s0; st < s1; ++st) {
-        const int buf = (st - s0) & 1;
-        if (st + 1 < s1) fetch(st + 1);
-        const uint32_t xs = base + buf * LW_STAGE;
+        cp_wait<LW_STAGES - 2>();
+        __syncthreads();                            // the step is there, the work tiles are free
+        const uint32_t e = e_in[0];
+#pragma unroll
+        for (int i = 0; i + 1 < LW_STAGES - 1; ++i) e_in[i] = e_in[i + 1];
+        e_in[LW_STAGES - 2] =
+            st + LW_STAGES - 1 < s1
+                ? load(st + LW_STAGES - 1, (slot + LW_STAGES - 1) % LW_STAGES) : 0u;
+        cp_commit();
+        const uint32_t xs = base + slot * lw_stage(NT), ls = xs + LW_X;
+        if (KIND == 1) {
+            const uint32_t e2 = e << 7 | e << 23;               // 2^e twice, as bf16
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint4 c = lds128(xs + xr * 128 + (((xq * 2 + j) ^ (xr & 7)) << 4));
+                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    s8x4_to_bf16x2_seq(w[q], o[2 * q], o[2 * q + 1]);
+                    o[2 * q] = bf16x2_mulrn(o[2 * q], e2);
+                    o[2 * q + 1] = bf16x2_mulrn(o[2 * q + 1], e2);
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                     xwork + xr * 256 + (((xq * 4 + 2 * j + q) ^ (xr & 7)) << 4)),
+                                 "r"(o[4 * q]), "r"(o[4 * q + 1]), "r"(o[4 * q + 2]),
+                                 "r"(o[4 * q + 3])
+                                 : "memory");
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * NT; j += 2) {
+            const int r = xq * 2 * NT + j;
+            float v[2];
+            asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
+                         : "=f"(v[0]), "=f"(v[1])
+                         : "r"(ls + xr * 32 * NT + r * 4)
+                         : "memory");
+            uint32_t hi = 0, lo = 0;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float u = v[q] * f;
+                const uint32_t b = bf16_bits_rn(u);
+                hi |= b << (16 * q);
+                lo |= bf16_bits_rn(u - __uint_as_float(b << 16)) << (16 * q);
+            }
+            const uint32_t to = work + xr * 128 + (((r >> 3) ^ (xr & 7)) << 4) + (r & 7) * 2;
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(hi) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + LW_LOW), "r"(lo) : "memory");
+        }
+        __syncthreads();
+        const uint32_t xt = KIND == 1 ? xwork : xs;
 #pragma unroll
         for (int k = 0; k < LW_ROWS / 16; ++k) {
             uint32_t a[2][4];
@@ -548,7 +555,7 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
                 // (m 8-15, p 0-7), (m 8-15, p 8-15), each transposed
                 const int m = k * 16 + (lane & 7) + ((lane >> 4) << 3);
                 const int pc = warp * 4 + q * 2 + ((lane >> 3) & 1);
-                ldsm4_t(xs + m * 256 + ((pc ^ (m & 7)) << 4), a[q]);
+                ldsm4_t(xt + m * 256 + ((pc ^ (m & 7)) << 4), a[q]);
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half)
@@ -556,7 +563,7 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
                 for (int n = 0; n < NT; n += 2) {
                     uint32_t b[4];
                     const int m = k * 16 + (lane & 15), pc = n + (NT > 1 ? lane >> 4 : 0);
-                    ldsm4_t(xs + LW_X + half * LW_LOW + m * 128 + ((pc ^ (m & 7)) << 4), b);
+                    ldsm4_t(work + half * LW_LOW + m * 128 + ((pc ^ (m & 7)) << 4), b);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         mma_bf16_16816(acc[q][n], a[q][0], a[q][1], a[q][2], a[q][3], b[0], b[1]);
@@ -566,9 +573,10 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
                     }
                 }
         }
-        if (st + 1 < s1) place(buf ^ 1);
-        __syncthreads();
+        slot = (slot + 1) % LW_STAGES;
     }
+    cp_wait<0>();
+    __syncthreads();
     // the tile in shared memory [128][8 NT + 1], added over the cluster in rank order
     constexpr int LD = 8 * NT + 1;
     float* mine = reinterpret_cast<float*>(sm);
@@ -617,7 +625,7 @@ __global__ __launch_bounds__(128) void k_lora_wgrad(const LoraGrad db, const Lor
 
 // ----------------------------------------------------------------------- host side
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_clustered(void (*k)(KArgs...), dim3 grid, int S, size_t smem,
+static cudaError_t launch_clustered(void (*k)(KArgs...), dim3 grid, int S, size_t smem, bool early,
                                     cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -626,7 +634,7 @@ static cudaError_t launch_clustered(void (*k)(KArgs...), dim3 grid, int S, size_
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = early;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = S;
     attr[1].val.clusterDim.y = 1;
@@ -635,6 +643,9 @@ static cudaError_t launch_clustered(void (*k)(KArgs...), dim3 grid, int S, size_
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
+template <int NT>
+constexpr int lsh_smem() { return lsh_stages(NT) * lsh_stage(NT); }
+static_assert(lsh_smem<1>() >= 64 * 9 * 4 && lsh_smem<8>() >= 64 * 65 * 4, "room for the parts");
 // columns of the rank per CTA, in n-tiles of 8
 static int rank_tiles(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : R <= 32 ? 4 : 8; }
 
@@ -654,9 +665,10 @@ cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, c
     const dim3 grid((unsigned)(tiles * S), z);
 #define LORA_SHRINK(NT_, B_)                                                                  \
     do {                                                                                      \
-        cudaError_t e = ensure_dyn_smem<k_lora_shrink<NT_, B_>>(LSH_BYTES);                   \
+        cudaError_t e = ensure_dyn_smem<k_lora_shrink<NT_, B_>>(lsh_smem<NT_>());                   \
         if (e != cudaSuccess) return e;                                                       \
-        return launch_clustered(k_lora_shrink<NT_, B_>, grid, S, LSH_BYTES, st, x, w, scale,  \
+        return launch_clustered(k_lora_shrink<NT_, B_>, grid, S, lsh_smem<NT_>(), true, st,   \
+                                x, w, scale,                                                  \
                                 perm, off, tl, C, R, S, h, hp);                                   \
     } while (0)
 #define LORA_SHRINK_NT(NT_)              \
@@ -683,21 +695,26 @@ cudaError_t launch_lora_wgrad(const void* dy, const float* h, float* db, const v
     const int NT = rank_tiles(R), z = (R + 8 * NT - 1) / (8 * NT);
     LoraGrad gb = {dy, h, db, N, db ? (N + 127) / 128 : 0};
     LoraGrad ga = {x, g, da, K, da ? (K + 127) / 128 : 0};
-    // parts of an adapter's rows: until four CTAs per SM, at least 64 rows each if the
+    // parts of an adapter's rows: as many CTAs as run at once, at least 64 rows each if the
     // adapters share the batch evenly
+    const int smem = NT == 1 ? lw_smem<1>() : NT == 2 ? lw_smem<2>() : NT == 4 ? lw_smem<4>()
+                                                                           : lw_smem<8>();
+    const int64_t at_once = (int64_t)(227 * 1024 / (smem + 1024)) * num_sms;
     int S = 1;
-    while (S < 8 && (int64_t)(gb.blocks + ga.blocks) * z * L * 2 * S <= 4 * num_sms &&
+    while (S < 8 && (int64_t)(gb.blocks + ga.blocks) * z * L * 2 * S <= at_once &&
            M / L / (2 * S) >= 64)
         S *= 2;
     gb.blocks *= S;
     ga.blocks *= S;
     const dim3 grid(gb.blocks + ga.blocks, z, L);
+    // Not launched early: the CTAs would gather on the first SMs that the GEMM leaves and wait
+    // there (measured: 216 us after the GEMM's end instead of 84).
 #define LORA_WG(NT_, K_)                                                                      \
     do {                                                                                      \
         cudaError_t e = ensure_dyn_smem<k_lora_wgrad<NT_, K_>>(lw_smem<NT_>());               \
         if (e != cudaSuccess) return e;                                                       \
-        return launch_clustered(k_lora_wgrad<NT_, K_>, grid, S, lw_smem<NT_>(), st, gb, ga,   \
-                                exps, gshift, scale, perm, off, accumulate, R, S);            \
+        return launch_clustered(k_lora_wgrad<NT_, K_>, grid, S, lw_smem<NT_>(), false, st,    \
+                                gb, ga, exps, gshift, scale, perm, off, accumulate, R, S);            \
     } while (0)
 #define LORA_WG_NT(NT_)                    \
     do {                                   \

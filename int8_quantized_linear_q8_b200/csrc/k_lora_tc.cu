@@ -33,9 +33,10 @@
 // stages; each owns 1 / S of the tile's columns and adds the other pairs' parts, which they
 // store in its shared memory (free by then), in pair order.
 //
-// Roles (19 warps): 0 and 2 TMA producers of the int8 and the bf16 operands; 1 tensor-memory
-// allocator and, in the pair's first CTA, MMA issuer; 3-10 converters, two groups of four
-// that take every other stage; 11-18 epilogue.  A stage is 64 of c.  Its int8 box (8 KB) has
+// Roles (15 warps): 0 and 2 TMA producers of the int8 and the bf16 operands; 1 tensor-memory
+// allocator and, in the pair's first CTA, MMA issuer; then converters, two groups of four that
+// take every other stage (PRE: one group, for the adapter columns), and four epilogue warps
+// (PRE: eight).  A stage is 64 of c.  Its int8 box (8 KB) has
 // a ring of its own, eight deep: that path is the longest (copy, conversion, MMA) and runs
 // ahead.  Its P tile and its T tile (16 KB each) share a slot of a ring of five (PRE: seven), so
 // that the issuing warp, whose own steps bound the main loop, has one barrier to wait for
@@ -52,8 +53,12 @@ __host__ __device__ constexpr int lt_slots(bool pre) { return pre ? 7 : 5; }
 constexpr int LT_SLOT = LT_A + LT_B, LT_RT = 5 * LT_SLOT;
 constexpr int LT_CTRL = LT_RT + LT_NR * LT_RAW;
 static_assert(LT_CTRL >= LT_N_MAX * LT_SLOT, "PRE uses the whole region for its slots");
-constexpr int LT_CONV = 8, LT_EPI = 8, LT_CONV0 = 3, LT_EPI0 = LT_CONV0 + LT_CONV;
-constexpr int LT_THREADS = 32 * (LT_EPI0 + LT_EPI);
+// warps: 15, which leaves each thread 128 registers (19 would leave 96, and spills)
+__host__ __device__ constexpr int lt_conv(bool pre) { return pre ? 4 : 8; }
+__host__ __device__ constexpr int lt_epi(bool pre) { return pre ? 8 : 4; }
+constexpr int LT_CONV0 = 3;
+constexpr int LT_THREADS = 32 * (LT_CONV0 + lt_conv(true) + lt_epi(true));
+static_assert(LT_THREADS == 32 * (LT_CONV0 + lt_conv(false) + lt_epi(false)), "warps");
 constexpr int LT_SMEM = LT_CTRL + 1024 + 512;
 static_assert(LT_SMEM <= 227 * 1024, "shared memory");
 
@@ -240,7 +245,8 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
     const LoraGemm a, int BN, int num_p, int num_t, int S, int* status) {
     constexpr bool A_MN = MODE != LORA_FWD;             // int8 operand with p contiguous
     constexpr bool B_MN = MODE == LORA_WGRAD;           // bf16 operand with t contiguous
-    constexpr int LT_N = lt_slots(PRE);
+    constexpr int LT_N = lt_slots(PRE), LT_CONV = lt_conv(PRE), LT_EPI = lt_epi(PRE);
+    constexpr int GROUPS = LT_CONV / 4, LT_EPI0 = LT_CONV0 + LT_CONV;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t* rfull = reinterpret_cast<uint64_t*>(smem + LT_CTRL);
@@ -285,10 +291,10 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
     if (threadIdx.x == 0) {
         for (int i = 0; i < LT_NR; ++i) {
             mbar_init(&rfull[i], 1);
-            mbar_init(&rempty[i], LT_CONV / 2);
+            mbar_init(&rempty[i], 4);
         }
         for (int i = 0; i < LT_N; ++i) {
-            mbar_init(&full[i], LT_CONV + 1);           // a group of either CTA, the copies
+            mbar_init(&full[i], 8 + 1);                 // a group of either CTA, the copies
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -459,13 +465,13 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
             const int sc = tid >> 3, sp = p0 + (tid & 7) * 16;     // this thread's first c, its p
             uint32_t nxt[4];                            // the next turn's scales
             if (A_MN && !PRE) {
-                const int kb = k0 + ((it & 1) == grp ? 0 : 1);
+                const int kb = k0 + (it % GROUPS == grp ? 0 : 1);   // GROUPS == 2 here
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     nxt[i] = lt_scale_bits<MODE>(a, kb * LT_BK + i * 16 + sc, sp);
             }
             for (int kb = k0; kb < k1; ++kb) {
-                if ((it & 1) == grp) {
+                if (it % GROUPS == grp) {
                     const uint32_t at = smem_u32(smem + r.s * LT_SLOT);
                     if (!PRE && kb < nk) {
                         const uint32_t raw = smem_u32(smem + LT_RT + rr.s * LT_RAW);
@@ -587,7 +593,8 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
         }
     } else {
         // ---------------------------------------------------------------- epilogue
-        // warp w: lane quarter w % 4 of the CTA's 128 p, every other chunk of 32 t
+        // warp w: lane quarter w % 4 of the CTA's 128 p, every CS-th chunk of 32 t
+        constexpr int CS = LT_EPI / 4;
         const int q = warp & 3, par = (warp - LT_EPI0) >> 2;
         const uint32_t tempty0 = lt_map(smem_u32(tempty), lead);
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
@@ -644,7 +651,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 }
             };
             bool held = true;
-            if (S == 1 && MODE != LORA_WGRAD && a.out_bf16 && (a.P & 1) == 0) {
+            if (PRE && S == 1 && MODE != LORA_WGRAD && a.out_bf16 && (a.P & 1) == 0) {
                 // all of the warp's columns into registers, rounded and packed in pairs of t,
                 // so that the accumulators are free before the stores
                 uint32_t w[4][16];
@@ -679,7 +686,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 }
             } else if (S == 1) {
 #pragma unroll 1
-                for (int c = par; live && c < BN / 32; c += 2) {
+                for (int c = par; live && c < BN / 32; c += CS) {
                     float v[32];
                     part(c, v);
                     lt_store<MODE>(a, t0 + c * 32, p, bs, v);
@@ -691,7 +698,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 const uint32_t ring = smem_u32(smem) + (uint32_t)((q * 32 + lane) * 4);
                 lt_cluster_sync();      // every pair's MMAs and copies are done: rings are free
 #pragma unroll 1
-                for (int c = par; live && c < BN / 32; c += 2) {
+                for (int c = par; live && c < BN / 32; c += CS) {
                     const int o = (c >> 1) % S;
                     if (o == pair) continue;
                     float v[32];
@@ -707,7 +714,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 }
                 lt_cluster_sync();      // all parts are there
 #pragma unroll 1
-                for (int c = par; live && c < BN / 32; c += 2) {
+                for (int c = par; live && c < BN / 32; c += CS) {
                     if ((c >> 1) % S != pair) continue;
                     float v[32], mine[32];
                     part(c, mine);
