@@ -190,7 +190,7 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
 cudaError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, void* ws, cudaStream_t st) {
     const LoraPlan p = plan_of(M);
     uint8_t* w = (uint8_t*)ws;
-    const int BN = lora_tc_tile(LORA_FWD, M);
+    const int BN = lora_tc_tile(M);
     const unsigned grid = 1 + (unsigned)((M + BN - 1) / BN);
     k_lora_plan<<<grid, 1024, 0, st>>>(ids, (int)M, L, BN, (int*)(w + p.lists), LT_LIST,
                                        (int*)(w + p.perm), (int*)(w + p.off),
@@ -238,7 +238,7 @@ __device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
 // Steps of 64 c through a ring of shared-memory stages (cp.async): 64 rows of x (128 bytes, 16-byte
 // pieces at piece ^ (row & 7)) and the adapter's piece: 8 NT rows of 128 bytes placed likewise,
 // or, backward, 64 rows of 16 NT bytes, their pieces rotated so that eight rows fill all banks.
-__host__ __device__ constexpr int lsh_stages(int nt) { return nt == 8 ? 4 : 5; }
+constexpr int LSH = 4;                              // stages
 __host__ __device__ constexpr int lsh_stage(int nt) { return 8192 + 1024 * nt; }
 template <int NT>
 __device__ __forceinline__ uint32_t lsh_piece(int row, int pc) {       // backward
@@ -254,7 +254,6 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
                                                      const int* __restrict__ tiles, int C, int R,
                                                      int S, float* __restrict__ h,
                                                      uint16_t* __restrict__ hp) {
-    constexpr int LSH = lsh_stages(NT);
     extern __shared__ __align__(1024) uint8_t sm[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -391,7 +390,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
 // (exactly) in shared memory, then X^T and low are read with transposing ldmatrix.  Clusters
 // split the rows as above.
 // One launch makes both: CTAs of dA (KIND 0: from bf16, 1: from codes) after those of dB (2).
-constexpr int LW_ROWS = 32, LW_STAGES = 3;
+constexpr int LW_ROWS = 32, LW_STAGES = 3, LW_THREADS = 256;
 constexpr int LW_X = LW_ROWS * 256, LW_LOW = LW_ROWS * 128;    // bf16 tiles: X, a part of low
 __host__ __device__ constexpr int lw_stage(int nt) { return LW_X + LW_ROWS * 32 * nt; }
 __host__ __device__ constexpr int lw_work(int nt) { return LW_STAGES * lw_stage(nt); }
@@ -430,8 +429,8 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
     const uint32_t base = smem_u32(sm);
     const float f = KIND == 2 && total > 0 ? __ldg(scale + key) : 1.0f;
 
-    // thread: row tid >> 2 of a step, a quarter of its p, columns 2 NT (tid & 3) of its low
-    const int xr = tid >> 2, xq = tid & 3;
+    // thread: row tid >> 3 of a step, 16 of its p, an eighth of its low
+    const int xr = tid >> 3, xq = tid & 7;
     const uint32_t work = base + lw_work(NT), xwork = work + 2 * LW_LOW;
     int row_next = -1;                              // this thread's row in the step loaded next
     // KIND 1: the exponent bytes of the steps on their way, oldest first (a load is not waited
@@ -448,28 +447,22 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
         const int64_t m = live ? row_next : 0;
         look(st + 1);
         if (KIND == 1) {
-            const int8_t* src = reinterpret_cast<const int8_t*>(X) + m * P + p0 + xq * 32;
+            const int8_t* src = reinterpret_cast<const int8_t*>(X) + m * P + p0 + xq * 16;
+            const bool in = live && p0 + xq * 16 < P;
+            cp_async16(xs + xr * 128 + ((xq ^ (xr & 7)) << 4), in ? (const void*)src : X, in);
+            e = in ? __ldg(exps + m * (P >> gshift) + ((p0 + xq * 16) >> gshift)) : 0u;
+        } else {
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(X) + m * P + p0 + xq * 16;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const bool in = live && p0 + xq * 32 + 16 * j < P;
-                cp_async16(xs + xr * 128 + (((xq * 2 + j) ^ (xr & 7)) << 4),
-                           in ? (const void*)(src + 16 * j) : X, in);
-            }
-            e = live && p0 + xq * 32 < P
-                          ? __ldg(exps + m * (P >> gshift) + ((p0 + xq * 32) >> gshift))
-                          : 0u;
-        } else {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(X) + m * P + p0 + xq * 32;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = live && p0 + xq * 32 + 8 * j < P;
-                cp_async16(xs + xr * 256 + (((xq * 4 + j) ^ (xr & 7)) << 4),
+                const bool in = live && p0 + xq * 16 + 8 * j < P;
+                cp_async16(xs + xr * 256 + (((xq * 2 + j) ^ (xr & 7)) << 4),
                            in ? (const void*)(src + 8 * j) : X, in);
             }
         }
 #pragma unroll
-        for (int j = 0; j < (NT + 1) / 2; ++j) {
-            const int pc = xq + 4 * j;                          // 4 columns a piece
+        for (int j = 0; j < (NT + 3) / 4; ++j) {
+            const int pc = xq + 8 * j;                          // 4 columns a piece
             if (pc < 2 * NT) {
                 const bool in = live && pc * 4 < rn;
                 cp_async16(ls + xr * 32 * NT + pc * 16, in ? low + m * R + r0 + pc * 4 : low, in);
@@ -477,13 +470,11 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
         }
         return e;
     };
-    float acc[2][NT][4];
+    float acc[NT][4];
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[a][i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
     look(s0);
 #pragma unroll
     for (int i = 0; i < LW_STAGES - 1; ++i) {
@@ -504,29 +495,28 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
         const uint32_t xs = base + slot * lw_stage(NT), ls = xs + LW_X;
         if (KIND == 1) {
             const uint32_t e2 = e << 7 | e << 23;               // 2^e twice, as bf16
+            const uint4 c = lds128(xs + xr * 128 + ((xq ^ (xr & 7)) << 4));
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+            uint32_t o[8];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint4 c = lds128(xs + xr * 128 + (((xq * 2 + j) ^ (xr & 7)) << 4));
-                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-                uint32_t o[8];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    s8x4_to_bf16x2_seq(w[q], o[2 * q], o[2 * q + 1]);
-                    o[2 * q] = bf16x2_mulrn(o[2 * q], e2);
-                    o[2 * q + 1] = bf16x2_mulrn(o[2 * q + 1], e2);
-                }
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                     xwork + xr * 256 + (((xq * 4 + 2 * j + q) ^ (xr & 7)) << 4)),
-                                 "r"(o[4 * q]), "r"(o[4 * q + 1]), "r"(o[4 * q + 2]),
-                                 "r"(o[4 * q + 3])
-                                 : "memory");
+            for (int q = 0; q < 4; ++q) {
+                s8x4_to_bf16x2_seq(w[q], o[2 * q], o[2 * q + 1]);
+                o[2 * q] = bf16x2_mulrn(o[2 * q], e2);
+                o[2 * q + 1] = bf16x2_mulrn(o[2 * q + 1], e2);
             }
-        }
 #pragma unroll
-        for (int j = 0; j < 2 * NT; j += 2) {
-            const int r = xq * 2 * NT + j;
+            for (int q = 0; q < 2; ++q)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                 xwork + xr * 256 + (((xq * 2 + q) ^ (xr & 7)) << 4)),
+                             "r"(o[4 * q]), "r"(o[4 * q + 1]), "r"(o[4 * q + 2]),
+                             "r"(o[4 * q + 3])
+                             : "memory");
+        }
+        // NT columns a thread (for a rank tile of 8: two, in half of the threads)
+#pragma unroll
+        for (int j = 0; j < (NT == 1 ? 2 : NT); j += 2) {
+            const int r = xq * (NT == 1 ? 2 : NT) + j;
+            if (r >= 8 * NT) break;
             float v[2];
             asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
                          : "=f"(v[0]), "=f"(v[1])
@@ -548,15 +538,12 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
         const uint32_t xt = KIND == 1 ? xwork : xs;
 #pragma unroll
         for (int k = 0; k < LW_ROWS / 16; ++k) {
-            uint32_t a[2][4];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                // stored rows m (k), 8 p a piece: matrices (m 0-7, p 0-7), (m 0-7, p 8-15),
-                // (m 8-15, p 0-7), (m 8-15, p 8-15), each transposed
-                const int m = k * 16 + (lane & 7) + ((lane >> 4) << 3);
-                const int pc = warp * 4 + q * 2 + ((lane >> 3) & 1);
-                ldsm4_t(xt + m * 256 + ((pc ^ (m & 7)) << 4), a[q]);
-            }
+            // stored rows m (k), 8 p a piece: matrices (m 0-7, p 0-7), (m 0-7, p 8-15),
+            // (m 8-15, p 0-7), (m 8-15, p 8-15), each transposed; a warp has 16 p
+            uint32_t a[4];
+            const int am = k * 16 + (lane & 7) + ((lane >> 4) << 3);
+            const int apc = warp * 2 + ((lane >> 3) & 1);
+            ldsm4_t(xt + am * 256 + ((apc ^ (am & 7)) << 4), a);
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -564,13 +551,9 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
                     uint32_t b[4];
                     const int m = k * 16 + (lane & 15), pc = n + (NT > 1 ? lane >> 4 : 0);
                     ldsm4_t(work + half * LW_LOW + m * 128 + ((pc ^ (m & 7)) << 4), b);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        mma_bf16_16816(acc[q][n], a[q][0], a[q][1], a[q][2], a[q][3], b[0], b[1]);
-                        if (NT > 1)
-                            mma_bf16_16816(acc[q][n + (NT > 1)], a[q][0], a[q][1], a[q][2],
-                                           a[q][3], b[2], b[3]);
-                    }
+                    mma_bf16_16816(acc[n], a[0], a[1], a[2], a[3], b[0], b[1]);
+                    if (NT > 1)
+                        mma_bf16_16816(acc[n + (NT > 1)], a[0], a[1], a[2], a[3], b[2], b[3]);
                 }
         }
         slot = (slot + 1) % LW_STAGES;
@@ -582,17 +565,14 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
     float* mine = reinterpret_cast<float*>(sm);
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                mine[(warp * 32 + q * 16 + g + 8 * (i >> 1)) * LD + n * 8 + 2 * t + (i & 1)] =
-                    acc[q][n][i];
+        for (int i = 0; i < 4; ++i)
+            mine[(warp * 16 + g + 8 * (i >> 1)) * LD + n * 8 + 2 * t + (i & 1)] = acc[n][i];
     if (S > 1) cluster_sync_all(); else __syncthreads();
     const int pn = min(128, P - p0), per = (pn + S - 1) / S;
     const int lo = part * per, hi = min(pn, lo + per), wide = max(hi - lo, 0);
-    for (int u = tid; u < wide * rn; u += 128) {
+    for (int u = tid; u < wide * rn; u += LW_THREADS) {
         const int p = lo + (KIND == 2 ? u / rn : u % wide), r = KIND == 2 ? u % rn : u / wide;
         float v = 0.0f;
         if (S > 1)
@@ -607,7 +587,7 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
 }
 
 template <int NT, int KIND>
-__global__ __launch_bounds__(128) void k_lora_wgrad(const LoraGrad db, const LoraGrad da,
+__global__ __launch_bounds__(LW_THREADS) void k_lora_wgrad(const LoraGrad db, const LoraGrad da,
                                                     const uint8_t* __restrict__ exps, int gshift,
                                                     const float* __restrict__ scale,
                                                     const int* __restrict__ perm,
@@ -625,11 +605,12 @@ __global__ __launch_bounds__(128) void k_lora_wgrad(const LoraGrad db, const Lor
 
 // ----------------------------------------------------------------------- host side
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_clustered(void (*k)(KArgs...), dim3 grid, int S, size_t smem, bool early,
+static cudaError_t launch_clustered(void (*k)(KArgs...), dim3 grid, int threads, int S,
+                                    size_t smem, bool early,
                                     cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -644,7 +625,7 @@ static cudaError_t launch_clustered(void (*k)(KArgs...), dim3 grid, int S, size_
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
 template <int NT>
-constexpr int lsh_smem() { return lsh_stages(NT) * lsh_stage(NT); }
+constexpr int lsh_smem() { return LSH * lsh_stage(NT); }
 static_assert(lsh_smem<1>() >= 64 * 9 * 4 && lsh_smem<8>() >= 64 * 65 * 4, "room for the parts");
 // columns of the rank per CTA, in n-tiles of 8
 static int rank_tiles(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : R <= 32 ? 4 : 8; }
@@ -659,15 +640,16 @@ cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, c
     const int* tl = (const int*)(wsb + p.tiles);
     const int NT = rank_tiles(R), z = (R + 8 * NT - 1) / (8 * NT);
     const int64_t tiles = (M + LP_ROWS - 1) / LP_ROWS + (M < L + 1 ? M : L + 1);
-    // parts of the summed axis: as many CTAs as run at once (three per SM), at least 256 of c each
+    // parts of the summed axis: as many CTAs as run at once, at least 256 of c each
+    const int64_t at_once = (int64_t)(227 * 1024 / (LSH * lsh_stage(NT) + 1024)) * num_sms;
     int S = 1;
-    while (S < 8 && tiles * z * 2 * S <= 3 * num_sms && C / (2 * S) >= 256) S *= 2;
+    while (S < 8 && tiles * z * 2 * S <= at_once && C / (2 * S) >= 256) S *= 2;
     const dim3 grid((unsigned)(tiles * S), z);
 #define LORA_SHRINK(NT_, B_)                                                                  \
     do {                                                                                      \
         cudaError_t e = ensure_dyn_smem<k_lora_shrink<NT_, B_>>(lsh_smem<NT_>());                   \
         if (e != cudaSuccess) return e;                                                       \
-        return launch_clustered(k_lora_shrink<NT_, B_>, grid, S, lsh_smem<NT_>(), true, st,   \
+        return launch_clustered(k_lora_shrink<NT_, B_>, grid, 128, S, lsh_smem<NT_>(), true, st,   \
                                 x, w, scale,                                                  \
                                 perm, off, tl, C, R, S, h, hp);                                   \
     } while (0)
@@ -713,7 +695,8 @@ cudaError_t launch_lora_wgrad(const void* dy, const float* h, float* db, const v
     do {                                                                                      \
         cudaError_t e = ensure_dyn_smem<k_lora_wgrad<NT_, K_>>(lw_smem<NT_>());               \
         if (e != cudaSuccess) return e;                                                       \
-        return launch_clustered(k_lora_wgrad<NT_, K_>, grid, S, lw_smem<NT_>(), false, st,    \
+        return launch_clustered(k_lora_wgrad<NT_, K_>, grid, LW_THREADS, S, lw_smem<NT_>(),   \
+                                false, st,                                                    \
                                 gb, ga, exps, gshift, scale, perm, off, accumulate, R, S);            \
     } while (0)
 #define LORA_WG_NT(NT_)                    \

@@ -16,7 +16,7 @@
 // each CTA holds 128 rows of P, half of the T rows, and the accumulators of its own 128 rows
 // (BN columns of tensor memory).  Against one CTA with 128 x 256 tiles this halves the shared
 // memory traffic of the T operand, which leaves room for the conversion's.  BN is the T extent
-// split evenly into tiles of at most 256, rounded up to 32.
+// split evenly into tiles of at most 256, rounded up to 32 (what a pair's MMA takes).
 //
 // The adapter term is more of the same contraction: for the adapters that the tile's tokens
 // use (a list made per tile beforehand), the rank's columns of b (or a) on the P side and of
@@ -200,9 +200,10 @@ __device__ __forceinline__ uint32_t lt_apply(uint32_t v, const LtScale& s) {
 }
 
 // ------------------------------------------------------------------------- the kernel
-// Writes 32 columns (t0 + j) of this lane's p: v + bias.  All lanes of the warp call it.
+// Writes 32 columns (t0 + j, those below t1) of this lane's p: v + bias.  All lanes of the warp
+// call it.
 template <int MODE>
-__device__ __forceinline__ void lt_store(const LoraGemm& a, int t0, int p, float bs,
+__device__ __forceinline__ void lt_store(const LoraGemm& a, int t0, int64_t t1, int p, float bs,
                                          float (&v)[32]) {
     const int lane = threadIdx.x & 31;
     if (MODE == LORA_FWD)
@@ -218,24 +219,24 @@ __device__ __forceinline__ void lt_store(const LoraGemm& a, int t0, int p, float
             const uint32_t lo = bf16_bits_rn(od ? got : v[j]);
             const uint32_t hi = bf16_bits_rn(od ? v[j + 1] : got);
             const int64_t t = t0 + j + (od ? 1 : 0);
-            if (t < a.T && p < a.P) out[(t * a.P + (p & ~1)) >> 1] = lo | hi << 16;
+            if (t < t1 && p < a.P) out[(t * a.P + (p & ~1)) >> 1] = lo | hi << 16;
         }
     } else if (MODE != LORA_WGRAD && a.out_bf16) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-            if (t0 + j < a.T && p < a.P)
+            if (t0 + j < t1 && p < a.P)
                 out[(int64_t)(t0 + j) * a.P + p] = __float2bfloat16_rn(v[j]);
     } else {
         float* out = reinterpret_cast<float*>(a.out) + (int64_t)t0 * a.P + p;
         if (MODE == LORA_WGRAD && a.accumulate) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (t0 + j < a.T && p < a.P) v[j] += out[(int64_t)j * a.P];
+                if (t0 + j < t1 && p < a.P) v[j] += out[(int64_t)j * a.P];
         }
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-            if (t0 + j < a.T && p < a.P) out[(int64_t)j * a.P] = v[j];
+            if (t0 + j < t1 && p < a.P) out[(int64_t)j * a.P] = v[j];
     }
 }
 
@@ -268,24 +269,38 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
     const int u0 = blockIdx.x / (2 * S), ustep = gridDim.x / (2 * S);
     const int nk = (a.C + LT_BK - 1) / LT_BK;
     const int half = BN >> 1;
-    // Tiles run over t first, in blocks of 16 t tiles: the pairs that run at once share both
+    // Tiles run over t first, in even blocks of at most 16 t tiles: the pairs that run at once share both
     // operands through L2 and the int8 operand is read from HBM once per block.
+    const int tblk = (num_t + (num_t + 15) / 16 - 1) / ((num_t + 15) / 16);
     auto tile_of = [&](int u, int& p0, int& t0) {
-        const int full = num_p * 16, blk = u / full, rem = u - blk * full;
-        const int tb = min(16, num_t - blk * 16);
+        const int full = num_p * tblk, blk = u / full, rem = u - blk * full;
+        const int tb = min(tblk, num_t - blk * tblk);
         p0 = rem / tb * 256 + (int)rank * 128;
-        t0 = (blk * 16 + rem % tb) * BN;
+        t0 = (blk * tblk + rem % tb) * BN;
     };
-    // A tile's stages: nk of the base sum, then those of its adapters' columns; this pair
-    // takes [k0, k1).
-    auto stages_of = [&](int t0, int& k0, int& k1) {
-        int total = nk;
-        if (MODE != LORA_WGRAD) {
-            const int cnt = ld_after(a.lists + (int64_t)(t0 / BN) * LT_LIST);
-            total += (cnt * 2 * a.R + LT_BK - 1) / LT_BK;
-        }
-        k0 = total * pair / S;
-        k1 = total * (pair + 1) / S;
+    // A tile's stages: first this pair's share of the nk of the base sum, then its share of
+    // those of the adapter columns, numbered from nk.  The latter need what the kernels before
+    // this one made (lists, hp).  The base sum does not, unless it reads the expansion: q, x and
+    // dy are older than the plan, whose launch waited for all of the stream's earlier work,
+    // so the forward and dgrad products start while h or g is still being made.
+    constexpr bool EARLY = !PRE && MODE != LORA_WGRAD;
+    struct Walk {
+        int kb, end;
+        bool low;               // in the adapter columns (or there are none)
+    };
+    auto walk = [&]() {
+        return Walk{nk * pair / S, nk * (pair + 1) / S, MODE == LORA_WGRAD};
+    };
+    auto more = [&](Walk& w, int t0) {
+        if (w.kb < w.end) return true;
+        if (w.low) return false;
+        if (EARLY) asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int cnt = ld_after(a.lists + (int64_t)(t0 / BN) * LT_LIST);
+        const int total = (cnt * 2 * a.R + LT_BK - 1) / LT_BK;
+        w.low = true;
+        w.kb = nk + total * pair / S;
+        w.end = nk + total * (pair + 1) / S;
+        return w.kb < w.end;
     };
 
     if (threadIdx.x == 0) {
@@ -318,7 +333,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *tmem_slot;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!EARLY) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == 0) {
         // ---------------------------------------------------------------- int8 producer
@@ -327,10 +342,9 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
         int it = 0;
         bool ok = true;
         for (int u = u0; u < units && ok && !PRE; u += ustep) {
-            int p0, t0, k0, k1;
+            int p0, t0;
             tile_of(u, p0, t0);
-            stages_of(t0, k0, k1);
-            for (int kb = k0; kb < min(nk, k1); ++kb) {
+            for (int kb = walk().kb; kb < walk().end; ++kb) {
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(&rempty[r.s], r.ph ^ 1u, status, abort_flag));
                 if (!ok) break;
@@ -354,15 +368,17 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
         // ---------------------------------------------------------------- bf16 producer
         if (lane == 0) tma_prefetch_desc(&tmap);
         const uint32_t full0 = lt_map(smem_u32(full), lead);
+        // bytes of both CTAs' T boxes: rows of 64 c, or boxes of 64 t
+        const uint32_t tbytes = B_MN ? (uint32_t)((half + 63) / 64) * 2u * 8192u : (uint32_t)BN * 128u;
         LtRing<LT_N> r;
         int it = 0;
         bool ok = true;
         for (int u = u0; u < units && ok; u += ustep) {
-            int p0, t0, k0, k1;
+            int p0, t0;
             tile_of(u, p0, t0);
-            stages_of(t0, k0, k1);
             const int tr = t0 + (int)rank * half;
-            for (int kb = k0; kb < k1; ++kb) {
+            for (Walk w = walk(); more(w, t0); ++w.kb) {
+                const int kb = w.kb;
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag));
                 if (!ok) break;
@@ -371,7 +387,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                         const int c0 = kb * LT_BK;
                         const uint32_t at = smem_u32(smem + r.s * LT_SLOT), bt = at + LT_A;
                         if (rank == 0)
-                            mbar_expect_tx(&full[r.s], (uint32_t)BN * 128u + (PRE ? 2 * LT_A : 0));
+                            mbar_expect_tx(&full[r.s], tbytes + (PRE ? 2 * LT_A : 0));
                         if (PRE && A_MN) {
                             lt_tma_pair(at, &pmap, p0 * 2, c0, full0 + r.s * 8);
                             lt_tma_pair(at + 8192, &pmap, (p0 + 64) * 2, c0, full0 + r.s * 8);
@@ -379,7 +395,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                             lt_tma_pair(at, &pmap, c0 * 2, p0, full0 + r.s * 8);
                         }
                         if (B_MN)
-                            for (int b = 0; b < half / 64; ++b)
+                            for (int b = 0; b < (half + 63) / 64; ++b)
                                 lt_tma_pair(bt + b * 8192, &tmap, (tr + b * 64) * 2, c0,
                                             full0 + r.s * 8);
                         else
@@ -403,17 +419,20 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
             LtRing<2> rt;
             bool ok = true, here = false;
             for (int u = u0; u < units && ok; u += ustep) {
-                int p0, t0, k0, k1;
+                int p0, t0;
                 tile_of(u, p0, t0);
-                stages_of(t0, k0, k1);
-                for (int kb = k0; kb < k1 && ok; ++kb) {
-                    const bool fresh = kb == k0 || (MODE == LORA_FWD && kb == nk);
+                bool first = true, in_low = MODE != LORA_FWD;
+                for (Walk w = walk(); ok && more(w, t0); ++w.kb) {
+                    // a sum begins: the base, or, forward, the adapter term
+                    const bool fresh = first || (w.kb >= nk && !in_low);
                     if (fresh) {
-                        if (kb > k0) {                  // base sum complete
+                        if (!first) {                   // base sum complete
                             if (lt_elect()) lt_commit(&tfull[rt.s], both);
                             __syncwarp();
                             rt.next();
+                            in_low = true;
                         }
+                        first = false;
                         ok = __all_sync(0xffffffffu,
                                         mbar_wait(&tempty[rt.s], rt.ph ^ 1u, status, abort_flag));
                         if (!ok) break;
@@ -456,31 +475,37 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
         const uint32_t full0 = lt_map(smem_u32(full), lead);
         LtRing<LT_NR> rr;
         LtRing<LT_N> r;
-        int it = 0;
+        int it = 0, pending = -1;           // slot whose adapter columns are still being copied
         bool live = true;
+        auto hand_over = [&](int slot) {
+            // make the generic-proxy writes visible to the tensor core, then hand over
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) lt_arrive(full0 + slot * 8);
+        };
         for (int u = u0; u < units; u += ustep) {
-            int p0, t0, k0, k1;
+            int p0, t0;
             tile_of(u, p0, t0);
-            stages_of(t0, k0, k1);
             const int sc = tid >> 3, sp = p0 + (tid & 7) * 16;     // this thread's first c, its p
             uint32_t nxt[4];                            // the next turn's scales
             if (A_MN && !PRE) {
-                const int kb = k0 + (it % GROUPS == grp ? 0 : 1);   // GROUPS == 2 here
+                const int kb = walk().kb + (it % GROUPS == grp ? 0 : 1);    // GROUPS == 2 here
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     nxt[i] = lt_scale_bits<MODE>(a, kb * LT_BK + i * 16 + sc, sp);
             }
-            for (int kb = k0; kb < k1; ++kb) {
+            for (Walk w = walk(); more(w, t0); ++w.kb) {
+                const int kb = w.kb;
                 if (it % GROUPS == grp) {
                     const uint32_t at = smem_u32(smem + r.s * LT_SLOT);
                     if (!PRE && kb < nk) {
                         const uint32_t raw = smem_u32(smem + LT_RT + rr.s * LT_RAW);
                         bool okw = mbar_wait(&rfull[rr.s], rr.ph, status, abort_flag);
                         live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
-                        uint4 w[4];
+                        uint4 cw[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            w[i] = A_MN ? lds128(raw + (i * 16 + sc) * 128 + (tid & 7) * 16)
+                            cw[i] = A_MN ? lds128(raw + (i * 16 + sc) * 128 + (tid & 7) * 16)
                                         : lds128(raw + tid * 64 + ((i ^ ((tid >> 1) & 3)) << 4));
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&rempty[rr.s]);      // codes in registers
@@ -499,10 +524,10 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                         uint32_t o[4][8];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            s8x4_to_bf16x2_seq(w[i].x, o[i][0], o[i][1]);
-                            s8x4_to_bf16x2_seq(w[i].y, o[i][2], o[i][3]);
-                            s8x4_to_bf16x2_seq(w[i].z, o[i][4], o[i][5]);
-                            s8x4_to_bf16x2_seq(w[i].w, o[i][6], o[i][7]);
+                            s8x4_to_bf16x2_seq(cw[i].x, o[i][0], o[i][1]);
+                            s8x4_to_bf16x2_seq(cw[i].y, o[i][2], o[i][3]);
+                            s8x4_to_bf16x2_seq(cw[i].z, o[i][4], o[i][5]);
+                            s8x4_to_bf16x2_seq(cw[i].w, o[i][6], o[i][7]);
                             if (A_MN) {
                                 const LtScale f = lt_scale<MODE>(cur[i]);
 #pragma unroll
@@ -578,17 +603,27 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                                 cp_async16(bt + tid * 128 + ((c ^ (tid & 7)) << 4),
                                            tl ? a.hp + (int64_t)t * 2 * a.R + in * 8 : a.hp, tl);
                         }
-                        cp_commit();
-                        cp_wait<0>();
                     }
-                    // make the generic-proxy writes visible to the tensor core, then hand over
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) lt_arrive(full0 + r.s * 8);
+                    if (MODE != LORA_WGRAD && kb >= nk) {
+                        // handed over a turn later, when the next copies are on their way
+                        cp_commit();
+                        if (pending >= 0) {
+                            cp_wait<1>();
+                            hand_over(pending);
+                        }
+                        pending = r.s;
+                    } else {
+                        hand_over(r.s);
+                    }
                 }
                 ++it;
                 if (!PRE && kb < nk) rr.next();
                 r.next();
+            }
+            if (pending >= 0) {
+                cp_wait<0>();
+                hand_over(pending);
+                pending = -1;
             }
         }
     } else {
@@ -601,23 +636,25 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
         LtRing<2> rt;
         bool live = true;
         for (int u = u0; u < units; u += ustep) {
-            int p0, t0, k0, k1;
+            int p0, t0;
             tile_of(u, p0, t0);
-            stages_of(t0, k0, k1);
             const int p = p0 + q * 32 + lane;
-            // forward: which of the two sums this pair has
-            const bool base = MODE != LORA_FWD || k0 < nk, low = MODE == LORA_FWD && k1 > nk;
+            const int64_t t1 = min((int64_t)t0 + BN, a.T);
+            const int chunks = (BN + 31) / 32;
+            // forward: whether this pair has an adapter term besides its base sum
+            Walk w = walk();
+            w.kb = w.end;
+            const bool low = MODE == LORA_FWD && more(w, t0);
             float sw = 1.0f, bs = 0.0f;
             if (MODE == LORA_FWD && p < a.P) {
                 sw = __ldg(a.s_w + p);
                 if (a.bias) bs = __ldg(a.bias + p);
             }
             const LtRing<2> r1 = rt;
-            if (base) rt.next();
+            rt.next();
             const LtRing<2> r2 = rt;
             if (low) rt.next();
-            bool okw = true;
-            if (base) okw = mbar_wait(&tfull[r1.s], r1.ph, status, abort_flag);
+            bool okw = mbar_wait(&tfull[r1.s], r1.ph, status, abort_flag);
             if (low) okw = mbar_wait(&tfull[r2.s], r2.ph, status, abort_flag) && okw;
             live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -625,24 +662,18 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    if (base) lt_arrive(tempty0 + r1.s * 8);
+                    lt_arrive(tempty0 + r1.s * 8);
                     if (low) lt_arrive(tempty0 + r2.s * 8);
                 }
             };
             // this pair's part of 32 columns
             auto part = [&](int c, float (&v)[32]) {
                 uint32_t r[32];
-                if (base) {
-                    lt_ld32(lanes + (uint32_t)(r1.s * 256 + c * 32), r);
-                    lt_ld_wait();
+                lt_ld32(lanes + (uint32_t)(r1.s * 256 + c * 32), r);
+                lt_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = MODE == LORA_FWD ? __uint_as_float(r[j]) * sw
-                                                : __uint_as_float(r[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                }
+                for (int j = 0; j < 32; ++j)
+                    v[j] = MODE == LORA_FWD ? __uint_as_float(r[j]) * sw : __uint_as_float(r[j]);
                 if (low) {
                     lt_ld32(lanes + (uint32_t)(r2.s * 256 + c * 32), r);
                     lt_ld_wait();
@@ -658,7 +689,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = par + 2 * i;
-                    if (live && c < BN / 32) {
+                    if (live && c < chunks) {
                         float v[32];
                         part(c, v);
 #pragma unroll
@@ -673,7 +704,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = par + 2 * i;
-                    if (!live || c >= BN / 32) continue;
+                    if (!live || c >= chunks) continue;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         // neighbouring lanes exchange, so that each stores two p of one t
@@ -681,15 +712,15 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                         const uint32_t two = od ? __byte_perm(got, w[i][j], 0x7632)
                                                 : __byte_perm(w[i][j], got, 0x5410);
                         const int64_t t = t0 + c * 32 + 2 * j + (od ? 1 : 0);
-                        if (t < a.T && p < a.P) out[(t * a.P + (p & ~1)) >> 1] = two;
+                        if (t < t1 && p < a.P) out[(t * a.P + (p & ~1)) >> 1] = two;
                     }
                 }
             } else if (S == 1) {
 #pragma unroll 1
-                for (int c = par; live && c < BN / 32; c += CS) {
+                for (int c = par; live && c < chunks; c += CS) {
                     float v[32];
                     part(c, v);
-                    lt_store<MODE>(a, t0 + c * 32, p, bs, v);
+                    lt_store<MODE>(a, t0 + c * 32, t1, p, bs, v);
                 }
             } else {
                 // chunk c belongs to pair (c >> 1) % S; a sender's parts of an owner's chunks
@@ -698,7 +729,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 const uint32_t ring = smem_u32(smem) + (uint32_t)((q * 32 + lane) * 4);
                 lt_cluster_sync();      // every pair's MMAs and copies are done: rings are free
 #pragma unroll 1
-                for (int c = par; live && c < BN / 32; c += CS) {
+                for (int c = par; live && c < chunks; c += CS) {
                     const int o = (c >> 1) % S;
                     if (o == pair) continue;
                     float v[32];
@@ -714,7 +745,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 }
                 lt_cluster_sync();      // all parts are there
 #pragma unroll 1
-                for (int c = par; live && c < BN / 32; c += CS) {
+                for (int c = par; live && c < chunks; c += CS) {
                     if ((c >> 1) % S != pair) continue;
                     float v[32], mine[32];
                     part(c, mine);
@@ -723,18 +754,22 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                     for (int o = 0; o < S; ++o) {
                         const uint32_t from =
                             ring + (uint32_t)((o * own + (c >> 1) / S * 2 + (c & 1)) * 16384);
+                        if (o == pair) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            float w = mine[j];
-                            if (o != pair)
-                                asm volatile("ld.shared.f32 %0, [%1];"
-                                             : "=f"(w)
-                                             : "r"(from + j * 512)
-                                             : "memory");
-                            v[j] += w;
+                            for (int j = 0; j < 32; ++j) v[j] += mine[j];
+                            continue;
                         }
+                        float got[32];              // all loads before the first addition
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            asm volatile("ld.shared.f32 %0, [%1];"
+                                         : "=f"(got[j])
+                                         : "r"(from + j * 512)
+                                         : "memory");
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] += got[j];
                     }
-                    lt_store<MODE>(a, t0 + c * 32, p, bs, v);
+                    lt_store<MODE>(a, t0 + c * 32, t1, p, bs, v);
                 }
             }
             if (held) free_sums();
@@ -756,27 +791,47 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
 }
 
 // ----------------------------------------------------------------------- host side
-int lora_tc_tile(int mode, int64_t T) {
+int lora_tc_tile(int64_t T) {
     const int64_t tiles = (T + 255) / 256;
-    const int step = mode == LORA_WGRAD ? 128 : 32;
-    const int64_t each = (T + tiles - 1) / tiles;
-    return (int)((each + step - 1) / step * step);
+    return (int)(((T + tiles - 1) / tiles + 31) / 32 * 32);
 }
 size_t lora_list_bytes(int64_t T) {
-    const int64_t BN = lora_tc_tile(LORA_FWD, T);
+    const int64_t BN = lora_tc_tile(T);
     return (size_t)((T + BN - 1) / BN) * LT_LIST * sizeof(int);
 }
-// Pairs that split a tile's stages (a cluster): while the tiles would leave more than half of
-// the pairs idle, and each part keeps at least 4 stages.
-static int lora_tc_split(int64_t tiles, int64_t C, int num_sms) {
-    int S = 1;
-    while (S < 4 && tiles * 2 * S <= num_sms / 2 && C / LT_BK >= 4 * 2 * S) S *= 2;
-    return S;
+
+// Clusters of 2 * S CTAs that run at once (a cluster lies in one GPC, so larger ones leave SMs
+// over), asked for once per device.
+template <int MODE, bool PRE>
+static int lora_tc_clusters(int S) {
+    static std::atomic<int> known[128][3];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
+    std::atomic<int>& k = known[dev][S >> 1];
+    int n = k.load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * S);
+    cfg.blockDim = dim3(LT_THREADS);
+    cfg.dynamicSmemBytes = LT_SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k_lora_tc<MODE, PRE>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    k.store(n, std::memory_order_relaxed);
+    return n;
 }
 
 template <int MODE, bool PRE>
 static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, int* status) {
-    const int BN = lora_tc_tile(MODE, a.T);
+    const int BN = lora_tc_tile(a.T);
     CUtensorMap pm, tm;
     bool okp;
     if (PRE)
@@ -798,8 +853,13 @@ static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, in
     if (e != cudaSuccess) return e;
     const int64_t num_p = (a.P + 255) / 256, num_t = (a.T + BN - 1) / BN, tiles = num_p * num_t;
     if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
-    const int S = lora_tc_split(tiles, a.C, num_sms);
-    const int64_t clusters = S > 1 || tiles < num_sms / 2 ? tiles : num_sms / 2;
+    // Pairs that split a tile's stages: while all clusters run at once and each part keeps at
+    // least 4 stages.
+    int S = 1;
+    while (S < 4 && tiles * 2 <= num_sms / 2 / S && a.C / LT_BK >= 4 * 2 * S &&
+           tiles <= lora_tc_clusters<MODE, PRE>(2 * S))
+        S *= 2;
+    const int64_t clusters = tiles < num_sms / 2 ? tiles : num_sms / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * S * clusters));
     cfg.blockDim = dim3(LT_THREADS);
@@ -829,30 +889,38 @@ cudaError_t launch_lora_tc(int mode, const LoraGemm& a, cudaStream_t st, int num
 }
 
 // ------------------------------------------------------------------------- expansion
-// The int8 operand in bf16 for PRE, 16 values a thread: q (forward), s_w[c] * q rounded once
+// The int8 operand in bf16 for PRE, twice 16 values a thread: q (forward), s_w[c] * q rounded once
 // (dgrad), or code * 2^e.
 template <int MODE>
 __global__ __launch_bounds__(256) void k_lora_expand(const LoraGemm a, int64_t n16, int row16,
                                                      uint16_t* __restrict__ out) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n16) return;
-    const uint4 w = ldg_stream(reinterpret_cast<const uint4*>(a.q) + i);
-    uint32_t o[8];
-    s8x4_to_bf16x2_seq(w.x, o[0], o[1]);
-    s8x4_to_bf16x2_seq(w.y, o[2], o[3]);
-    s8x4_to_bf16x2_seq(w.z, o[4], o[5]);
-    s8x4_to_bf16x2_seq(w.w, o[6], o[7]);
-    if (MODE != LORA_FWD) {
-        const int64_t c = i / row16;
-        const LtScale f = lt_scale<MODE>(lt_scale_bits<MODE>(a, (int)c, (int)(i - c * row16) * 16));
+    const int64_t i0 = (int64_t)blockIdx.x * 512 + threadIdx.x;
+    uint4 w[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = lt_apply<MODE>(o[j], f);
+    for (int u = 0; u < 2; ++u)
+        if (i0 + u * 256 < n16) w[u] = ldg_stream(reinterpret_cast<const uint4*>(a.q) + i0 + u * 256);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int64_t i = i0 + u * 256;
+        if (i >= n16) break;
+        uint32_t o[8];
+        s8x4_to_bf16x2_seq(w[u].x, o[0], o[1]);
+        s8x4_to_bf16x2_seq(w[u].y, o[2], o[3]);
+        s8x4_to_bf16x2_seq(w[u].z, o[4], o[5]);
+        s8x4_to_bf16x2_seq(w[u].w, o[6], o[7]);
+        if (MODE != LORA_FWD) {
+            const int64_t c = i / row16;
+            const LtScale f =
+                lt_scale<MODE>(lt_scale_bits<MODE>(a, (int)c, (int)(i - c * row16) * 16));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = lt_apply<MODE>(o[j], f);
+        }
+        uint4* to = reinterpret_cast<uint4*>(out) + 2 * i;
+        to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        to[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
-    uint4* to = reinterpret_cast<uint4*>(out) + 2 * i;
-    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // The expansion moves 3 bytes a value, the conversion inside the GEMM costs it about a fifth of
@@ -865,7 +933,7 @@ cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, cudaS
     const int64_t n16 = (int64_t)a.P * a.C / 16;
     const int row16 = (mode == LORA_FWD ? a.C : a.P) / 16;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((n16 + 255) / 256));
+    cfg.gridDim = dim3((unsigned)((n16 + 511) / 512));
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

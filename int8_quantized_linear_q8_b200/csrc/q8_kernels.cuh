@@ -230,7 +230,7 @@ cudaError_t launch_lora_wgrad(const void* dy, const float* h, float* db, const v
 // k_lora_tc.cu
 // adapter list of a token tile: [0] their number, then their ids in ascending order
 constexpr int LT_LIST = 260;
-int lora_tc_tile(int mode, int64_t T);          // tokens per tile
+int lora_tc_tile(int64_t T);                    // tokens per tile
 size_t lora_pre_bytes(int64_t P, int64_t C, int64_t T);     // of the expansion; 0: none
 cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, cudaStream_t st);
 size_t lora_list_bytes(int64_t T);
