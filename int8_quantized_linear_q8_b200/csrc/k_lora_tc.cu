@@ -155,6 +155,15 @@ __device__ __forceinline__ void lt_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[31])
         : "r"(taddr));
 }
+__device__ __forceinline__ void lt_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 __device__ __forceinline__ void lt_ld_wait() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -200,20 +209,20 @@ __device__ __forceinline__ uint32_t lt_apply(uint32_t v, const LtScale& s) {
 }
 
 // ------------------------------------------------------------------------- the kernel
-// Writes 32 columns (t0 + j, those below t1) of this lane's p: v + bias.  All lanes of the warp
+// Writes W columns (t0 + j, those below t1) of this lane's p: v + bias.  All lanes of the warp
 // call it.
-template <int MODE>
+template <int MODE, int W>
 __device__ __forceinline__ void lt_store(const LoraGemm& a, int t0, int64_t t1, int p, float bs,
-                                         float (&v)[32]) {
+                                         float (&v)[W]) {
     const int lane = threadIdx.x & 31;
     if (MODE == LORA_FWD)
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += bs;
+        for (int j = 0; j < W; ++j) v[j] += bs;
     if (MODE != LORA_WGRAD && a.out_bf16 && (a.P & 1) == 0) {
         // neighbouring lanes exchange, so that each stores two p of one t
         uint32_t* out = reinterpret_cast<uint32_t*>(a.out);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
+        for (int j = 0; j < W; j += 2) {
             const bool od = lane & 1;
             const float got = __shfl_xor_sync(0xffffffffu, od ? v[j] : v[j + 1], 1);
             const uint32_t lo = bf16_bits_rn(od ? got : v[j]);
@@ -224,18 +233,18 @@ __device__ __forceinline__ void lt_store(const LoraGemm& a, int t0, int64_t t1, 
     } else if (MODE != LORA_WGRAD && a.out_bf16) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < W; ++j)
             if (t0 + j < t1 && p < a.P)
                 out[(int64_t)(t0 + j) * a.P + p] = __float2bfloat16_rn(v[j]);
     } else {
         float* out = reinterpret_cast<float*>(a.out) + (int64_t)t0 * a.P + p;
         if (MODE == LORA_WGRAD && a.accumulate) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < W; ++j)
                 if (t0 + j < t1 && p < a.P) v[j] += out[(int64_t)j * a.P];
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < W; ++j)
             if (t0 + j < t1 && p < a.P) out[(int64_t)j * a.P] = v[j];
     }
 }
@@ -304,6 +313,8 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
     };
 
     if (threadIdx.x == 0) {
+        tma_prefetch_desc(&pmap);
+        tma_prefetch_desc(&tmap);
         for (int i = 0; i < LT_NR; ++i) {
             mbar_init(&rfull[i], 1);
             mbar_init(&rempty[i], 4);
@@ -337,7 +348,6 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
 
     if (warp == 0) {
         // ---------------------------------------------------------------- int8 producer
-        if (lane == 0) tma_prefetch_desc(&pmap);
         LtRing<LT_NR> r;
         int it = 0;
         bool ok = true;
@@ -366,7 +376,6 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
             mbar_drain(&rfull[i % LT_NR], (uint32_t)(i / LT_NR) & 1u, status);
     } else if (warp == 2) {
         // ---------------------------------------------------------------- bf16 producer
-        if (lane == 0) tma_prefetch_desc(&tmap);
         const uint32_t full0 = lt_map(smem_u32(full), lead);
         // bytes of both CTAs' T boxes: rows of 64 c, or boxes of 64 t
         const uint32_t tbytes = B_MN ? (uint32_t)((half + 63) / 64) * 2u * 8192u : (uint32_t)BN * 128u;
@@ -635,7 +644,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         LtRing<2> rt;
         bool live = true;
-        for (int u = u0; u < units; u += ustep) {
+        for (int u = u0; u < units && S == 1; u += ustep) {
             int p0, t0;
             tile_of(u, p0, t0);
             const int p = p0 + q * 32 + lane;
@@ -682,7 +691,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 }
             };
             bool held = true;
-            if (PRE && S == 1 && MODE != LORA_WGRAD && a.out_bf16 && (a.P & 1) == 0) {
+            if (PRE && MODE != LORA_WGRAD && a.out_bf16 && (a.P & 1) == 0) {
                 // all of the warp's columns into registers, rounded and packed in pairs of t,
                 // so that the accumulators are free before the stores
                 uint32_t w[4][16];
@@ -715,70 +724,100 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                         if (t < t1 && p < a.P) out[(t * a.P + (p & ~1)) >> 1] = two;
                     }
                 }
-            } else if (S == 1) {
-#pragma unroll 1
-                for (int c = par; live && c < chunks; c += CS) {
-                    float v[32];
-                    part(c, v);
-                    lt_store<MODE>(a, t0 + c * 32, t1, p, bs, v);
-                }
             } else {
-                // chunk c belongs to pair (c >> 1) % S; a sender's parts of an owner's chunks
-                // lie at [sender][(c >> 1) / S * 2 + (c & 1)][column][128 p] of its ring region
-                const int own = ((BN + 63) / 64 + S - 1) / S * 2;  // chunks an owner has, at most
-                const uint32_t ring = smem_u32(smem) + (uint32_t)((q * 32 + lane) * 4);
-                lt_cluster_sync();      // every pair's MMAs and copies are done: rings are free
 #pragma unroll 1
                 for (int c = par; live && c < chunks; c += CS) {
-                    const int o = (c >> 1) % S;
-                    if (o == pair) continue;
                     float v[32];
                     part(c, v);
-                    const uint32_t to =
-                        lt_map(ring + (uint32_t)((pair * own + (c >> 1) / S * 2 + (c & 1)) * 16384),
-                               (uint32_t)o * 2 + rank);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + j * 512),
-                                     "f"(v[j])
-                                     : "memory");
-                }
-                lt_cluster_sync();      // all parts are there
-#pragma unroll 1
-                for (int c = par; live && c < chunks; c += CS) {
-                    if ((c >> 1) % S != pair) continue;
-                    float v[32], mine[32];
-                    part(c, mine);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                    for (int o = 0; o < S; ++o) {
-                        const uint32_t from =
-                            ring + (uint32_t)((o * own + (c >> 1) / S * 2 + (c & 1)) * 16384);
-                        if (o == pair) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] += mine[j];
-                            continue;
-                        }
-                        float got[32];              // all loads before the first addition
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            asm volatile("ld.shared.f32 %0, [%1];"
-                                         : "=f"(got[j])
-                                         : "r"(from + j * 512)
-                                         : "memory");
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] += got[j];
-                    }
-                    lt_store<MODE>(a, t0 + c * 32, t1, p, bs, v);
+                    lt_store<MODE, 32>(a, t0 + c * 32, t1, p, bs, v);
                 }
             }
             if (held) free_sums();
         }
     }
-    if (S > 1 && warp < LT_EPI0) {      // the epilogue's two barriers, for the other roles
+    if (S > 1) {
+        // A tile of several pairs: all warps but the first three finish it.  Chunk c of 16 columns
+        // belongs to pair c % S; a sender's parts of an owner's chunks lie at [sender][c / S]
+        // [column][128 p] of the owner's ring region.  (Chunks of 16 and rolled loops: this code
+        // runs once, and fetching its instructions is what it waits for.)
         __syncwarp();
-        lt_cluster_sync();
-        lt_cluster_sync();
+        const int q = warp & 3, par = (warp - LT_CONV0) >> 2, step = (LT_CONV + LT_EPI) / 4;
+        const int chunks = BN / 16, own = (chunks + S - 1) / S;
+        const uint32_t ring = smem_u32(smem) + (uint32_t)((q * 32 + lane) * 4);
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        int p0, t0;
+        tile_of(u0, p0, t0);
+        const int p = p0 + q * 32 + lane;
+        const int64_t t1 = min((int64_t)t0 + BN, a.T);
+        float sw = 1.0f, bs = 0.0f;
+        bool low = false, live = warp >= LT_CONV0;
+        if (live) {
+            Walk w = walk();
+            w.kb = w.end;
+            low = MODE == LORA_FWD && more(w, t0);
+            if (MODE == LORA_FWD && p < a.P) {
+                sw = __ldg(a.s_w + p);
+                if (a.bias) bs = __ldg(a.bias + p);
+            }
+            bool okw = mbar_wait(&tfull[0], 0, status, abort_flag);
+            if (low) okw = mbar_wait(&tfull[1], 0, status, abort_flag) && okw;
+            live = __shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        }
+        auto part = [&](int c, float (&v)[16]) {
+            uint32_t r[16];
+            lt_ld16(lanes + (uint32_t)(c * 16), r);
+            lt_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                v[j] = MODE == LORA_FWD ? __uint_as_float(r[j]) * sw : __uint_as_float(r[j]);
+            if (low) {
+                lt_ld16(lanes + (uint32_t)(256 + c * 16), r);
+                lt_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
+            }
+        };
+        __syncwarp();
+        lt_cluster_sync();              // every pair's MMAs and copies are done: rings are free
+#pragma unroll 1
+        for (int c = par; live && c < chunks; c += step) {
+            const int o = c % S;
+            if (o == pair) continue;
+            float v[16];
+            part(c, v);
+            const uint32_t to =
+                lt_map(ring + (uint32_t)((pair * own + c / S) * 8192), (uint32_t)o * 2 + rank);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + j * 512), "f"(v[j])
+                             : "memory");
+        }
+        __syncwarp();
+        lt_cluster_sync();              // all parts are there
+#pragma unroll 1
+        for (int k = par; live && k * S + pair < chunks; k += step) {
+            const int c = k * S + pair;
+            float v[16], mine[16];
+            part(c, mine);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+#pragma unroll 1
+            for (int o = 0; o < S; ++o) {                               // in pair order
+                const uint32_t from = ring + (uint32_t)((o * own + k) * 8192);
+                float got[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    asm volatile("ld.shared.f32 %0, [%1];"
+                                 : "=f"(got[j])
+                                 : "r"(from + j * 512)
+                                 : "memory");
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] += o == pair ? mine[j] : got[j];
+            }
+            lt_store<MODE, 16>(a, t0 + c * 16, t1, p, bs, v);
+        }
+        __syncwarp();
     }
 
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -923,11 +962,13 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraGemm a, int64_t n
     }
 }
 
-// The expansion moves 3 bytes a value, the conversion inside the GEMM costs it about a fifth of
-// its time, which grows with T.
+// The expansion moves 3 bytes a value and is a launch more; the conversion inside the GEMM costs
+// about a fifth of its time, which grows with T.
 constexpr int64_t LT_PRE_T = 1024;
+constexpr double LT_PRE_FLOPS = 2e10;
 size_t lora_pre_bytes(int64_t P, int64_t C, int64_t T) {
-    return T >= LT_PRE_T ? (size_t)P * (size_t)C * 2 : 0;
+    return T >= LT_PRE_T && 2.0 * (double)P * (double)C * (double)T >= LT_PRE_FLOPS
+               ? (size_t)P * (size_t)C * 2 : 0;
 }
 cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, cudaStream_t st) {
     const int64_t n16 = (int64_t)a.P * a.C / 16;

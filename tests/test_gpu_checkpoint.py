@@ -70,7 +70,7 @@ def test_empty():
 
 WGRAD = [(1, 8, 32, 32), (2, 16, 64, 64), (7, 24, 96, 32), (63, 264, 128, 128),
          (64, 128, 256, 256), (65, 136, 352, 32), (100, 8, 4096, 64), (129, 520, 640, 128),
-         (200, 2560, 960, 64), (333, 256, 288, 32), (1000, 1032, 512, 256), (4096, 264, 384, 128)]
+         (200, 2560, 960, 64), (333, 256, 288, 32), (1000, 1032, 512, 256), (4096, 264, 384, 128), (2048, 5512, 1056, 32)]
 
 
 @pytest.mark.parametrize("M,N,K,G", WGRAD)

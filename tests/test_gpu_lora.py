@@ -58,7 +58,7 @@ FORWARD = [
     (128, 384, 256, 8, 128, "each"), (129, 200, 448, 136, 3, "runs"), (200, 96, 48, 8, 4, "none"),
     (255, 65, 96, 32, 5, "wild"), (256, 128, 128, 64, 3, "each"), (257, 1025, 144, 16, 6, "runs"),
     (333, 100, 960, 8, 3, "runs"), (513, 72, 208, 48, 20, "each"), (1000, 520, 320, 16, 1000, "each"),
-    (1300, 264, 64, 8, 1024, "each"),
+    (1300, 264, 64, 8, 1024, "each"), (2051, 2561, 2080, 16, 5, "runs"), (2048, 5120, 1024, 40, 3, "each"),
 ]
 BACKWARD = [
     (1, 16, 64, 8, 1, "each", 0), (1, 2560, 960, 8, 1, "runs", 64), (2, 8, 16, 8, 3, "each", 0),
@@ -68,6 +68,7 @@ BACKWARD = [
     (129, 200, 448, 136, 3, "runs", 64), (200, 96, 48, 8, 4, "none", 0), (255, 72, 96, 32, 5, "wild", 32),
     (257, 1032, 144, 16, 6, "runs", 0), (333, 104, 960, 8, 3, "runs", 32), (513, 72, 224, 48, 20, "each", 32),
     (1000, 520, 320, 16, 1000, "each", 64), (700, 264, 4096, 64, 2, "runs", 128),
+    (2051, 2568, 2080, 16, 5, "runs", 32), (2048, 5120, 1024, 40, 3, "each", 0),
 ]
 
 

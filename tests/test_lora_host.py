@@ -131,11 +131,11 @@ def test_checkpoint_refusals(L):
     for name in ("dy", "c", "dw"):
         assert wg(**{name: ODD}) == q8.Q8_ERR_ALIGN
     assert wg(M=0, acc=1, dy=None) == q8.Q8_OK
-    need = q8.q8_workspace_bytes(q8.Q8_OP_CHECKPOINT_WGRAD, 256, 8192, 64)
+    need = q8.q8_workspace_bytes(q8.Q8_OP_CHECKPOINT_WGRAD, 4096, 65536, 64)
     assert need > 0
-    assert wg(M=256, N=8192) == q8.Q8_ERR_WORKSPACE
-    assert wg(M=256, N=8192, ws=GOOD, wsb=need - 1) == q8.Q8_ERR_WORKSPACE
-    assert wg(M=256, N=8192, ws=ODD, wsb=need) == q8.Q8_ERR_ALIGN
+    assert wg(M=4096, N=65536) == q8.Q8_ERR_WORKSPACE
+    assert wg(M=4096, N=65536, ws=GOOD, wsb=need - 1) == q8.Q8_ERR_WORKSPACE
+    assert wg(M=4096, N=65536, ws=ODD, wsb=need) == q8.Q8_ERR_ALIGN
 
 
 def test_binding_refuses_cpu_tensors():
