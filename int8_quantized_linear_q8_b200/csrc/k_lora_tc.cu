@@ -265,7 +265,9 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
     uint64_t* empty = full + LT_N;
     uint64_t* tfull = empty + LT_N;
     uint64_t* tempty = tfull + 2;                       // first CTA
-    uint64_t* mma_done = tempty + 2;
+    uint64_t* lready = tempty + 2;          // PRE, first CTA: adapter columns written
+    uint64_t* lgo = lready + LT_N;          // PRE: slot free for adapter columns
+    uint64_t* mma_done = lgo + LT_N;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -320,7 +322,10 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
             mbar_init(&rempty[i], 4);
         }
         for (int i = 0; i < LT_N; ++i) {
-            mbar_init(&full[i], 8 + 1);                 // a group of either CTA, the copies
+            // the copies' producer and, unless PRE, a converter group of either CTA
+            mbar_init(&full[i], PRE ? 1 : 1 + 8);
+            mbar_init(&lready[i], 8);
+            mbar_init(&lgo[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -409,8 +414,9 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                                             full0 + r.s * 8);
                         else
                             lt_tma_pair(bt, &tmap, c0 * 2, tr, full0 + r.s * 8);
-                    } else if (rank == 0) {             // written by the converters
-                        mbar_arrive(&full[r.s]);
+                    } else {                            // written by the converters
+                        if (rank == 0) mbar_arrive(&full[r.s]);
+                        if (PRE) mbar_arrive(&lgo[r.s]);
                     }
                 }
                 ++it;
@@ -426,6 +432,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
             const uint32_t idesc = lt_idesc(BN, A_MN, B_MN);
             LtRing<LT_N> r;
             LtRing<2> rt;
+            uint32_t lph = 0;                           // PRE: parity of each slot's lready
             bool ok = true, here = false;
             for (int u = u0; u < units && ok; u += ustep) {
                 int p0, t0;
@@ -450,6 +457,12 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                         ok = __all_sync(0xffffffffu,
                                         mbar_wait(&full[r.s], r.ph, status, abort_flag));
                         if (!ok) break;
+                    }
+                    if (PRE && w.kb >= nk) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(&lready[r.s], lph >> r.s & 1u,
+                                                               status, abort_flag));
+                        if (!ok) break;
+                        lph ^= 1u << r.s;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const int cur = r.s;
@@ -482,15 +495,17 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
         const int grp = (warp - LT_CONV0) >> 2;
         const int tid = threadIdx.x - 32 * LT_CONV0 - grp * 128;
         const uint32_t full0 = lt_map(smem_u32(full), lead);
+        const uint32_t lready0 = lt_map(smem_u32(lready), lead);
         LtRing<LT_NR> rr;
         LtRing<LT_N> r;
+        uint32_t lph = 0;                   // PRE: parity of each slot's lgo
         int it = 0, pending = -1;           // slot whose adapter columns are still being copied
         bool live = true;
         auto hand_over = [&](int slot) {
             // make the generic-proxy writes visible to the tensor core, then hand over
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) lt_arrive(full0 + slot * 8);
+            if (lane == 0) lt_arrive((PRE ? lready0 : full0) + slot * 8);
         };
         for (int u = u0; u < units; u += ustep) {
             int p0, t0;
@@ -503,7 +518,11 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 for (int i = 0; i < 4; ++i)
                     nxt[i] = lt_scale_bits<MODE>(a, kb * LT_BK + i * 16 + sc, sp);
             }
-            for (Walk w = walk(); more(w, t0); ++w.kb) {
+            Walk w = walk();
+            if (PRE) {                                  // the base stages are not theirs
+                for (; w.kb < w.end; ++w.kb) r.next();
+            }
+            for (; more(w, t0); ++w.kb) {
                 const int kb = w.kb;
                 if (it % GROUPS == grp) {
                     const uint32_t at = smem_u32(smem + r.s * LT_SLOT);
@@ -572,10 +591,13 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                             }
                         }
                     } else {
-                        // PRE base stages: nothing to write, but the arrival is counted, so it
-                        // must not come before the slot is free; adapter columns: both tiles
-                        // are written here
-                        const bool okw = mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag);
+                        // Adapter columns: both tiles are written here.  (PRE: the producer says
+                        // when the slot is free; who has not followed every phase of `empty`
+                        // cannot tell one from the one before the last.)
+                        const bool okw =
+                            PRE ? mbar_wait(&lgo[r.s], lph >> r.s & 1u, status, abort_flag)
+                                : mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag);
+                        lph ^= 1u << r.s;
                         live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
                     }
                     if (MODE != LORA_WGRAD && live && kb >= nk) {
