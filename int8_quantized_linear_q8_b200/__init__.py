@@ -438,11 +438,11 @@ def q8_linear_w8a8_noalloc(x: torch.Tensor, first, q: torch.Tensor, wsum: torch.
 
 def _is(t, name: str, dtype: torch.dtype, shape: Tuple[int, ...], dev: int) -> int:
     """The address of a contiguous tensor of this type and shape on the current device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
             and t.get_device() == dev and t.is_contiguous()):
-        _need(t, name, dtype, shape)
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    return t.data_ptr()
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
 def _device(t: torch.Tensor) -> int:
@@ -452,13 +452,13 @@ def _device(t: torch.Tensor) -> int:
     return torch.cuda.current_device()
 
 
-def _new(shape, dtype, dev: int, stream):
-    """A new tensor that belongs to the stream the call runs on (the caching allocator
-    may hand its memory on in that stream's order only)."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _new(shape, like: torch.Tensor, dtype: torch.dtype, stream):
+    """A new tensor on `like`'s device that belongs to the stream the call runs on (the caching
+    allocator may hand its memory on in that stream's order only)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return like.new_empty(shape, dtype=dtype)
+    return like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
 
 
 def _on(stream, dev: int) -> int:
@@ -474,8 +474,9 @@ def _scratch_bytes(op: int, M: int, N: int, K: int, extra: int) -> int:
     return _lib().q8_workspace_bytes(op, M, N, K, extra)
 
 
-def _scratch(ws, op: int, M: int, N: int, K: int, extra: int, dev: int, stream):
-    """(the workspace, its address, its bytes)"""
+def _scratch(ws, op: int, M: int, N: int, K: int, extra: int, like: torch.Tensor, dev: int,
+             stream):
+    """(the workspace, its address, its bytes); like: an 8-bit tensor on the device"""
     if ws is not None:
         if not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the current device")
@@ -483,7 +484,7 @@ def _scratch(ws, op: int, M: int, N: int, K: int, extra: int, dev: int, stream):
     nbytes = _scratch_bytes(op, M, N, K, extra)
     if nbytes == 0:
         return None, None, 0
-    ws = _new((nbytes,), torch.uint8, dev, stream)
+    ws = _new(nbytes, like, like.dtype, stream)
     return ws, ws.data_ptr(), nbytes
 
 
@@ -522,12 +523,16 @@ def q8_linear_w8a16_lora(x: torch.Tensor, q: torch.Tensor, s_w: torch.Tensor, a:
         raise ValueError("out_dtype must be bfloat16 or float32")
     R = a.shape[1]
     if y is None:
-        y = _new((M, N), out_dtype, dev, stream)
+        y = _new((M, N), x, out_dtype, stream)
+        yp = y.data_ptr()
+    else:
+        yp = _is(y, "y", out_dtype, (M, N), dev)
     if h is None:
-        h = _new((M, R), torch.float32, dev, stream)
-    yp = _is(y, "y", out_dtype, (M, N), dev)
-    hp = _is(h, "h", torch.float32, (M, R), dev)
-    ws, wp, wsb = _scratch(workspace, Q8_OP_LINEAR_W8A16_LORA, M, N, K, R, dev, stream)
+        h = _new((M, R), s_w, torch.float32, stream)
+        hp = h.data_ptr()
+    else:
+        hp = _is(h, "h", torch.float32, (M, R), dev)
+    ws, wp, wsb = _scratch(workspace, Q8_OP_LINEAR_W8A16_LORA, M, N, K, R, q, dev, stream)
     _check(_lib().q8_linear_w8a16_lora(xp, qp, sp, bp, ad, ip, yp,
                                        Q8_BF16 if out_dtype is torch.bfloat16 else Q8_F32, hp, M,
                                        N, K, wp, wsb, _on(stream, dev)), "q8_linear_w8a16_lora")
@@ -572,15 +577,16 @@ def q8_linear_w8a16_lora_backward(dy: torch.Tensor, q: torch.Tensor, s_w: torch.
             raise ValueError("db needs h, the forward call's second result")
         hp = _is(h, "h", torch.float32, (M, R), dev)
     if want_dx and dx is None:
-        dx = _new((M, K), torch.bfloat16, dev, stream)
+        dx = _new((M, K), dy, torch.bfloat16, stream)
     if want_da and da is None:
-        da = _new((L, R, K), torch.float32, dev, stream)
+        da = _new((L, R, K), s_w, torch.float32, stream)
     if want_db and db is None:
-        db = _new((L, N, R), torch.float32, dev, stream)
+        db = _new((L, N, R), s_w, torch.float32, stream)
     dxp = _is(dx, "dx", torch.bfloat16, (M, K), dev) if want_dx else None
     dap = _is(da, "da", torch.float32, (L, R, K), dev) if want_da else None
     dbp = _is(db, "db", torch.float32, (L, N, R), dev) if want_db else None
-    ws, wp, wsb = _scratch(workspace, Q8_OP_LINEAR_W8A16_LORA_BACKWARD, M, N, K, R, dev, stream)
+    ws, wp, wsb = _scratch(workspace, Q8_OP_LINEAR_W8A16_LORA_BACKWARD, M, N, K, R, q, dev,
+                            stream)
     _check(_lib().q8_linear_w8a16_lora_backward(dyp, qp, sp, ad, ip, hp, saved, dxp, dap, dbp,
                                                 1 if accumulate else 0, M, N, K, wp, wsb,
                                                 _on(stream, dev)),
@@ -608,11 +614,15 @@ def q8_checkpoint_save(x: torch.Tensor, group: int = 128, codes=None, exps=None,
     if group not in (32, 64, 128, 256) or K % group:
         raise ValueError("group must be 32, 64, 128 or 256 and divide K")
     if codes is None:
-        codes = _new((M, K), torch.int8, dev, stream)
+        codes = _new((M, K), x, torch.int8, stream)
+        cp = codes.data_ptr()
+    else:
+        cp = _is(codes, "codes", torch.int8, (M, K), dev)
     if exps is None:
-        exps = _new((M, K // group), torch.uint8, dev, stream)
-    cp = _is(codes, "codes", torch.int8, (M, K), dev)
-    ep = _is(exps, "exps", torch.uint8, (M, K // group), dev)
+        exps = _new((M, K // group), x, torch.uint8, stream)
+        ep = exps.data_ptr()
+    else:
+        ep = _is(exps, "exps", torch.uint8, (M, K // group), dev)
     _check(_lib().q8_checkpoint_save(xp, Q8_BF16 if bf16 else Q8_F32, M, K, group, cp, ep,
                                      _on(stream, dev)), "q8_checkpoint_save")
     return codes, exps
@@ -627,8 +637,10 @@ def q8_checkpoint_load(codes: torch.Tensor, exps: torch.Tensor, y=None,
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
     if y is None:
-        y = _new((M, K), out_dtype, dev, stream)
-    yp = _is(y, "y", out_dtype, (M, K), dev)
+        y = _new((M, K), codes, out_dtype, stream)
+        yp = y.data_ptr()
+    else:
+        yp = _is(y, "y", out_dtype, (M, K), dev)
     _check(_lib().q8_checkpoint_load(saved.x, saved.exps, saved.group, yp,
                                      Q8_BF16 if out_dtype is torch.bfloat16 else Q8_F32, M, K,
                                      _on(stream, dev)), "q8_checkpoint_load")
@@ -647,9 +659,9 @@ def q8_checkpoint_wgrad(dy: torch.Tensor, codes: torch.Tensor, exps: torch.Tenso
     if dw is None:
         if accumulate:
             raise ValueError("accumulate adds to dw: pass it")
-        dw = _new((N, K), torch.float32, dev, stream)
+        dw = _new((N, K), dy, torch.float32, stream)
     dwp = _is(dw, "dw", torch.float32, (N, K), dev)
-    ws, wp, wsb = _scratch(workspace, Q8_OP_CHECKPOINT_WGRAD, M, N, K, 0, dev, stream)
+    ws, wp, wsb = _scratch(workspace, Q8_OP_CHECKPOINT_WGRAD, M, N, K, 0, codes, dev, stream)
     _check(_lib().q8_checkpoint_wgrad(dyp, saved.x, saved.exps, saved.group, dwp,
                                       1 if accumulate else 0, M, N, K, wp, wsb, _on(stream, dev)),
            "q8_checkpoint_wgrad")

@@ -956,7 +956,6 @@ template <int MODE>
 __global__ __launch_bounds__(256) void k_lora_expand(const LoraGemm a, int64_t n16, int row16,
                                                      uint16_t* __restrict__ out) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t i0 = (int64_t)blockIdx.x * 512 + threadIdx.x;
     uint4 w[2];
 #pragma unroll
@@ -995,19 +994,16 @@ size_t lora_pre_bytes(int64_t P, int64_t C, int64_t T) {
 cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, cudaStream_t st) {
     const int64_t n16 = (int64_t)a.P * a.C / 16;
     const int row16 = (mode == LORA_FWD ? a.C : a.P) / 16;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((n16 + 511) / 512));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (mode == LORA_FWD) return cudaLaunchKernelEx(&cfg, k_lora_expand<LORA_FWD>, a, n16, row16, out);
-    if (mode == LORA_DGRAD)
-        return cudaLaunchKernelEx(&cfg, k_lora_expand<LORA_DGRAD>, a, n16, row16, out);
-    return cudaLaunchKernelEx(&cfg, k_lora_expand<LORA_WGRAD>, a, n16, row16, out);
+    // launched after all of the stream's earlier work (no early start): the plan beside it and
+    // the kernels after that rely on it
+    const unsigned grid = (unsigned)((n16 + 511) / 512);
+    if (mode == LORA_FWD)
+        k_lora_expand<LORA_FWD><<<grid, 256, 0, st>>>(a, n16, row16, out);
+    else if (mode == LORA_DGRAD)
+        k_lora_expand<LORA_DGRAD><<<grid, 256, 0, st>>>(a, n16, row16, out);
+    else
+        k_lora_expand<LORA_WGRAD><<<grid, 256, 0, st>>>(a, n16, row16, out);
+    return cudaGetLastError();
 }
 
 }  // namespace q8

@@ -489,13 +489,13 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     a.lists = lora_plan_lists(ws + w.plan);
     a.R = R;
     a.L = L;
-    Q8_TRY(launched(launch_lora_plan(ids, M, L, ws + w.plan, st)));
-    Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
-                                       ad->scale, ws + w.plan, h, hp, M, (int)K, R, L, st, sms)));
     if (w.pre_bytes) {
         Q8_TRY(launched(launch_lora_expand(LORA_FWD, a, (uint16_t*)(ws + w.pre), st)));
         a.pre = (const uint16_t*)(ws + w.pre);
     }
+    Q8_TRY(launched(launch_lora_plan(ids, M, L, ws + w.plan, w.pre_bytes > 0, st)));
+    Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
+                                       ad->scale, ws + w.plan, h, hp, M, (int)K, R, L, st, sms)));
     return launched(launch_lora_tc(LORA_FWD, a, st, sms, status));
 }
 
@@ -541,32 +541,31 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
     float* g = (float*)(ws + w.g);
     uint16_t* hp = (uint16_t*)(ws + w.hp);
     void* plan = ws + w.plan;
-    Q8_TRY(launched(launch_lora_plan(ids, M, L, plan, st)));
+    LoraGemm a = {};
+    a.q = q;
+    a.t = (const uint16_t*)dy;
+    a.s_w = s_w;
+    a.out = dx;
+    a.out_bf16 = 1;
+    a.P = (int)K;
+    a.C = (int)N;
+    a.T = M;
+    a.ids = ids;
+    a.low = (const uint16_t*)ad->a;
+    a.hp = hp;
+    a.lists = lora_plan_lists(plan);
+    a.R = R;
+    a.L = L;
+    const bool pre = dx && w.pre_bytes;
+    if (pre) {
+        Q8_TRY(launched(launch_lora_expand(LORA_DGRAD, a, (uint16_t*)(ws + w.pre), st)));
+        a.pre = (const uint16_t*)(ws + w.pre);
+    }
+    Q8_TRY(launched(launch_lora_plan(ids, M, L, plan, pre, st)));
     if (dx || da)
         Q8_TRY(launched(launch_lora_shrink(true, (const uint16_t*)dy, (const uint16_t*)ad->b,
                                            ad->scale, plan, g, hp, M, (int)N, R, L, st, sms)));
-    if (dx) {
-        LoraGemm a = {};
-        a.q = q;
-        a.t = (const uint16_t*)dy;
-        a.s_w = s_w;
-        a.out = dx;
-        a.out_bf16 = 1;
-        a.P = (int)K;
-        a.C = (int)N;
-        a.T = M;
-        a.ids = ids;
-        a.low = (const uint16_t*)ad->a;
-        a.hp = hp;
-        a.lists = lora_plan_lists(plan);
-        a.R = R;
-        a.L = L;
-        if (w.pre_bytes) {
-            Q8_TRY(launched(launch_lora_expand(LORA_DGRAD, a, (uint16_t*)(ws + w.pre), st)));
-            a.pre = (const uint16_t*)(ws + w.pre);
-        }
-        Q8_TRY(launched(launch_lora_tc(LORA_DGRAD, a, st, sms, status)));
-    }
+    if (dx) Q8_TRY(launched(launch_lora_tc(LORA_DGRAD, a, st, sms, status)));
     if (da || db)
         Q8_TRY(launched(launch_lora_wgrad(
             dy, h, db, da ? input->x : nullptr, da && input->group ? input->exps : nullptr,

@@ -216,7 +216,9 @@ struct LoraGemm {
 };
 size_t lora_plan_bytes(int64_t M);               // workspace of the plan
 const int* lora_plan_lists(const void* ws);
-cudaError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, void* ws, cudaStream_t st);
+// beside: right behind launch_lora_expand on the stream, and at the same time
+cudaError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, void* ws, bool beside,
+                             cudaStream_t st);
 // h (or, backward, g) of every row, and its two bf16 parts hp [M, 2 R]; ws: the plan of its ids
 cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, const float* scale,
                                const void* ws, float* h, uint16_t* hp, int64_t M, int C, int R,
