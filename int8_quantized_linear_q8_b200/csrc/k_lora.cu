@@ -10,8 +10,7 @@
 // works on blocks of rows of one adapter, gathered row by row through the permutation; rows
 // without an adapter form a last group, whose h is zero.  The products run on the warp-level
 // bf16 MMA: with at most 64 columns of rank per block there is no tile for tcgen05, and the
-// operand loads, not the MMAs, take the time.  fp32 rows (h, g) enter as two bf16 parts, high
-// and rest, off by at most 2^-17.
+// operand loads, not the MMAs, take the time.
 #include "q8_kernels.cuh"
 
 namespace q8 {
@@ -232,15 +231,28 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// a float of another CTA of the cluster (its shared memory, same offset)
-__device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
-    float v;
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
-        "ld.shared::cluster.f32 %0, [a];\n\t}"
-        : "=f"(v)
-        : "r"(addr), "r"(rank)
-        : "memory");
+// Four floats at the same place of every CTA's shared memory, added in rank order.  All loads are
+// on their way before the first addition: a load from another CTA takes most of a microsecond.
+__device__ __forceinline__ float4 cluster_sum4(uint32_t addr, int S) {
+    float4 q[8];
+#pragma unroll
+    for (int o = 0; o < 8; ++o)
+        if (o < S)
+            asm volatile(
+                "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+                "ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a];\n\t}"
+                : "=f"(q[o].x), "=f"(q[o].y), "=f"(q[o].z), "=f"(q[o].w)
+                : "r"(addr), "r"(o)
+                : "memory");
+    float4 v = q[0];
+#pragma unroll
+    for (int o = 1; o < 8; ++o)
+        if (o < S) {
+            v.x += q[o].x;
+            v.y += q[o].y;
+            v.z += q[o].z;
+            v.w += q[o].w;
+        }
     return v;
 }
 
@@ -287,30 +299,46 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
     const int steps = (C + 63) / 64;
     const int s0 = steps * part / S, s1 = steps * (part + 1) / S;
     const uint32_t base = smem_u32(sm);
-    // copies: thread -> row tid >> 1, four 16-byte pieces from 4 * (tid & 1)
-    const int crow = tid >> 1, cp0 = (tid & 1) * 4;
-    const uint16_t* xrow =
-        x + (int64_t)ld_after(perm + start + (crow < rows ? crow : 0)) * C;
+    // copies: eight neighbouring threads take a row's 128 bytes (a whole line a request: two
+    // threads with four pieces each made half-used sectors of every request, and the kernel
+    // half as fast); thread: piece tid & 7 of rows tid >> 3, + 16, + 32, + 48
+    const int cr = tid >> 3, cpc = tid & 7;
+    const uint16_t* xrow[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int row = cr + 16 * j;
+        xrow[j] = x + (int64_t)ld_after(perm + start + (row < rows ? row : 0)) * C + cpc * 8;
+    }
     const uint16_t* wmat = W + (int64_t)key * R * C;
     auto load = [&](int st, int slot) {
         const uint32_t xs = base + slot * lsh_stage(NT), wsm = xs + 8192;
-        const int c0 = st * 64;
+        const int c0 = st * 64, c = c0 + cpc * 8;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int pc = cp0 + j, c = c0 + pc * 8;
-            const bool live = crow < rows && c < C;
-            cp_async16(xs + crow * 128 + ((pc ^ (crow & 7)) << 4), live ? xrow + c : x, live);
-            if (!BWD) {
-                if (crow < 8 * NT) {
-                    const bool lw = crow < rn && c < C;
-                    cp_async16(wsm + crow * 128 + ((pc ^ (crow & 7)) << 4),
-                               lw ? wmat + (int64_t)(r0 + crow) * C + c : W, lw);
+            const int row = cr + 16 * j;
+            const bool live = row < rows && c < C;
+            cp_async16(xs + row * 128 + ((cpc ^ (row & 7)) << 4), live ? xrow[j] + c0 : x, live);
+        }
+        if (!BWD) {
+#pragma unroll
+            for (int j = 0; j < (8 * NT + 15) / 16; ++j) {
+                const int row = cr + 16 * j;
+                if (row < 8 * NT) {
+                    const bool lw = row < rn && c < C;
+                    cp_async16(wsm + row * 128 + ((cpc ^ (row & 7)) << 4),
+                               lw ? wmat + (int64_t)(r0 + row) * C + c : W, lw);
                 }
-            } else if (pc < NT) {
-                const int cc = c0 + crow;
-                const bool lw = cc < C && pc * 8 < rn;
-                cp_async16(wsm + lsh_piece<NT>(crow, pc),
-                           lw ? wmat + (int64_t)cc * R + r0 + pc * 8 : W, lw);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < (NT + 1) / 2; ++j) {
+                const int u = tid + 128 * j, row = u / NT, pc = u % NT;
+                if (row < 64) {
+                    const int cc = c0 + row;
+                    const bool lw = cc < C && pc * 8 < rn;
+                    cp_async16(wsm + lsh_piece<NT>(row, pc),
+                               lw ? wmat + (int64_t)cc * R + r0 + pc * 8 : W, lw);
+                }
             }
         }
     };
@@ -331,23 +359,34 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
         if (st + LSH - 1 < s1) load(st + LSH - 1, (slot + LSH - 1) % LSH);
         cp_commit();
         const uint32_t xs = base + slot * lsh_stage(NT), wsm = xs + 8192;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t a[4];
+        // fragments of a k step are read before the MMAs of the step before it: the few warps of
+        // a block wait on nothing else
+        uint32_t fa[2][4], fb[2][(NT + 1) / 2][4];
+        auto frags = [&](int k) {
             const int ar = warp * 16 + (lane & 15);
-            ldsm4(xs + ar * 128 + (((2 * k + (lane >> 4)) ^ (ar & 7)) << 4), a);
+            ldsm4(xs + ar * 128 + (((2 * k + (lane >> 4)) ^ (ar & 7)) << 4), fa[k & 1]);
 #pragma unroll
             for (int n = 0; n < NT; n += 2) {
-                uint32_t b[4];
                 if (!BWD) {
                     // rows r of two n-tiles, k halves
                     const int br = (n + (NT > 1 ? lane >> 4 : 0)) * 8 + (lane & 7);
-                    ldsm4(wsm + br * 128 + (((2 * k + ((lane >> 3) & 1)) ^ (br & 7)) << 4), b);
+                    ldsm4(wsm + br * 128 + (((2 * k + ((lane >> 3) & 1)) ^ (br & 7)) << 4),
+                          fb[k & 1][n >> 1]);
                 } else {
                     const int br = k * 16 + (lane & 15);
                     const int pc = n + (NT > 1 ? lane >> 4 : 0);
-                    ldsm4_t(wsm + lsh_piece<NT>(br, pc), b);
+                    ldsm4_t(wsm + lsh_piece<NT>(br, pc), fb[k & 1][n >> 1]);
                 }
+            }
+        };
+        frags(0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k < 3) frags(k + 1);
+            const uint32_t* a = fa[k & 1];
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                const uint32_t* b = fb[k & 1][n >> 1];
                 mma_bf16_16816(acc[n], a[0], a[1], a[2], a[3], b[0], b[1]);
                 if (NT > 1) mma_bf16_16816(acc[n + (NT > 1)], a[0], a[1], a[2], a[3], b[2], b[3]);
             }
@@ -375,10 +414,10 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
             }
         return;
     }
-    // parts in shared memory [64][8 NT + 1], added over the cluster in rank order
+    // parts in shared memory [64][8 NT + 4], added over the cluster in rank order
     cp_wait<0>();
     __syncthreads();
-    constexpr int LD = 8 * NT + 1;
+    constexpr int LD = 8 * NT + 4;
     float* mine = reinterpret_cast<float*>(sm);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -387,11 +426,14 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
             mine[(warp * 16 + g + 8 * (i >> 1)) * LD + n * 8 + 2 * t + (i & 1)] = acc[n][i];
     cluster_sync_all();
     const int per = (rows + S - 1) / S, lo = part * per, hi = min(rows, lo + per);
-    for (int u = tid; u < (hi - lo) * rn; u += 128) {
-        const int row = lo + u / rn, r = u % rn;
-        float v = 0.0f;
-        for (int q = 0; q < S; ++q) v += ld_peer(base + (row * LD + r) * 4, q);
-        put(row, r, v);
+    const int quads = rn >> 2;
+    for (int u = tid; u < (hi - lo) * quads; u += 128) {
+        const int row = lo + u / quads, r = u % quads * 4;
+        const float4 v = cluster_sum4(base + (row * LD + r) * 4, S);
+        put(row, r, v.x);
+        put(row, r + 1, v.y);
+        put(row, r + 2, v.z);
+        put(row, r + 3, v.w);
     }
     cluster_sync_all();                             // nobody leaves while its part is read
 }
@@ -400,8 +442,8 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
 // out[p, r] = sum over the rows m of adapter i of X[m, p] * low[m, r], for 128 p and up to
 // 8 * NT columns of the rank; X is dy (dB) or the layer's input in bf16 or 8 bits (dA).  Steps
 // of 32 rows through a ring of three shared-memory stages (cp.async of the gathered rows: X as it
-// is kept, low in fp32); a step's low values become two bf16 tiles and its codes a bf16 tile
-// (exactly) in shared memory, then X^T and low are read with transposing ldmatrix.  Clusters
+// is kept, low in fp32); a step's low values become three bf16 tiles (their sum is off by
+// at most 2^-25 of the value) and its codes a bf16 tile (exactly) in shared memory, then X^T and low are read with transposing ldmatrix.  Clusters
 // split the rows as above.
 // One launch makes both: CTAs of dA (KIND 0: from bf16, 1: from codes) after those of dB (2).
 constexpr int LW_ROWS = 32, LW_STAGES = 3, LW_THREADS = 256;
@@ -410,7 +452,7 @@ __host__ __device__ constexpr int lw_stage(int nt) { return LW_X + LW_ROWS * 32 
 __host__ __device__ constexpr int lw_work(int nt) { return LW_STAGES * lw_stage(nt); }
 template <int NT>
 constexpr int lw_smem() {
-    constexpr int loop = lw_work(NT) + 2 * LW_LOW + LW_X, tile = 128 * (8 * NT + 1) * 4;
+    constexpr int loop = lw_work(NT) + 3 * LW_LOW + LW_X, tile = 128 * (8 * NT + 4) * 4;
     return loop > tile ? loop : tile;
 }
 struct LoraGrad {
@@ -445,7 +487,7 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
 
     // thread: row tid >> 3 of a step, 16 of its p, an eighth of its low
     const int xr = tid >> 3, xq = tid & 7;
-    const uint32_t work = base + lw_work(NT), xwork = work + 2 * LW_LOW;
+    const uint32_t work = base + lw_work(NT), xwork = work + 3 * LW_LOW;
     int row_next = -1;                              // this thread's row in the step loaded next
     // KIND 1: the exponent bytes of the steps on their way, oldest first (a load is not waited
     // for before the step after the one that issued it)
@@ -466,12 +508,13 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
             cp_async16(xs + xr * 128 + ((xq ^ (xr & 7)) << 4), in ? (const void*)src : X, in);
             e = in ? __ldg(exps + m * (P >> gshift) + ((p0 + xq * 16) >> gshift)) : 0u;
         } else {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(X) + m * P + p0 + xq * 16;
+            // eight neighbouring threads: 128 bytes of a row at a time
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(X) + m * P + p0 + xq * 8;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const bool in = live && p0 + xq * 16 + 8 * j < P;
-                cp_async16(xs + xr * 256 + (((xq * 2 + j) ^ (xr & 7)) << 4),
-                           in ? (const void*)(src + 8 * j) : X, in);
+                const bool in = live && p0 + xq * 8 + 64 * j < P;
+                cp_async16(xs + xr * 256 + (((xq + 8 * j) ^ (xr & 7)) << 4),
+                           in ? (const void*)(src + 64 * j) : X, in);
             }
         }
 #pragma unroll
@@ -536,46 +579,62 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
                          : "=f"(v[0]), "=f"(v[1])
                          : "r"(ls + xr * 32 * NT + r * 4)
                          : "memory");
-            uint32_t hi = 0, lo = 0;
+            uint32_t o[3] = {0, 0, 0};
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const float u = v[q] * f;
-                const uint32_t b = bf16_bits_rn(u);
-                hi |= b << (16 * q);
-                lo |= bf16_bits_rn(u - __uint_as_float(b << 16)) << (16 * q);
+                float u = v[q] * f;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {                   // each part of what is left
+                    const uint32_t b = bf16_bits_rn(u);
+                    o[i] |= b << (16 * q);
+                    u -= __uint_as_float(b << 16);
+                }
             }
             const uint32_t to = work + xr * 128 + (((r >> 3) ^ (xr & 7)) << 4) + (r & 7) * 2;
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(hi) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + LW_LOW), "r"(lo) : "memory");
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i * LW_LOW), "r"(o[i])
+                             : "memory");
         }
         __syncthreads();
         const uint32_t xt = KIND == 1 ? xwork : xs;
-#pragma unroll
-        for (int k = 0; k < LW_ROWS / 16; ++k) {
-            // stored rows m (k), 8 p a piece: matrices (m 0-7, p 0-7), (m 0-7, p 8-15),
-            // (m 8-15, p 0-7), (m 8-15, p 8-15), each transposed; a warp has 16 p
-            uint32_t a[4];
+        // Stored rows m (k), 8 p a piece: matrices (m 0-7, p 0-7), (m 0-7, p 8-15), (m 8-15, p 0-7),
+        // (m 8-15, p 8-15), each transposed; a warp has 16 p.  Fragments are read ahead of the
+        // MMAs before them, as above.
+        uint32_t fa[2][4], fb[2][(NT + 1) / 2][4];
+        auto frag_a = [&](int k) {
             const int am = k * 16 + (lane & 7) + ((lane >> 4) << 3);
             const int apc = warp * 2 + ((lane >> 3) & 1);
-            ldsm4_t(xt + am * 256 + ((apc ^ (am & 7)) << 4), a);
+            ldsm4_t(xt + am * 256 + ((apc ^ (am & 7)) << 4), fa[k]);
+        };
+        auto frags_b = [&](int i) {                             // k step i / 3, part i % 3
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int n = 0; n < NT; n += 2) {
+                const int m = i / 3 * 16 + (lane & 15), pc = n + (NT > 1 ? lane >> 4 : 0);
+                ldsm4_t(work + i % 3 * LW_LOW + m * 128 + ((pc ^ (m & 7)) << 4),
+                        fb[i & 1][n >> 1]);
+            }
+        };
+        frag_a(0);
+        frags_b(0);
+        frag_a(1);
 #pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                    uint32_t b[4];
-                    const int m = k * 16 + (lane & 15), pc = n + (NT > 1 ? lane >> 4 : 0);
-                    ldsm4_t(work + half * LW_LOW + m * 128 + ((pc ^ (m & 7)) << 4), b);
-                    mma_bf16_16816(acc[n], a[0], a[1], a[2], a[3], b[0], b[1]);
-                    if (NT > 1)
-                        mma_bf16_16816(acc[n + (NT > 1)], a[0], a[1], a[2], a[3], b[2], b[3]);
-                }
+        for (int i = 0; i < 3 * LW_ROWS / 16; ++i) {
+            if (i + 1 < 3 * LW_ROWS / 16) frags_b(i + 1);
+            const uint32_t* a = fa[i / 3];
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                const uint32_t* b = fb[i & 1][n >> 1];
+                mma_bf16_16816(acc[n], a[0], a[1], a[2], a[3], b[0], b[1]);
+                if (NT > 1) mma_bf16_16816(acc[n + (NT > 1)], a[0], a[1], a[2], a[3], b[2], b[3]);
+            }
         }
         slot = (slot + 1) % LW_STAGES;
     }
     cp_wait<0>();
     __syncthreads();
-    // the tile in shared memory [128][8 NT + 1], added over the cluster in rank order
-    constexpr int LD = 8 * NT + 1;
+    // the tile in shared memory [128][8 NT + 4], added over the cluster in rank order
+    constexpr int LD = 8 * NT + 4;
     float* mine = reinterpret_cast<float*>(sm);
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -585,17 +644,30 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
             mine[(warp * 16 + g + 8 * (i >> 1)) * LD + n * 8 + 2 * t + (i & 1)] = acc[n][i];
     if (S > 1) cluster_sync_all(); else __syncthreads();
     const int pn = min(128, P - p0), per = (pn + S - 1) / S;
-    const int lo = part * per, hi = min(pn, lo + per), wide = max(hi - lo, 0);
-    for (int u = tid; u < wide * rn; u += LW_THREADS) {
-        const int p = lo + (KIND == 2 ? u / rn : u % wide), r = KIND == 2 ? u % rn : u / wide;
-        float v = 0.0f;
+    const int lo = part * per, hi = min(pn, lo + per), wide = max(hi - lo, 0), quads = rn >> 2;
+    for (int u = tid; u < wide * quads; u += LW_THREADS) {
+        // neighbouring threads: neighbouring columns (dB) or p (dA)
+        const int p = lo + (KIND == 2 ? u / quads : u % wide);
+        const int r = (KIND == 2 ? u % quads : u / wide) * 4;
+        float4 v;
         if (S > 1)
-            for (int o = 0; o < S; ++o) v += ld_peer(base + (p * LD + r) * 4, o);
+            v = cluster_sum4(base + (p * LD + r) * 4, S);
         else
-            v = mine[p * LD + r];
-        float* to = out + (KIND == 2 ? ((int64_t)key * P + p0 + p) * R + r0 + r
-                                    : ((int64_t)key * R + r0 + r) * P + p0 + p);
-        *to = accumulate ? *to + v : v;
+            v = *reinterpret_cast<const float4*>(mine + p * LD + r);
+        if (KIND == 2) {
+            float4* to = reinterpret_cast<float4*>(out + ((int64_t)key * P + p0 + p) * R + r0 + r);
+            if (accumulate) {
+                const float4 w = *to;
+                v = make_float4(w.x + v.x, w.y + v.y, w.z + v.z, w.w + v.w);
+            }
+            *to = v;
+        } else {
+            float* to = out + ((int64_t)key * R + r0 + r) * P + p0 + p;
+            const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                to[(int64_t)j * P] = accumulate ? to[(int64_t)j * P] + w[j] : w[j];
+        }
     }
     if (S > 1) cluster_sync_all();              // nobody leaves while its part is read
 }
@@ -640,7 +712,7 @@ static cudaError_t launch_clustered(void (*k)(KArgs...), dim3 grid, int threads,
 }
 template <int NT>
 constexpr int lsh_smem() { return LSH * lsh_stage(NT); }
-static_assert(lsh_smem<1>() >= 64 * 9 * 4 && lsh_smem<8>() >= 64 * 65 * 4, "room for the parts");
+static_assert(lsh_smem<1>() >= 64 * 12 * 4 && lsh_smem<8>() >= 64 * 68 * 4, "room for the parts");
 // columns of the rank per CTA, in n-tiles of 8
 static int rank_tiles(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : R <= 32 ? 4 : 8; }
 
