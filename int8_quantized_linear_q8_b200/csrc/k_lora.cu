@@ -442,8 +442,8 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
 // out[p, r] = sum over the rows m of adapter i of X[m, p] * low[m, r], for 128 p and up to
 // 8 * NT columns of the rank; X is dy (dB) or the layer's input in bf16 or 8 bits (dA).  Steps
 // of 32 rows through a ring of three shared-memory stages (cp.async of the gathered rows: X as it
-// is kept, low in fp32); a step's low values become three bf16 tiles (their sum is off by
-// at most 2^-25 of the value) and its codes a bf16 tile (exactly) in shared memory, then X^T and low are read with transposing ldmatrix.  Clusters
+// is kept, low in fp32); a step's low values become three bf16 tiles (8 bits of the number each,
+// so that their sum is the fp32 value) and its codes a bf16 tile (exactly) in shared memory, then X^T and low are read with transposing ldmatrix.  Clusters
 // split the rows as above.
 // One launch makes both: CTAs of dA (KIND 0: from bf16, 1: from codes) after those of dB (2).
 constexpr int LW_ROWS = 32, LW_STAGES = 3, LW_THREADS = 256;
@@ -569,32 +569,45 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
                              "r"(o[4 * q + 3])
                              : "memory");
         }
-        // NT columns a thread (for a rank tile of 8: two, in half of the threads)
+        // NT columns a thread (for a rank tile of 8: two, in half of the threads), each cut into
+        // three bf16 numbers: 8 bits at a time, which is the whole of an fp32 number
+        constexpr int CW = NT == 1 ? 2 : NT;
+        if (xq * CW < 8 * NT) {
+            const int r = xq * CW;
+            float v[CW];
+            const uint32_t from = ls + xr * 32 * NT + r * 4;
 #pragma unroll
-        for (int j = 0; j < (NT == 1 ? 2 : NT); j += 2) {
-            const int r = xq * (NT == 1 ? 2 : NT) + j;
-            if (r >= 8 * NT) break;
-            float v[2];
-            asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
-                         : "=f"(v[0]), "=f"(v[1])
-                         : "r"(ls + xr * 32 * NT + r * 4)
-                         : "memory");
-            uint32_t o[3] = {0, 0, 0};
+            for (int j = 0; j < CW; j += 2)
+                asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
+                             : "=f"(v[j]), "=f"(v[j + 1])
+                             : "r"(from + j * 4)
+                             : "memory");
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float u = v[q] * f;
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {                   // each part of what is left
-                    const uint32_t b = bf16_bits_rn(u);
-                    o[i] |= b << (16 * q);
-                    u -= __uint_as_float(b << 16);
-                }
-            }
+            for (int j = 0; j < CW; ++j) v[j] *= f;
             const uint32_t to = work + xr * 128 + (((r >> 3) ^ (xr & 7)) << 4) + (r & 7) * 2;
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i * LW_LOW), "r"(o[i])
-                             : "memory");
+            for (int i = 0; i < 3; ++i) {
+                uint32_t o[CW / 2];
+#pragma unroll
+                for (int j = 0; j < CW; j += 2) {
+                    const uint32_t a = __float_as_uint(v[j]), b = __float_as_uint(v[j + 1]);
+                    o[j >> 1] = __byte_perm(a, b, 0x7632);
+                    v[j] -= __uint_as_float(a & 0xFFFF0000u);
+                    v[j + 1] -= __uint_as_float(b & 0xFFFF0000u);
+                }
+                if (CW == 8)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + i * LW_LOW),
+                                 "r"(o[0]), "r"(o[CW > 2 ? 1 : 0]), "r"(o[CW > 4 ? 2 : 0]),
+                                 "r"(o[CW > 6 ? 3 : 0])
+                                 : "memory");
+                else if (CW == 4)
+                    asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(to + i * LW_LOW),
+                                 "r"(o[0]), "r"(o[CW > 2 ? 1 : 0])
+                                 : "memory");
+                else
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i * LW_LOW), "r"(o[0])
+                                 : "memory");
+            }
         }
         __syncthreads();
         const uint32_t xt = KIND == 1 ? xwork : xs;

@@ -245,7 +245,14 @@ __device__ __forceinline__ void lt_store(const LoraGemm& a, int t0, int64_t t1, 
         }
 #pragma unroll
         for (int j = 0; j < W; ++j)
-            if (t0 + j < t1 && p < a.P) out[(int64_t)j * a.P] = v[j];
+            if (t0 + j < t1 && p < a.P) {
+                // a weight gradient is larger than L2 can hold beside the operands: streamed past
+                // them (wgrad 4096 x 11008 x 4096: 292 -> 275 us)
+                if (MODE == LORA_WGRAD)
+                    st_stream_f32(out + (int64_t)j * a.P, v[j]);
+                else
+                    out[(int64_t)j * a.P] = v[j];
+            }
     }
 }
 
@@ -280,9 +287,9 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
     const int u0 = blockIdx.x / (2 * S), ustep = gridDim.x / (2 * S);
     const int nk = (a.C + LT_BK - 1) / LT_BK;
     const int half = BN >> 1;
-    // Tiles run over t first, in even blocks of at most 16 t tiles: the pairs that run at once share both
+    // Tiles run over t first, in even blocks of at most 8 t tiles: the pairs that run at once share both
     // operands through L2 and the int8 operand is read from HBM once per block.
-    const int tblk = (num_t + (num_t + 15) / 16 - 1) / ((num_t + 15) / 16);
+    const int tblk = (num_t + (num_t + 7) / 8 - 1) / ((num_t + 7) / 8);
     auto tile_of = [&](int u, int& p0, int& t0) {
         const int full = num_p * tblk, blk = u / full, rem = u - blk * full;
         const int tb = min(tblk, num_t - blk * tblk);
@@ -984,9 +991,11 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraGemm a, int64_t n
 }
 
 // The expansion moves 3 bytes a value and is a launch more; the conversion inside the GEMM costs
-// about a fifth of its time, which grows with T.
-constexpr int64_t LT_PRE_T = 1024;
-constexpr double LT_PRE_FLOPS = 2e10;
+// about a quarter of its time, which grows with T.  Measured, us, expanded / converted inside, for
+// K x N = 2048 x 8192 and 4096 x 11008: forward, T = 512: 43 / 40, 93 / 83; 1024: 57 / 64, 115 / 129;
+// 4096: 129 / 188, 295 / 398; dgrad the same way; 960 x 2560 at T = 1024 (5e9 operations): 29 / 23.
+constexpr int64_t LT_PRE_T = 896;
+constexpr double LT_PRE_FLOPS = 8e9;
 size_t lora_pre_bytes(int64_t P, int64_t C, int64_t T) {
     return T >= LT_PRE_T && 2.0 * (double)P * (double)C * (double)T >= LT_PRE_FLOPS
                ? (size_t)P * (size_t)C * 2 : 0;
