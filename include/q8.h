@@ -340,6 +340,7 @@ typedef struct {
  *   workspace: at least q8_workspace_bytes(Q8_OP_LINEAR_W8A16_LORA, M, N, K, rank) bytes
  *   (may be NULL when that is 0); its contents on entry do not matter.  Calls that overlap
  *   on the GPU, replays of captured graphs among them, need a workspace each.
+ * M <= 0x7fffff00 and N < 2^30 here and in the backward pass (Q8_ERR_SHAPE).
  * Finite inputs are a precondition, as everywhere: adapters that no row uses are not read,
  * but a non-finite weight of an adapter in use may reach the other rows of its tile. */
 q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
@@ -404,7 +405,8 @@ q8_status q8_checkpoint_load(const int8_t* codes, const uint8_t* exps, int group
 /* Weight gradient of a linear from the checkpoint of its input:
  *     dw[n,k] = sum_m dy[m,n] * codes[m,k] * 2^(exps[m,k/group] - 127)
  * exact products, fp32 accumulation.
- *   dy device bf16 [M, N] (N % 8 == 0, Q8_ERR_SHAPE otherwise); codes, exps, group as
+ *   dy device bf16 [M, N] (N % 8 == 0, M and N as for the adapter calls, Q8_ERR_SHAPE
+ *   otherwise); codes, exps, group as
  *   written by q8_checkpoint_save; dw device fp32 [N, K]: overwritten, or added to when
  *   accumulate != 0.  M == 0 sets dw to 0 (leaves it when accumulating).
  *   workspace: at least q8_workspace_bytes(Q8_OP_CHECKPOINT_WGRAD, M, N, K, 0) bytes (may be

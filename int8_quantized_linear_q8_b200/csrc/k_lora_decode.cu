@@ -25,13 +25,21 @@ __global__ __cluster_dims__(LD_CTAS, 1, 1) __launch_bounds__(LD_THREADS) void k_
     const float* __restrict__ bias, const int32_t* __restrict__ ids, float* __restrict__ h,
     float* __restrict__ t, int64_t N, int K, int R, int L) {
     __shared__ float sums[LD_SUMS];
-    __shared__ float hs[256];
+    __shared__ __align__(16) float hs[256];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int m = blockIdx.y, part = blockIdx.x;            // a row's cluster: its CTAs in order
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int id = __ldg(ids + m);
     const bool has = id >= 0 && id < L;
+    const int64_t n0 = N * part / LD_CTAS, n1 = N * (part + 1) / LD_CTAS;
+    if (has) {
+        // this CTA's rows of B on their way to L2 while h is made
+        const char* b0 = reinterpret_cast<const char*>(B + ((int64_t)id * N + n0) * R);
+        const int64_t bytes = (n1 - n0) * R * 2;
+        for (int64_t o = (int64_t)tid * 128; o < bytes; o += LD_THREADS * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(b0 + o) : "memory");
+    }
     // h: sum j = r * parts + q is row r of A over the q-th part of K
     const int parts = R >= 64 ? 1 : 64 / R;
     const int chunks = (K + 255) / 256;                     // of 256 k: 8 a lane
@@ -77,30 +85,40 @@ __global__ __cluster_dims__(LD_CTAS, 1, 1) __launch_bounds__(LD_THREADS) void k_
         if (part == 0) h[(int64_t)m * R + r] = v;
     }
     __syncthreads();
-    // t: a thread per n, its row of B 16 bytes at a time
+    // t: three n a thread at a time, their rows of B in 16-byte pieces
     const float c = has ? __ldg(scale + id) : 0.0f;
-    const int64_t n1 = N * (part + 1) / LD_CTAS;
-    for (int64_t n = N * part / LD_CTAS + tid; n < n1; n += LD_THREADS) {
-        float v = 0.0f;
+    constexpr int U = 3;
+    for (int64_t n = n0 + tid; n < n1; n += U * LD_THREADS) {
+        float v[U] = {};
         if (has) {
             const uint16_t* bp = B + ((int64_t)id * N + n) * R;
-#pragma unroll 4
+#pragma unroll 2
             for (int r = 0; r < R; r += 8) {
-                const uint4 b = ldg_keep(bp + r);
+                uint4 b[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    b[u] = n + u * LD_THREADS < n1 ? ldg_keep(bp + (int64_t)u * LD_THREADS * R + r)
+                                                   : make_uint4(0, 0, 0, 0);
                 const float4 h0 = *reinterpret_cast<const float4*>(hs + r);
                 const float4 h1 = *reinterpret_cast<const float4*>(hs + r + 4);
-                v = fmaf(bf16lo(b.x), h0.x, v);
-                v = fmaf(bf16hi(b.x), h0.y, v);
-                v = fmaf(bf16lo(b.y), h0.z, v);
-                v = fmaf(bf16hi(b.y), h0.w, v);
-                v = fmaf(bf16lo(b.z), h1.x, v);
-                v = fmaf(bf16hi(b.z), h1.y, v);
-                v = fmaf(bf16lo(b.w), h1.z, v);
-                v = fmaf(bf16hi(b.w), h1.w, v);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    v[u] = fmaf(bf16lo(b[u].x), h0.x, v[u]);
+                    v[u] = fmaf(bf16hi(b[u].x), h0.y, v[u]);
+                    v[u] = fmaf(bf16lo(b[u].y), h0.z, v[u]);
+                    v[u] = fmaf(bf16hi(b[u].y), h0.w, v[u]);
+                    v[u] = fmaf(bf16lo(b[u].z), h1.x, v[u]);
+                    v[u] = fmaf(bf16hi(b[u].z), h1.y, v[u]);
+                    v[u] = fmaf(bf16lo(b[u].w), h1.z, v[u]);
+                    v[u] = fmaf(bf16hi(b[u].w), h1.w, v[u]);
+                }
             }
-            v *= c;
         }
-        t[(int64_t)m * N + n] = bias ? v + __ldg(bias + n) : v;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t nn = n + u * LD_THREADS;
+            if (nn < n1) t[(int64_t)m * N + nn] = bias ? fmaf(v[u], c, __ldg(bias + nn)) : v[u] * c;
+        }
     }
 }
 

@@ -208,6 +208,9 @@ static inline bool valid_group(int G) { return G == 32 || G == 64 || G == 128 ||
 // ------------------------------------------------------------------ adapters
 constexpr int64_t kMaxAdapters = 1024;
 constexpr int64_t kMaxRank = 256;
+// Largest sizes of the adapter and checkpoint products: row tiles and copy coordinates (two
+// bytes an element) are counted in 32 bits.
+constexpr int64_t kLoraMaxM = 0x7fffff00, kLoraMaxN = 0x3fffffff;
 static inline bool valid_rank(int64_t r) { return r >= 8 && r <= kMaxRank && r % 8 == 0; }
 
 static q8_status check_adapters(const q8_adapters* ad) {
@@ -423,12 +426,14 @@ size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K, int extra) 
         case Q8_OP_GPTQ_INT8:
             if (K > kGptqMaxK || !gptq_block_ok(extra)) return 0;
             return plan_gptq(N, K).bytes;
-        case Q8_OP_CHECKPOINT_WGRAD: return M > 0 ? lora_pre_bytes(K, M, N) : 0;
+        case Q8_OP_CHECKPOINT_WGRAD:
+            if (M > kLoraMaxM || N > kLoraMaxN) return 0;
+            return M > 0 ? lora_pre_bytes(K, M, N) : 0;
         case Q8_OP_LINEAR_W8A16_LORA:
-            if (M > 0x7fffffff || !valid_rank(extra)) return 0;
+            if (M > kLoraMaxM || N > kLoraMaxN || !valid_rank(extra)) return 0;
             return lora_fwd_bytes(M, N, K, extra);
         case Q8_OP_LINEAR_W8A16_LORA_BACKWARD:
-            if (M > 0x7fffffff || !valid_rank(extra)) return 0;
+            if (M > kLoraMaxM || N > kLoraMaxN || !valid_rank(extra)) return 0;
             return plan_lora(true, M, N, K, extra).bytes;
         case Q8_OP_LINEAR_DQ8CA_Q4GSW: {
             if (!valid_group(extra) || K % 128 != 0 || K % extra != 0) return 0;
@@ -445,7 +450,7 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
                                void* y, q8_dtype yt, float* h, int64_t M, int64_t N, int64_t K,
                                void* workspace, size_t ws_bytes, void* stream) {
     if (yt != Q8_F32 && yt != Q8_BF16) return Q8_ERR_ARG;
-    if (M < 0 || M > 0x7fffffff || N < 1 || N > 0x7fffffff) return Q8_ERR_SHAPE;
+    if (M < 0 || M > kLoraMaxM || N < 1 || N > kLoraMaxN) return Q8_ERR_SHAPE;
     Q8_TRY(check_k(K));
     Q8_TRY(check_adapters(ad));
     if (M == 0) return Q8_OK;
@@ -505,7 +510,7 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
                                         float* da, float* db, int accumulate, int64_t M,
                                         int64_t N, int64_t K, void* workspace, size_t ws_bytes,
                                         void* stream) {
-    if (M < 0 || M > 0x7fffffff || N < 1 || N > 0x7fffffff || N % 8) return Q8_ERR_SHAPE;
+    if (M < 0 || M > kLoraMaxM || N < 1 || N > kLoraMaxN || N % 8) return Q8_ERR_SHAPE;
     Q8_TRY(check_k(K));
     Q8_TRY(check_adapters(ad));
     if (da && M > 0) {
@@ -608,7 +613,7 @@ q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t
                               float* dw, int accumulate, int64_t M, int64_t N, int64_t K,
                               void* workspace, size_t ws_bytes, void* stream) {
     if (!valid_group(group)) return Q8_ERR_ARG;
-    if (M < 0 || M > 0x7fffffff || N < 1 || N > 0x7fffffff || N % 8) return Q8_ERR_SHAPE;
+    if (M < 0 || M > kLoraMaxM || N < 1 || N > kLoraMaxN || N % 8) return Q8_ERR_SHAPE;
     Q8_TRY(check_k(K));
     if (K % group) return Q8_ERR_SHAPE;
     if (M == 0 && accumulate) return Q8_OK;

@@ -45,7 +45,7 @@ def _bwd(L, **k):
 
 def test_forward_refusals(L):
     assert _fwd(L, yt=7) == q8.Q8_ERR_ARG
-    for bad in (dict(M=-1), dict(M=1 << 31), dict(N=0), dict(K=40), dict(K=8), dict(K=65536)):
+    for bad in (dict(M=-1), dict(M=1 << 31), dict(M=(1 << 31) - 1), dict(N=1 << 30), dict(N=0), dict(K=40), dict(K=8), dict(K=65536)):
         assert _fwd(L, **bad) == q8.Q8_ERR_SHAPE, bad
     for ad in (_ad(count=0), _ad(count=1025), _ad(rank=0), _ad(rank=4), _ad(rank=20),
                _ad(rank=264)):
