@@ -61,7 +61,7 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
         __syncthreads();
         const int64_t t = (int64_t)(blockIdx.x - 1) * BN + tid;
         if (tid < BN && t < M) {
-            const int id = __ldg(ids + t);
+            const int id = ld_after(ids + t);
             if (id >= 0 && id < L) atomicOr(&seen[id >> 5], 1u << (id & 31));
         }
         __syncthreads();
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int64_t m = (int64_t)(c0 + j) * 1024 + tid;
-            keys[j] = m < M ? __ldg(ids + m) : -1;
+            keys[j] = m < M ? ld_after(ids + m) : -1;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -394,7 +394,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
         slot = (slot + 1) % LSH;
     }
     // h (or g) in fp32, and times the scale in two bf16 parts, [M, 2 R]: high, rest
-    const float f = __ldg(scale + key);
+    const float f = ld_after(scale + key);
     auto put = [&](int row, int r, float v) {
         const int64_t m = ld_after(perm + start + row);
         const float sv = v * f;
@@ -483,7 +483,7 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
     const int steps = (total + LW_ROWS - 1) / LW_ROWS;
     const int s0 = (int)((int64_t)steps * part / S), s1 = (int)((int64_t)steps * (part + 1) / S);
     const uint32_t base = smem_u32(sm);
-    const float f = KIND == 2 && total > 0 ? __ldg(scale + key) : 1.0f;
+    const float f = KIND == 2 && total > 0 ? ld_after(scale + key) : 1.0f;
 
     // thread: row tid >> 3 of a step, 16 of its p, an eighth of its low
     const int xr = tid >> 3, xq = tid & 7;
@@ -506,7 +506,7 @@ __device__ __forceinline__ void lora_grad_tile(const LoraGrad& q, int bx,
             const int8_t* src = reinterpret_cast<const int8_t*>(X) + m * P + p0 + xq * 16;
             const bool in = live && p0 + xq * 16 < P;
             cp_async16(xs + xr * 128 + ((xq ^ (xr & 7)) << 4), in ? (const void*)src : X, in);
-            e = in ? __ldg(exps + m * (P >> gshift) + ((p0 + xq * 16) >> gshift)) : 0u;
+            e = in ? ld_after(exps + m * (P >> gshift) + ((p0 + xq * 16) >> gshift)) : 0u;
         } else {
             // eight neighbouring threads: 128 bytes of a row at a time
             const uint16_t* src = reinterpret_cast<const uint16_t*>(X) + m * P + p0 + xq * 8;

@@ -30,7 +30,7 @@ __global__ __cluster_dims__(LD_CTAS, 1, 1) __launch_bounds__(LD_THREADS) void k_
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int m = blockIdx.y, part = blockIdx.x;            // a row's cluster: its CTAs in order
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int id = __ldg(ids + m);
+    const int id = ld_after(ids + m);
     const bool has = id >= 0 && id < L;
     const int64_t n0 = N * part / LD_CTAS, n1 = N * (part + 1) / LD_CTAS;
     if (has) {
@@ -86,7 +86,7 @@ __global__ __cluster_dims__(LD_CTAS, 1, 1) __launch_bounds__(LD_THREADS) void k_
     }
     __syncthreads();
     // t: three n a thread at a time, their rows of B in 16-byte pieces
-    const float c = has ? __ldg(scale + id) : 0.0f;
+    const float c = has ? ld_after(scale + id) : 0.0f;
     constexpr int U = 3;
     for (int64_t n = n0 + tid; n < n1; n += U * LD_THREADS) {
         float v[U] = {};
@@ -117,7 +117,7 @@ __global__ __cluster_dims__(LD_CTAS, 1, 1) __launch_bounds__(LD_THREADS) void k_
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t nn = n + u * LD_THREADS;
-            if (nn < n1) t[(int64_t)m * N + nn] = bias ? fmaf(v[u], c, __ldg(bias + nn)) : v[u] * c;
+            if (nn < n1) t[(int64_t)m * N + nn] = bias ? fmaf(v[u], c, ld_after(bias + nn)) : v[u] * c;
         }
     }
 }

@@ -180,9 +180,9 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 // raw bits, so that nothing waits on the load before its turn.
 template <int MODE>
 __device__ __forceinline__ uint32_t lt_scale_bits(const LoraGemm& a, int c, int p) {
-    if (MODE == LORA_DGRAD && c < a.C) return __float_as_uint(__ldg(a.s_w + c));
+    if (MODE == LORA_DGRAD && c < a.C) return __float_as_uint(ld_after(a.s_w + c));
     if (MODE == LORA_WGRAD && c < a.C && p < a.P)
-        return __ldg(a.exps + (int64_t)c * (a.P >> a.gshift) + (p >> a.gshift));
+        return ld_after(a.exps + (int64_t)c * (a.P >> a.gshift) + (p >> a.gshift));
     return 0u;
 }
 struct LtScale {
@@ -616,7 +616,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                         const int* list = a.lists + (int64_t)(t0 / BN) * LT_LIST;
                         const int cnt = ld_after(list);
                         const int t = t0 + (int)rank * half + tid;
-                        const int id = tid < half && t < a.T ? __ldg(a.ids + t) : -1;
+                        const int id = tid < half && t < a.T ? ld_after(a.ids + t) : -1;
                         const int pr = tid >> 4, pc = tid & 15;     // A_MN: row and 8 p of a piece
                         const int p = A_MN ? p0 + pc * 8 : p0 + tid;
                         int ad[8];
@@ -685,8 +685,8 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
             const bool low = MODE == LORA_FWD && more(w, t0);
             float sw = 1.0f, bs = 0.0f;
             if (MODE == LORA_FWD && p < a.P) {
-                sw = __ldg(a.s_w + p);
-                if (a.bias) bs = __ldg(a.bias + p);
+                sw = ld_after(a.s_w + p);
+                if (a.bias) bs = ld_after(a.bias + p);
             }
             const LtRing<2> r1 = rt;
             rt.next();
@@ -785,8 +785,8 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
             w.kb = w.end;
             low = MODE == LORA_FWD && more(w, t0);
             if (MODE == LORA_FWD && p < a.P) {
-                sw = __ldg(a.s_w + p);
-                if (a.bias) bs = __ldg(a.bias + p);
+                sw = ld_after(a.s_w + p);
+                if (a.bias) bs = ld_after(a.bias + p);
             }
             bool okw = mbar_wait(&tfull[0], 0, status, abort_flag);
             if (low) okw = mbar_wait(&tfull[1], 0, status, abort_flag) && okw;

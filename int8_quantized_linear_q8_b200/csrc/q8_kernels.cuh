@@ -69,9 +69,10 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Loads of what an earlier kernel of a chain of programmatic dependent launches wrote: volatile,
-// so that none is moved ahead of the griddepcontrol.wait before it (a __ldg is taken to read
-// memory that never changes).
+// Loads of what an earlier kernel may have written, in kernels that start before it ends
+// (programmatic dependent launch): volatile, so that none is moved ahead of the
+// griddepcontrol.wait before it, as the compiler may a __ldg, which it takes to read memory that
+// never changes.
 __device__ __forceinline__ int ld_after(const int* p) {
     int v;
     asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -80,6 +81,11 @@ __device__ __forceinline__ int ld_after(const int* p) {
 __device__ __forceinline__ float ld_after(const float* p) {
     float v;
     asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_after(const uint8_t* p) {
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
 __device__ __forceinline__ float4 ld_after4(const float* p) {
