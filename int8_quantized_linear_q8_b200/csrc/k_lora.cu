@@ -45,16 +45,14 @@ const int* lora_plan_lists(const void* ws) { return reinterpret_cast<const int*>
 __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ ids, int M, int L,
                                                     int BN, int* __restrict__ lists, int list_len,
                                                     int* __restrict__ perm, int* __restrict__ off,
-                                                    int* __restrict__ tiles, bool beside) {
+                                                    int* __restrict__ tiles) {
     __shared__ int cnt[LP_KEYS + 1], pos[LP_KEYS + 1], tpos[LP_KEYS + 1];
     __shared__ int wsum[2][32];
     __shared__ __align__(16) uint8_t part[32][LP_KEYS + 3];     // rows of a key in each warp
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // beside: the kernel before this one is the weight's expansion, which does not touch what is
-    // read or written here; it was launched after all of the stream's earlier work, so there
-    // is nothing to wait for but at the end, for whoever waits for this kernel.
+    // launched after all of the stream's earlier work (no early start): the kernels behind it
+    // that start early rely on it
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x > 0) {
         uint32_t* seen = reinterpret_cast<uint32_t*>(cnt);
         if (tid < 32) seen[tid] = 0;
@@ -83,7 +81,6 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
                 out[1 + before++] = tid * 32 + b;
             }
         }
-        if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     for (int i = tid; i <= L; i += 1024) cnt[i] = 0;
@@ -188,27 +185,17 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
             __syncthreads();
         }
     }
-    if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-cudaError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, void* ws, bool beside,
-                             cudaStream_t st) {
+cudaError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, void* ws, cudaStream_t st) {
     const LoraPlan p = plan_of(M);
     uint8_t* w = (uint8_t*)ws;
     const int BN = lora_tc_tile(M);
     const unsigned grid = 1 + (unsigned)((M + BN - 1) / BN);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = beside ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_lora_plan, ids, (int)M, L, BN, (int*)(w + p.lists),
-                              (int)LT_LIST, (int*)(w + p.perm), (int*)(w + p.off),
-                              (int*)(w + p.tiles), beside);
+    k_lora_plan<<<grid, 1024, 0, st>>>(ids, (int)M, L, BN, (int*)(w + p.lists), LT_LIST,
+                                       (int*)(w + p.perm), (int*)(w + p.off),
+                                       (int*)(w + p.tiles));
+    return cudaGetLastError();
 }
 
 // --------------------------------------------------------------------- shared pieces

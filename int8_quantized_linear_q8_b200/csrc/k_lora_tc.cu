@@ -961,7 +961,7 @@ cudaError_t launch_lora_tc(int mode, const LoraGemm& a, cudaStream_t st, int num
 // (dgrad), or code * 2^e.
 template <int MODE>
 __global__ __launch_bounds__(256) void k_lora_expand(const LoraGemm a, int64_t n16, int row16,
-                                                     uint16_t* __restrict__ out) {
+                                                     uint16_t* __restrict__ out, bool beside) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t i0 = (int64_t)blockIdx.x * 512 + threadIdx.x;
     uint4 w[2];
@@ -988,6 +988,10 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraGemm a, int64_t n
         to[0] = make_uint4(o[0], o[1], o[2], o[3]);
         to[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
+    // beside the kernels that make h or g: it neither reads nor writes what they do, and what it
+    // reads is older than the plan, whose launch waited for all of the stream's earlier work.
+    // Who waits for this kernel waits for those too: its last block does.
+    if (beside && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // The expansion moves 3 bytes a value and is a launch more; the conversion inside the GEMM costs
@@ -1000,19 +1004,24 @@ size_t lora_pre_bytes(int64_t P, int64_t C, int64_t T) {
     return T >= LT_PRE_T && 2.0 * (double)P * (double)C * (double)T >= LT_PRE_FLOPS
                ? (size_t)P * (size_t)C * 2 : 0;
 }
-cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, cudaStream_t st) {
+cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, bool beside,
+                               cudaStream_t st) {
     const int64_t n16 = (int64_t)a.P * a.C / 16;
     const int row16 = (mode == LORA_FWD ? a.C : a.P) / 16;
-    // launched after all of the stream's earlier work (no early start): the plan beside it and
-    // the kernels after that rely on it
-    const unsigned grid = (unsigned)((n16 + 511) / 512);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((n16 + 511) / 512));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = beside ? 1 : 0;
     if (mode == LORA_FWD)
-        k_lora_expand<LORA_FWD><<<grid, 256, 0, st>>>(a, n16, row16, out);
-    else if (mode == LORA_DGRAD)
-        k_lora_expand<LORA_DGRAD><<<grid, 256, 0, st>>>(a, n16, row16, out);
-    else
-        k_lora_expand<LORA_WGRAD><<<grid, 256, 0, st>>>(a, n16, row16, out);
-    return cudaGetLastError();
+        return cudaLaunchKernelEx(&cfg, k_lora_expand<LORA_FWD>, a, n16, row16, out, beside);
+    if (mode == LORA_DGRAD)
+        return cudaLaunchKernelEx(&cfg, k_lora_expand<LORA_DGRAD>, a, n16, row16, out, beside);
+    return cudaLaunchKernelEx(&cfg, k_lora_expand<LORA_WGRAD>, a, n16, row16, out, beside);
 }
 
 }  // namespace q8

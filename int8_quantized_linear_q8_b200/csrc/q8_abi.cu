@@ -494,13 +494,13 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     a.lists = lora_plan_lists(ws + w.plan);
     a.R = R;
     a.L = L;
-    if (w.pre_bytes) {
-        Q8_TRY(launched(launch_lora_expand(LORA_FWD, a, (uint16_t*)(ws + w.pre), st)));
-        a.pre = (const uint16_t*)(ws + w.pre);
-    }
-    Q8_TRY(launched(launch_lora_plan(ids, M, L, ws + w.plan, w.pre_bytes > 0, st)));
+    Q8_TRY(launched(launch_lora_plan(ids, M, L, ws + w.plan, st)));
     Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
                                        ad->scale, ws + w.plan, h, hp, M, (int)K, R, L, st, sms)));
+    if (w.pre_bytes) {
+        Q8_TRY(launched(launch_lora_expand(LORA_FWD, a, (uint16_t*)(ws + w.pre), true, st)));
+        a.pre = (const uint16_t*)(ws + w.pre);
+    }
     return launched(launch_lora_tc(LORA_FWD, a, st, sms, status));
 }
 
@@ -561,15 +561,14 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
     a.lists = lora_plan_lists(plan);
     a.R = R;
     a.L = L;
-    const bool pre = dx && w.pre_bytes;
-    if (pre) {
-        Q8_TRY(launched(launch_lora_expand(LORA_DGRAD, a, (uint16_t*)(ws + w.pre), st)));
-        a.pre = (const uint16_t*)(ws + w.pre);
-    }
-    Q8_TRY(launched(launch_lora_plan(ids, M, L, plan, pre, st)));
+    Q8_TRY(launched(launch_lora_plan(ids, M, L, plan, st)));
     if (dx || da)
         Q8_TRY(launched(launch_lora_shrink(true, (const uint16_t*)dy, (const uint16_t*)ad->b,
                                            ad->scale, plan, g, hp, M, (int)N, R, L, st, sms)));
+    if (dx && w.pre_bytes) {
+        Q8_TRY(launched(launch_lora_expand(LORA_DGRAD, a, (uint16_t*)(ws + w.pre), true, st)));
+        a.pre = (const uint16_t*)(ws + w.pre);
+    }
     if (dx) Q8_TRY(launched(launch_lora_tc(LORA_DGRAD, a, st, sms, status)));
     if (da || db)
         Q8_TRY(launched(launch_lora_wgrad(
@@ -638,7 +637,8 @@ q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t
     a.C = (int)M;
     a.T = N;
     if (need) {
-        Q8_TRY(launched(launch_lora_expand(LORA_WGRAD, a, (uint16_t*)workspace, st)));
+        Q8_TRY(launched(launch_lora_expand(LORA_WGRAD, a, (uint16_t*)workspace, false,
+                                           st)));
         a.pre = (const uint16_t*)workspace;
     }
     return launched(launch_lora_tc(LORA_WGRAD, a, st, sms, status));

@@ -222,9 +222,7 @@ struct LoraGemm {
 };
 size_t lora_plan_bytes(int64_t M);               // workspace of the plan
 const int* lora_plan_lists(const void* ws);
-// beside: right behind launch_lora_expand on the stream, and at the same time
-cudaError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, void* ws, bool beside,
-                             cudaStream_t st);
+cudaError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, void* ws, cudaStream_t st);
 // h (or, backward, g) of every row, and its two bf16 parts hp [M, 2 R]; ws: the plan of its ids
 cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, const float* scale,
                                const void* ws, float* h, uint16_t* hp, int64_t M, int C, int R,
@@ -240,7 +238,9 @@ cudaError_t launch_lora_wgrad(const void* dy, const float* h, float* db, const v
 constexpr int LT_LIST = 260;
 int lora_tc_tile(int64_t T);                    // tokens per tile
 size_t lora_pre_bytes(int64_t P, int64_t C, int64_t T);     // of the expansion; 0: none
-cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, cudaStream_t st);
+// beside: right behind launch_lora_shrink on the stream, and at the same time
+cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, bool beside,
+                               cudaStream_t st);
 size_t lora_list_bytes(int64_t T);
 cudaError_t launch_lora_tc(int mode, const LoraGemm& a, cudaStream_t st, int num_sms,
                            int* status);
