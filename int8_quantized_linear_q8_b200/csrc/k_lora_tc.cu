@@ -27,7 +27,18 @@
 // Two variants.  PRE: the int8 operand was expanded to bf16 in the workspace beforehand
 // (k_lora_expand) and both operands come by TMA.  Otherwise it stays int8 in HBM and L2 and the
 // kernel converts it, which costs nothing extra to read but adds 24 KB of shared-memory traffic
-// to the 64 KB that a stage and CTA move anyway, more than the port carries in the MMAs' time.
+// to the 64 KB that a stage and CTA move anyway, more than the port carries in the MMAs' time
+// (4096 x 11008 x 4096: about 500 ns a stage against 360 expanded).
+//
+// What bounds it, measured on the expanded form (cycles a stage of 64 c; its MMAs take 512): dgrad
+// 538, tensor pipe active 91% of the time a pair has work; forward 608 (the adapter term's
+// second accumulator, drained between tiles); weight gradient 715 before its stores were
+// streamed past L2.  dgrad of 4096 x 11008 x 4096: 250 us, 1.48 PFLOP/s, of which the fourth round
+// of tiles, which 34 of 74 pairs have, costs 13%.  Two things cost most on the way: cluster-scope
+// acquire and release on the hand-offs (538 -> 328 us), and everything on the issuing warp's
+// path between two stages.  Not kept: a second launch that splits the last round's tiles over
+// clusters of two pairs (only 32 such clusters run at once; the exchange costs what it saves),
+// L2 evict-last hints on the operands (no change), t blocks of 16 and 64 tiles (1% and 8% slower).
 //
 // Few tiles (fewer than half the CTA pairs): S = 2 or 4 pairs of one cluster split a tile's
 // stages; each owns 1 / S of the tile's columns and adds the other pairs' parts, which they
@@ -36,9 +47,8 @@
 // Roles (15 warps): 0 and 2 TMA producers of the int8 and the bf16 operands; 1 tensor-memory
 // allocator and, in the pair's first CTA, MMA issuer; then converters, two groups of four that
 // take every other stage (PRE: one group, for the adapter columns), and four epilogue warps
-// (PRE: eight).  A stage is 64 of c.  Its int8 box (8 KB) has
-// a ring of its own, eight deep: that path is the longest (copy, conversion, MMA) and runs
-// ahead.  Its P tile and its T tile (16 KB each) share a slot of a ring of five (PRE: seven), so
+// (PRE: eight).  A stage is 64 of c.  Its int8 box (8 KB) has a ring of its own, eight deep: that
+// path is the longest (copy, conversion, MMA) and runs ahead.  Its P tile and its T tile (16 KB each) share a slot of a ring of five (PRE: seven), so
 // that the issuing warp, whose own steps bound the main loop, has one barrier to wait for
 // and one commit to make per stage; it tests the next stage's barrier before it issues this
 // stage's MMAs, which hides the test.  Every wait is bounded.
@@ -53,7 +63,7 @@ __host__ __device__ constexpr int lt_slots(bool pre) { return pre ? 7 : 5; }
 constexpr int LT_SLOT = LT_A + LT_B, LT_RT = 5 * LT_SLOT;
 constexpr int LT_CTRL = LT_RT + LT_NR * LT_RAW;
 static_assert(LT_CTRL >= LT_N_MAX * LT_SLOT, "PRE uses the whole region for its slots");
-// warps: 15, which leaves each thread 128 registers (19 would leave 96, and spills)
+// warps: 15, which leaves each thread 128 registers (19 would leave 96)
 __host__ __device__ constexpr int lt_conv(bool pre) { return pre ? 4 : 8; }
 __host__ __device__ constexpr int lt_epi(bool pre) { return pre ? 8 : 4; }
 constexpr int LT_CONV0 = 3;

@@ -1,6 +1,9 @@
 """Refusals of the adapter and checkpoint entry points: every documented status code comes
 from the arguments alone, before any device work (no GPU needed)."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -136,6 +139,18 @@ def test_checkpoint_refusals(L):
     assert wg(M=4096, N=65536) == q8.Q8_ERR_WORKSPACE
     assert wg(M=4096, N=65536, ws=GOOD, wsb=need - 1) == q8.Q8_ERR_WORKSPACE
     assert wg(M=4096, N=65536, ws=ODD, wsb=need) == q8.Q8_ERR_ALIGN
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
+def test_c99_caller(tmp_path, L):
+    here = os.path.dirname(os.path.abspath(__file__))
+    libdir, exe = os.path.dirname(q8.LIB_PATH), str(tmp_path / "c_abi_lora_check")
+    subprocess.check_call(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic",
+                           "-I", os.path.join(os.path.dirname(here), "include"),
+                           os.path.join(here, "c_abi_lora_check.c"), "-L", libdir, "-lq8",
+                           "-Wl,-rpath," + libdir, "-o", exe])
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0 and "failures: 0" in out.stdout, out.stdout + out.stderr
 
 
 def test_binding_refuses_cpu_tensors():
