@@ -80,6 +80,14 @@ struct LtRing {
     __device__ __forceinline__ void next() {
         if (++s == N) { s = 0; ph ^= 1u; }
     }
+    __device__ __forceinline__ void next2() {
+        if ((s += 2) >= N) { s -= N; ph ^= 1u; }
+    }
+    __device__ __forceinline__ void skip(int n) {
+        n += s;
+        s = n % N;
+        ph ^= (uint32_t)(n / N) & 1u;
+    }
 };
 
 // ------------------------------------------------------------------ cluster and tcgen05
@@ -220,50 +228,66 @@ __device__ __forceinline__ uint32_t lt_apply(uint32_t v, const LtScale& s) {
 
 // ------------------------------------------------------------------------- the kernel
 // Writes W columns (t0 + j, those below t1) of this lane's p: v + bias.  All lanes of the warp
-// call it.
-template <int MODE, int W>
-__device__ __forceinline__ void lt_store(const LoraGemm& a, int t0, int64_t t1, int p, float bs,
-                                         float (&v)[W]) {
+// call it.  Whole chunks go without a test or a product per store: with them a weight
+// gradient's tile took 5.7 us to write, without 2.9 (40 x 11008 x 4096: 62 -> 32.5 us a call).
+template <int MODE, int W, bool FULL>
+__device__ __forceinline__ void lt_store_rows(const LoraGemm& a, int t0, int rows, int p,
+                                              float (&v)[W]) {
     const int lane = threadIdx.x & 31;
-    if (MODE == LORA_FWD)
-#pragma unroll
-        for (int j = 0; j < W; ++j) v[j] += bs;
+    const int64_t step = a.P;
     if (MODE != LORA_WGRAD && a.out_bf16 && (a.P & 1) == 0) {
         // neighbouring lanes exchange, so that each stores two p of one t
-        uint32_t* out = reinterpret_cast<uint32_t*>(a.out);
+        const int od = lane & 1;
+        uint32_t* out = reinterpret_cast<uint32_t*>(a.out) + (((t0 + od) * step + (p & ~1)) >> 1);
 #pragma unroll
         for (int j = 0; j < W; j += 2) {
-            const bool od = lane & 1;
             const float got = __shfl_xor_sync(0xffffffffu, od ? v[j] : v[j + 1], 1);
             const uint32_t lo = bf16_bits_rn(od ? got : v[j]);
             const uint32_t hi = bf16_bits_rn(od ? v[j + 1] : got);
-            const int64_t t = t0 + j + (od ? 1 : 0);
-            if (t < t1 && p < a.P) out[(t * a.P + (p & ~1)) >> 1] = lo | hi << 16;
+            if ((FULL || j + od < rows) && p < a.P) *out = lo | hi << 16;
+            out += step;
         }
     } else if (MODE != LORA_WGRAD && a.out_bf16) {
-        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + t0 * step + p;
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            if (t0 + j < t1 && p < a.P)
-                out[(int64_t)(t0 + j) * a.P + p] = __float2bfloat16_rn(v[j]);
-    } else {
-        float* out = reinterpret_cast<float*>(a.out) + (int64_t)t0 * a.P + p;
+        for (int j = 0; j < W; ++j) {
+            if ((FULL || j < rows) && p < a.P) *out = __float2bfloat16_rn(v[j]);
+            out += step;
+        }
+    } else if (p < a.P) {
+        float* out = reinterpret_cast<float*>(a.out) + t0 * step + p;
         if (MODE == LORA_WGRAD && a.accumulate) {
+            const float* in = out;
 #pragma unroll
-            for (int j = 0; j < W; ++j)
-                if (t0 + j < t1 && p < a.P) v[j] += out[(int64_t)j * a.P];
+            for (int j = 0; j < W; ++j) {
+                if (FULL || j < rows) v[j] += *in;
+                in += step;
+            }
         }
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            if (t0 + j < t1 && p < a.P) {
+        for (int j = 0; j < W; ++j) {
+            if (FULL || j < rows) {
                 // a weight gradient is larger than L2 can hold beside the operands: streamed past
                 // them (wgrad 4096 x 11008 x 4096: 292 -> 275 us)
                 if (MODE == LORA_WGRAD)
-                    st_stream_f32(out + (int64_t)j * a.P, v[j]);
+                    st_stream_f32(out, v[j]);
                 else
-                    out[(int64_t)j * a.P] = v[j];
+                    *out = v[j];
             }
+            out += step;
+        }
     }
+}
+template <int MODE, int W>
+__device__ __forceinline__ void lt_store(const LoraGemm& a, int t0, int64_t t1, int p, float bs,
+                                         float (&v)[W]) {
+    if (MODE == LORA_FWD)
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[j] += bs;
+    if (t0 + W <= t1)
+        lt_store_rows<MODE, W, true>(a, t0, W, p, v);
+    else
+        lt_store_rows<MODE, W, false>(a, t0, (int)(t1 - t0), p, v);
 }
 
 template <int MODE, bool PRE>
@@ -527,97 +551,112 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
         for (int u = u0; u < units; u += ustep) {
             int p0, t0;
             tile_of(u, p0, t0);
-            const int sc = tid >> 3, sp = p0 + (tid & 7) * 16;     // this thread's first c, its p
-            uint32_t nxt[4];                            // the next turn's scales
-            if (A_MN && !PRE) {
-                const int kb = walk().kb + (it % GROUPS == grp ? 0 : 1);    // GROUPS == 2 here
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    nxt[i] = lt_scale_bits<MODE>(a, kb * LT_BK + i * 16 + sc, sp);
-            }
             Walk w = walk();
             if (PRE) {                                  // the base stages are not theirs
                 for (; w.kb < w.end; ++w.kb) r.next();
+            } else {
+                // Base stages: this group's are every other one.  A loop of its own, without
+                // the adapter columns' bookkeeping: with few rows, what a group does between two
+                // stages is what a stage takes (77 rows, 2048 x 8192: 0.57 us a stage before).
+                const int sc = tid >> 3, sp = p0 + (tid & 7) * 16;  // this thread's first c, its p
+                const int n = w.end - w.kb, skip = (it ^ grp) & 1;  // GROUPS == 2 here
+                int kb = w.kb + skip;
+                LtRing<LT_N> rc = r;
+                LtRing<LT_NR> rq = rr;
+                if (skip) {
+                    rc.next();
+                    rq.next();
+                }
+                uint32_t nxt[4];                        // the next turn's scales
+                if (A_MN)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        nxt[i] = lt_scale_bits<MODE>(a, kb * LT_BK + i * 16 + sc, sp);
+#pragma unroll 1
+                for (; kb < w.end; kb += 2) {
+                    const uint32_t raw = smem_u32(smem + LT_RT + rq.s * LT_RAW);
+                    live = mbar_wait(&rfull[rq.s], rq.ph, status, abort_flag) && live;
+                    uint4 cw[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        cw[i] = A_MN ? lds128(raw + (i * 16 + sc) * 128 + (tid & 7) * 16)
+                                    : lds128(raw + tid * 64 + ((i ^ ((tid >> 1) & 3)) << 4));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&rempty[rq.s]);          // codes in registers
+                    rq.next2();
+                    uint32_t cur[4];
+                    if (A_MN) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+                        if (kb + 2 < w.end)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                nxt[i] = lt_scale_bits<MODE>(a, (kb + 2) * LT_BK + i * 16 + sc, sp);
+                    }
+                    // converted in registers first: what lies between a free tile and
+                    // its hand-over is on the ring's critical path
+                    uint32_t o[4][8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s8x4_to_bf16x2_seq(cw[i].x, o[i][0], o[i][1]);
+                        s8x4_to_bf16x2_seq(cw[i].y, o[i][2], o[i][3]);
+                        s8x4_to_bf16x2_seq(cw[i].z, o[i][4], o[i][5]);
+                        s8x4_to_bf16x2_seq(cw[i].w, o[i][6], o[i][7]);
+                        if (A_MN) {
+                            const LtScale f = lt_scale<MODE>(cur[i]);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) o[i][j] = lt_apply<MODE>(o[i][j], f);
+                        }
+                    }
+                    const uint32_t at = smem_u32(smem + rc.s * LT_SLOT);
+                    live = mbar_wait(&empty[rc.s], rc.ph ^ 1u, status, abort_flag) && live;
+                    if (live) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (!A_MN) {
+                                // thread: row tid, 64 codes
+                                const uint32_t row = at + tid * 128;
+                                sts128(row + (((2 * i) ^ (tid & 7)) << 4), o[i][0], o[i][1],
+                                       o[i][2], o[i][3]);
+                                sts128(row + (((2 * i + 1) ^ (tid & 7)) << 4), o[i][4], o[i][5],
+                                       o[i][6], o[i][7]);
+                            } else {
+                                // thread: 16 codes of p in each of 4 rows of c, two 16-byte
+                                // pieces; lanes of the second 64-p block write theirs in the
+                                // other order, which keeps a row's lanes on different banks
+                                const int ch = tid & 7, odd = ch >> 2, c = i * 16 + sc;
+                                const uint32_t row = at + odd * 8192 + c * 128;
+                                const int j0 = (ch & 3) * 2;
+                                sts128(row + (((j0 + odd) ^ (c & 7)) << 4),
+                                       odd ? o[i][4] : o[i][0], odd ? o[i][5] : o[i][1],
+                                       odd ? o[i][6] : o[i][2], odd ? o[i][7] : o[i][3]);
+                                sts128(row + (((j0 + 1 - odd) ^ (c & 7)) << 4),
+                                       odd ? o[i][0] : o[i][4], odd ? o[i][1] : o[i][5],
+                                       odd ? o[i][2] : o[i][6], odd ? o[i][3] : o[i][7]);
+                            }
+                        }
+                    }
+                    hand_over(rc.s);
+                    rc.next2();
+                }
+                r.skip(n);
+                rr.skip(n);
+                it += n;
+                w.kb = w.end;
             }
+            // Adapter columns: both tiles are written here.  (PRE: the producer says when the
+            // slot is free; who has not followed every phase of `empty` cannot tell one from the
+            // one before the last.)
             for (; more(w, t0); ++w.kb) {
                 const int kb = w.kb;
                 if (it % GROUPS == grp) {
                     const uint32_t at = smem_u32(smem + r.s * LT_SLOT);
-                    if (!PRE && kb < nk) {
-                        const uint32_t raw = smem_u32(smem + LT_RT + rr.s * LT_RAW);
-                        bool okw = mbar_wait(&rfull[rr.s], rr.ph, status, abort_flag);
-                        live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
-                        uint4 cw[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            cw[i] = A_MN ? lds128(raw + (i * 16 + sc) * 128 + (tid & 7) * 16)
-                                        : lds128(raw + tid * 64 + ((i ^ ((tid >> 1) & 3)) << 4));
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&rempty[rr.s]);      // codes in registers
-                        uint32_t cur[4];
-                        if (A_MN) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
-                            if (kb + 2 < nk)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    nxt[i] =
-                                        lt_scale_bits<MODE>(a, (kb + 2) * LT_BK + i * 16 + sc, sp);
-                        }
-                        // converted in registers first: what lies between a free tile and
-                        // its hand-over is on the ring's critical path
-                        uint32_t o[4][8];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            s8x4_to_bf16x2_seq(cw[i].x, o[i][0], o[i][1]);
-                            s8x4_to_bf16x2_seq(cw[i].y, o[i][2], o[i][3]);
-                            s8x4_to_bf16x2_seq(cw[i].z, o[i][4], o[i][5]);
-                            s8x4_to_bf16x2_seq(cw[i].w, o[i][6], o[i][7]);
-                            if (A_MN) {
-                                const LtScale f = lt_scale<MODE>(cur[i]);
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) o[i][j] = lt_apply<MODE>(o[i][j], f);
-                            }
-                        }
-                        okw = mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag);
-                        live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
-                        if (live) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if (!A_MN) {
-                                    // thread: row tid, 64 codes
-                                    const uint32_t row = at + tid * 128;
-                                    sts128(row + (((2 * i) ^ (tid & 7)) << 4), o[i][0], o[i][1],
-                                           o[i][2], o[i][3]);
-                                    sts128(row + (((2 * i + 1) ^ (tid & 7)) << 4), o[i][4],
-                                           o[i][5], o[i][6], o[i][7]);
-                                } else {
-                                    // thread: 16 codes of p in each of 4 rows of c, two 16-byte
-                                    // pieces; lanes of the second 64-p block write theirs in the
-                                    // other order, which keeps a row's lanes on different banks
-                                    const int ch = tid & 7, odd = ch >> 2, c = i * 16 + sc;
-                                    const uint32_t row = at + odd * 8192 + c * 128;
-                                    const int j0 = (ch & 3) * 2;
-                                    sts128(row + (((j0 + odd) ^ (c & 7)) << 4),
-                                           odd ? o[i][4] : o[i][0], odd ? o[i][5] : o[i][1],
-                                           odd ? o[i][6] : o[i][2], odd ? o[i][7] : o[i][3]);
-                                    sts128(row + (((j0 + 1 - odd) ^ (c & 7)) << 4),
-                                           odd ? o[i][0] : o[i][4], odd ? o[i][1] : o[i][5],
-                                           odd ? o[i][2] : o[i][6], odd ? o[i][3] : o[i][7]);
-                                }
-                            }
-                        }
-                    } else {
-                        // Adapter columns: both tiles are written here.  (PRE: the producer says
-                        // when the slot is free; who has not followed every phase of `empty`
-                        // cannot tell one from the one before the last.)
-                        const bool okw =
-                            PRE ? mbar_wait(&lgo[r.s], lph >> r.s & 1u, status, abort_flag)
-                                : mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag);
-                        lph ^= 1u << r.s;
-                        live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
-                    }
-                    if (MODE != LORA_WGRAD && live && kb >= nk) {
+                    const bool okw =
+                        PRE ? mbar_wait(&lgo[r.s], lph >> r.s & 1u, status, abort_flag)
+                            : mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag);
+                    lph ^= 1u << r.s;
+                    live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
+                    if (live) {
                         // Columns (kb - nk) * 64 .. +64 of the adapter term, in pieces of 8:
                         // per adapter of the list R / 8 pieces against the high parts and
                         // R / 8 against the rest.
@@ -652,20 +691,15 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                                            tl ? a.hp + (int64_t)t * 2 * a.R + in * 8 : a.hp, tl);
                         }
                     }
-                    if (MODE != LORA_WGRAD && kb >= nk) {
-                        // handed over a turn later, when the next copies are on their way
-                        cp_commit();
-                        if (pending >= 0) {
-                            cp_wait<1>();
-                            hand_over(pending);
-                        }
-                        pending = r.s;
-                    } else {
-                        hand_over(r.s);
+                    // handed over a turn later, when the next copies are on their way
+                    cp_commit();
+                    if (pending >= 0) {
+                        cp_wait<1>();
+                        hand_over(pending);
                     }
+                    pending = r.s;
                 }
                 ++it;
-                if (!PRE && kb < nk) rr.next();
                 r.next();
             }
             if (pending >= 0) {
@@ -747,20 +781,23 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 }
                 free_sums();
                 held = false;
-                uint32_t* out = reinterpret_cast<uint32_t*>(a.out);
-                const bool od = lane & 1;
+                const int od = lane & 1;
+                const int64_t step = a.P;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = par + 2 * i;
                     if (!live || c >= chunks) continue;
+                    const int rows = (int)min((int64_t)32, t1 - t0 - c * 32) - od;
+                    uint32_t* out = reinterpret_cast<uint32_t*>(a.out) +
+                                    (((t0 + c * 32 + od) * step + (p & ~1)) >> 1);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         // neighbouring lanes exchange, so that each stores two p of one t
                         const uint32_t got = __shfl_xor_sync(0xffffffffu, w[i][j], 1);
                         const uint32_t two = od ? __byte_perm(got, w[i][j], 0x7632)
                                                 : __byte_perm(w[i][j], got, 0x5410);
-                        const int64_t t = t0 + c * 32 + 2 * j + (od ? 1 : 0);
-                        if (t < t1 && p < a.P) out[(t * a.P + (p & ~1)) >> 1] = two;
+                        if (2 * j < rows && p < a.P) *out = two;
+                        out += step;
                     }
                 }
             } else {
