@@ -362,9 +362,6 @@ __global__ __launch_bounds__(WT_THREADS, 1) void k_w8a16_tma(
             }
     };
     for (int rg = rg0; rg < rg1; ++rg) {
-        // loaded ahead of their use, but for the first row group's: those are waited for
-        // when its sums are done
-        if (LOW && rg > rg0) load_terms(rg);
         float acc[CH][MT][4];
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -440,8 +437,10 @@ __global__ __launch_bounds__(WT_THREADS, 1) void k_w8a16_tma(
         // the WT_CONSUMERS partials in warp order (no float atomics, so the sum is the same
         // on every run), scales and writes y.  Slots rotate, so no barrier is needed: a
         // warp can run at most `stages` stages (nslots - 2 groups) ahead of the slowest one.
-        if (LOW && rg == rg0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (LOW) {
+            // on their way while the partial sums meet (loaded at the group's start, they took
+            // 12 registers of the loop and 0.6 us of a 20 us call)
+            if (rg == rg0) asm volatile("griddepcontrol.wait;" ::: "memory");
             load_terms(rg);
         }
         float* sl = slots + (size_t)slot * WT_CONSUMERS * MT * 128;

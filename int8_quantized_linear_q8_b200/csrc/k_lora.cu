@@ -778,6 +778,33 @@ cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, c
 #undef LORA_SHRINK_NT
 }
 
+// CTAs of the gradients' kernel that an SM takes, asked for once per device
+template <int NT, int KIND>
+static int lora_wgrad_occupancy() {
+    static std::atomic<int> known[128];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) {
+        cudaGetLastError();
+        return 1;
+    }
+    n = known[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (ensure_dyn_smem<k_lora_wgrad<NT, KIND>>(lw_smem<NT>()) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_lora_wgrad<NT, KIND>, LW_THREADS,
+                                                      lw_smem<NT>()) != cudaSuccess) {
+        cudaGetLastError();
+        return 1;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+static int lora_wgrad_per_sm(int NT, bool codes) {
+    if (NT == 1) return codes ? lora_wgrad_occupancy<1, 1>() : lora_wgrad_occupancy<1, 0>();
+    if (NT == 2) return codes ? lora_wgrad_occupancy<2, 1>() : lora_wgrad_occupancy<2, 0>();
+    if (NT == 4) return codes ? lora_wgrad_occupancy<4, 1>() : lora_wgrad_occupancy<4, 0>();
+    return codes ? lora_wgrad_occupancy<8, 1>() : lora_wgrad_occupancy<8, 0>();
+}
+
 cudaError_t launch_lora_wgrad(const void* dy, const float* h, float* db, const void* x,
                               const uint8_t* exps, int gshift, const float* g, float* da,
                               const float* scale, const void* ws, int accumulate, int64_t M, int N,
@@ -790,14 +817,12 @@ cudaError_t launch_lora_wgrad(const void* dy, const float* h, float* db, const v
     LoraGrad gb = {dy, h, db, N, db ? (N + 127) / 128 : 0};
     LoraGrad ga = {x, g, da, K, da ? (K + 127) / 128 : 0};
     // parts of an adapter's rows: as many CTAs as run at once, at least 64 rows each if the
-    // adapters share the batch evenly
-    const int smem = NT == 1 ? lw_smem<1>() : NT == 2 ? lw_smem<2>() : NT == 4 ? lw_smem<4>()
-                                                                           : lw_smem<8>();
-    const int64_t at_once = (int64_t)(227 * 1024 / (smem + 1024)) * num_sms;
+    // adapters share the batch evenly (1000 rows of one adapter, 2048 x 8192, rank 64, in 3 parts,
+    // 2 CTAs an SM: X_US us; in 4, which do not all run at once: 33)
+    const int64_t ctas = (int64_t)(gb.blocks + ga.blocks) * z * L;
+    const int64_t at_once = (int64_t)lora_wgrad_per_sm(NT, exps != nullptr) * num_sms;
     int S = 1;
-    while (S < 8 && (int64_t)(gb.blocks + ga.blocks) * z * L * 2 * S <= at_once &&
-           M / L / (2 * S) >= 64)
-        S *= 2;
+    while (S < 8 && ctas * (S + 1) <= at_once && M / L / (S + 1) >= 64) ++S;
     gb.blocks *= S;
     ga.blocks *= S;
     const dim3 grid(gb.blocks + ga.blocks, z, L);

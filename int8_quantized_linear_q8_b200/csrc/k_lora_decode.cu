@@ -130,6 +130,7 @@ __global__ __cluster_dims__(LD_CTAS, 1, 1) __launch_bounds__(LD_THREADS) void k_
 cudaError_t launch_lora_decode(const uint16_t* x, const uint16_t* A, const uint16_t* B,
                                const float* scale, const float* bias, const int32_t* ids, float* h,
                                float* t, int M, int64_t N, int K, int R, int L, cudaStream_t st) {
+    prefer_shared_memory<k_lora_decode>();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(LD_CTAS, M);
     cfg.blockDim = dim3(LD_THREADS);

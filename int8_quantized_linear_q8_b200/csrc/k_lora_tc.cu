@@ -1041,14 +1041,22 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraGemm a, int64_t n
     if (beside && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// The expansion moves 3 bytes a value and is a launch more; the conversion inside the GEMM costs
-// about a quarter of its time, which grows with T.  Measured, us, expanded / converted inside, for
-// K x N = 2048 x 8192 and 4096 x 11008: forward, T = 512: 43 / 40, 93 / 83; 1024: 57 / 64, 115 / 129;
-// 4096: 129 / 188, 295 / 398; dgrad the same way; 960 x 2560 at T = 1024 (5e9 operations): 29 / 23.
-constexpr int64_t LT_PRE_T = 896;
-constexpr double LT_PRE_FLOPS = 8e9;
-size_t lora_pre_bytes(int64_t P, int64_t C, int64_t T) {
-    return T >= LT_PRE_T && 2.0 * (double)P * (double)C * (double)T >= LT_PRE_FLOPS
+// The expansion moves 3 bytes a value and is a launch more; the conversion inside the GEMM costs up
+// to a seventh of its time, which grows with the product.  Measured, us, expanded / converted
+// inside, rank 16: forward, 4096 x 11008, T = 1024: 107 / 90, 2048: 159 / 151, 4096: 290 / 294;
+// 2048 x 8192, 2048: 75 / 76, 4096: 121 / 128; 960 x 2560, 4096 (2e10 operations): 42 / 43.  dgrad,
+// whose conversion rounds: 4096 x 11008, 768: 92 / 90, 1536: 149 / 162, 4096: 311 / 354; 4096 x 4096,
+// 1024: 45 / 45, 2048: 67 / 74; 960 x 2560, 1536 (8e9): 28 / 29.  Weight gradient of M rows:
+// 4096 x 11008, M = 512: 51 / 52, 4096: 310 / 327; 2048 x 8192, 768 (3e10): 30 / 29, 2048: 59 / 62.
+struct LtPreRule {
+    int64_t t;
+    double ops;
+};
+size_t lora_pre_bytes(int mode, int64_t P, int64_t C, int64_t T) {
+    const LtPreRule r = mode == LORA_FWD     ? LtPreRule{2560, 3e10}
+                        : mode == LORA_DGRAD ? LtPreRule{1280, 5e9}
+                                             : LtPreRule{896, 3e10};
+    return T >= r.t && 2.0 * (double)P * (double)C * (double)T >= r.ops
                ? (size_t)P * (size_t)C * 2 : 0;
 }
 cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, bool beside,

@@ -238,7 +238,7 @@ static LoraWs plan_lora(bool bwd, int64_t M, int64_t N, int64_t K, int64_t R) {
     w.hp = bwd ? align_up((size_t)M * R * 4, 256) : 0;
     w.plan = w.hp + align_up((size_t)M * R * 4, 256);
     w.pre = w.plan + align_up(lora_plan_bytes(M), 256);
-    w.pre_bytes = lora_pre_bytes(N, K, M);
+    w.pre_bytes = bwd ? lora_pre_bytes(LORA_DGRAD, K, N, M) : lora_pre_bytes(LORA_FWD, N, K, M);
     w.bytes = w.pre + w.pre_bytes;
     return w;
 }
@@ -428,7 +428,7 @@ size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K, int extra) 
             return plan_gptq(N, K).bytes;
         case Q8_OP_CHECKPOINT_WGRAD:
             if (M > kLoraMaxM || N > kLoraMaxN) return 0;
-            return M > 0 ? lora_pre_bytes(K, M, N) : 0;
+            return M > 0 ? lora_pre_bytes(LORA_WGRAD, K, M, N) : 0;
         case Q8_OP_LINEAR_W8A16_LORA:
             if (M > kLoraMaxM || N > kLoraMaxN || !valid_rank(extra)) return 0;
             return lora_fwd_bytes(M, N, K, extra);
@@ -493,7 +493,6 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     a.hp = hp;
     a.lists = lora_plan_lists(ws + w.plan);
     a.R = R;
-    a.L = L;
     Q8_TRY(launched(launch_lora_plan(ids, M, L, ws + w.plan, st)));
     Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
                                        ad->scale, ws + w.plan, h, hp, M, (int)K, R, L, st, sms)));
@@ -560,7 +559,6 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
     a.hp = hp;
     a.lists = lora_plan_lists(plan);
     a.R = R;
-    a.L = L;
     Q8_TRY(launched(launch_lora_plan(ids, M, L, plan, st)));
     if (dx || da)
         Q8_TRY(launched(launch_lora_shrink(true, (const uint16_t*)dy, (const uint16_t*)ad->b,
@@ -618,7 +616,7 @@ q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t
     if (M == 0 && accumulate) return Q8_OK;
     if (!dw || (M > 0 && (!dy || !codes || !exps))) return Q8_ERR_NULL;
     if (!aligned16(dw) || !aligned16(dy) || !aligned16(codes)) return Q8_ERR_ALIGN;
-    const size_t need = M > 0 ? lora_pre_bytes(K, M, N) : 0;
+    const size_t need = M > 0 ? lora_pre_bytes(LORA_WGRAD, K, M, N) : 0;
     if (need && (!workspace || ws_bytes < need)) return Q8_ERR_WORKSPACE;
     if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     int sms = 0;

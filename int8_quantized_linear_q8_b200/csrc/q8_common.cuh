@@ -376,4 +376,22 @@ inline cudaError_t ensure_dyn_smem(int bytes) {
     return e;
 }
 
+// Keeps an SM at its largest shared memory while it runs kernel K: a kernel of large tiles that
+// starts before K ends would else wait for the SM to empty and change over.  Once per device; a
+// refusal only loses that time.
+template <auto K>
+inline void prefer_shared_memory() {
+    static std::atomic<bool> done[128];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) {
+        cudaGetLastError();
+        return;
+    }
+    if (done[dev].load(std::memory_order_relaxed)) return;
+    if (cudaFuncSetAttribute(K, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+        cudaGetLastError();
+    done[dev].store(true, std::memory_order_relaxed);
+}
+
 }  // namespace q8

@@ -218,7 +218,7 @@ struct LoraGemm {
     const uint16_t* low;
     const uint16_t* hp;         // [T, 2 R]: scale * h (LORA_DGRAD: g) in two bf16 parts
     const int* lists;           // lora_plan_lists
-    int R, L;
+    int R;
 };
 size_t lora_plan_bytes(int64_t M);               // workspace of the plan
 const int* lora_plan_lists(const void* ws);
@@ -237,7 +237,7 @@ cudaError_t launch_lora_wgrad(const void* dy, const float* h, float* db, const v
 // adapter list of a token tile: [0] their number, then their ids in ascending order
 constexpr int LT_LIST = 260;
 int lora_tc_tile(int64_t T);                    // tokens per tile
-size_t lora_pre_bytes(int64_t P, int64_t C, int64_t T);     // of the expansion; 0: none
+size_t lora_pre_bytes(int mode, int64_t P, int64_t C, int64_t T);     // of the expansion; 0: none
 // beside: right behind launch_lora_shrink on the stream, and at the same time
 cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, bool beside,
                                cudaStream_t st);

@@ -41,10 +41,31 @@ def _same(a, b):
     return all(torch.equal(u, v) for u, v in zip(a, b))
 
 
+def _expands(M, N, K):
+    """Whether all three products expand their int8 operand in the workspace."""
+    for op, n in ((q8.Q8_OP_LINEAR_W8A16_LORA, N * K), (q8.Q8_OP_LINEAR_W8A16_LORA_BACKWARD, N * K),
+                  (q8.Q8_OP_CHECKPOINT_WGRAD, M * K)):
+        assert q8.q8_workspace_bytes(op, M, N, K, 8) >= 2 * n
+
+
+@pytest.mark.parametrize("M,N,K,G", [(2563, 2568, 2336, 32), (2817, 4104, 1344, 64)])
+def test_large_products_of_odd_sizes(M, N, K, G):
+    _expands(M, N, K)
+    d = ref.make(M, N, K, 24, 5, seed=30, mix="runs")
+    _check(d, _step(d, G))
+    n = dict(d, q=d["q"][:N - 7].contiguous(), s_w=d["s_w"][:N - 7].contiguous(),
+             b=d["b"][:, :N - 7].contiguous(), bias=torch.randn(N - 7, device="cuda"))
+    for out in (torch.float32, torch.bfloat16):
+        y, _ = q8.q8_linear_w8a16_lora(n["x"], n["q"], n["s_w"], n["a"], n["b"], n["scale"],
+                                       n["ids"], bias=n["bias"], out_dtype=out)
+        wy, _, by, _ = ref.forward(n)
+        ref.near(y, wy, by + (ref.EPS8 * wy.abs() if out == torch.bfloat16 else 0.0), "y")
+
+
 def test_large_products_captured_and_replayed():
     """Sizes whose int8 operand is expanded beforehand, in one graph of 13 kernels."""
-    size = (1100, 2048, 2048, 24, 6)
-    assert q8.q8_workspace_bytes(q8.Q8_OP_CHECKPOINT_WGRAD, 1100, 2048, 2048, 0) > 0
+    size = (2600, 4096, 2048, 24, 6)
+    _expands(*size[:3])
     d = ref.make(*size, seed=31)
     _step(d, 128)
     torch.cuda.synchronize()
@@ -116,11 +137,11 @@ def test_host_threads():
     assert not wrong, wrong
 
 
-@pytest.mark.parametrize("M", [1, 12, 40, 1000])
+@pytest.mark.parametrize("M", [1, 12, 40, 2600])
 def test_operands_made_just_before(M):
     """Weights, checkpoints and gradients made by the calls before, with nothing between them:
     each call reads what the last one wrote."""
-    N, K = 1024, 4096 if M == 1000 else 512
+    N, K = (4096, 2048) if M == 2600 else (1024, 512)
     ds = [ref.make(M, N, K, 16, 3, seed=36 + i) for i in range(3)]
     Ws = [torch.randn(N, K, device="cuda", generator=torch.Generator("cuda").manual_seed(i)) * 0.02
           for i in range(3)]
@@ -150,7 +171,7 @@ def test_operands_made_just_before(M):
         assert all(_same(u, v) for u, v in zip(got, want))
 
 
-@pytest.mark.parametrize("M,N,K", [(5, 72, 256), (90, 72, 256), (1000, 2048, 2048)])
+@pytest.mark.parametrize("M,N,K", [(5, 72, 256), (90, 72, 256), (2600, 4096, 2048)])
 def test_what_a_workspace_held_does_not_matter(M, N, K):
     d = ref.make(M, N, K, 8, 3, seed=37)
     want = _step(d, 64)
