@@ -814,12 +814,12 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
     if (S > 1) {
         // A tile of several pairs: all warps but the first three finish it.  Chunk c of 16 columns
         // belongs to pair c % S; a sender's parts of an owner's chunks lie at [sender][c / S]
-        // [column][128 p] of the owner's ring region.  (Chunks of 16 and rolled loops: this code
+        // [column / 4][128 p][4 columns] of the owner's ring region.  (Chunks of 16 and rolled loops: this code
         // runs once, and fetching its instructions is what it waits for.)
         __syncwarp();
         const int q = warp & 3, par = (warp - LT_CONV0) >> 2, step = (LT_CONV + LT_EPI) / 4;
         const int chunks = BN / 16, own = (chunks + S - 1) / S;
-        const uint32_t ring = smem_u32(smem) + (uint32_t)((q * 32 + lane) * 4);
+        const uint32_t ring = smem_u32(smem) + (uint32_t)((q * 32 + lane) * 16);
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         int p0, t0;
         tile_of(u0, p0, t0);
@@ -865,8 +865,9 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
             const uint32_t to =
                 lt_map(ring + (uint32_t)((pair * own + c / S) * 8192), (uint32_t)o * 2 + rank);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + j * 512), "f"(v[j])
+            for (int j = 0; j < 16; j += 4)
+                asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(to + j * 512),
+                             "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3])
                              : "memory");
         }
         __syncwarp();
@@ -883,9 +884,10 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 const uint32_t from = ring + (uint32_t)((o * own + k) * 8192);
                 float got[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    asm volatile("ld.shared.f32 %0, [%1];"
-                                 : "=f"(got[j])
+                for (int j = 0; j < 16; j += 4)
+                    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(got[j]), "=f"(got[j + 1]), "=f"(got[j + 2]),
+                                   "=f"(got[j + 3])
                                  : "r"(from + j * 512)
                                  : "memory");
 #pragma unroll
