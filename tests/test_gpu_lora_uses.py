@@ -41,6 +41,13 @@ def _same(a, b):
     return all(torch.equal(u, v) for u, v in zip(a, b))
 
 
+@pytest.mark.parametrize("M,L,mix", [(4096, 1024, "each"), (4097, 3, "wild"), (8192, 1023, "runs"),
+                                     (9001, 1024, "each"), (13000, 1, "each"), (20011, 40, "each")])
+def test_many_rows_sorted(M, L, mix):
+    d = ref.make(M, 24, 64, 8, L, seed=29 + M, mix=mix)
+    _check(d, _step(d, 32))
+
+
 def _expands(M, N, K):
     """Whether all three products expand their int8 operand in the workspace."""
     for op, n in ((q8.Q8_OP_LINEAR_W8A16_LORA, N * K), (q8.Q8_OP_LINEAR_W8A16_LORA_BACKWARD, N * K),
