@@ -647,49 +647,78 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
             // Adapter columns: both tiles are written here.  (PRE: the producer says when the
             // slot is free; who has not followed every phase of `empty` cannot tell one from the
             // one before the last.)
-            for (; more(w, t0); ++w.kb) {
-                const int kb = w.kb;
+            if (!more(w, t0)) continue;
+            const int* list = a.lists + (int64_t)(t0 / BN) * LT_LIST;
+            const int cnt = ld_after(list), rc2 = a.R >> 2;
+            // Copies: eight neighbouring threads take a row's 128 bytes (a thread a row, every
+            // request touched 32 lines, and a stage took 1.4 us).  Thread: piece pc of rows
+            // pr, pr + 16, ...; b's rows for the P tile, h's (or g's) for the T tile.
+            const int pr = tid >> 3, pc = tid & 7;
+            const uint32_t swz = (uint32_t)(pr * 128 + ((pc ^ (pr & 7)) << 4));
+            const int tr = t0 + (int)rank * half + pr;
+            int ids[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                ids[i] = 16 * i < half && tr + 16 * i < a.T ? ld_after(a.ids + tr + 16 * i) : -1;
+            // the list's entries win .. win + 31, one a lane
+            int win = (w.kb - nk) * 8 / rc2;
+            int entry = ld_after(list + 1 + min(win + lane, 255));
+            for (; w.kb < w.end; ++w.kb) {
                 if (it % GROUPS == grp) {
-                    const uint32_t at = smem_u32(smem + r.s * LT_SLOT);
+                    const uint32_t at = smem_u32(smem + r.s * LT_SLOT), bt = at + LT_A;
                     const bool okw =
                         PRE ? mbar_wait(&lgo[r.s], lph >> r.s & 1u, status, abort_flag)
                             : mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag);
                     lph ^= 1u << r.s;
                     live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
+                    // Columns (kb - nk) * 64 .. +64 of the adapter term, in pieces of 8: per adapter
+                    // of the list R / 8 pieces against the high parts and R / 8 against the
+                    // rest; `in` is a piece's place among an adapter's.
+                    const int first = (w.kb - nk) * 8, e0 = first / rc2;
+                    if (e0 + 4 > win + 31) {                    // a stage spans at most 5 adapters
+                        win = e0;
+                        entry = ld_after(list + 1 + min(win + lane, 255));
+                    }
+                    const int e = (first + pc) / rc2, in = first + pc - e * rc2;
+                    const int ad = __shfl_sync(0xffffffffu, entry, e - win);
                     if (live) {
-                        // Columns (kb - nk) * 64 .. +64 of the adapter term, in pieces of 8:
-                        // per adapter of the list R / 8 pieces against the high parts and
-                        // R / 8 against the rest.
-                        const uint32_t bt = at + LT_A;
-                        const int rc = a.R >> 3;
-                        const int* list = a.lists + (int64_t)(t0 / BN) * LT_LIST;
-                        const int cnt = ld_after(list);
-                        const int t = t0 + (int)rank * half + tid;
-                        const int id = tid < half && t < a.T ? ld_after(a.ids + t) : -1;
-                        const int pr = tid >> 4, pc = tid & 15;     // A_MN: row and 8 p of a piece
-                        const int p = A_MN ? p0 + pc * 8 : p0 + tid;
-                        int ad[8];
+                        if (A_MN) {                             // rows of a: r, 256 bytes of p each
+                            const int ar = tid >> 4, ac = tid & 15, p = p0 + ac * 8;
+                            const uint32_t to = at + (ac >> 3) * 8192 + ar * 128 +
+                                                (((ac & 7) ^ ar) << 4);
+                            int ec = e0, ic = first - e0 * rc2;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            ad[c] = ld_after(list + 1 + min(((kb - nk) * 8 + c) / (2 * rc), 255));
+                            for (int c = 0; c < 8; ++c) {
+                                const int adc = __shfl_sync(0xffffffffu, ad, c);
+                                const int col = (ic >= rc2 >> 1 ? ic - (rc2 >> 1) : ic) * 8;
+                                const bool pl = ec < cnt && p < a.P;
+                                cp_async16(to + 1024 * c,
+                                           pl ? a.low + ((int64_t)adc * a.R + col + ar) * a.P + p
+                                              : a.low, pl);
+                                if (++ic == rc2) {
+                                    ic = 0;
+                                    ++ec;
+                                }
+                            }
+                        } else {
+                            const int col = (in >= rc2 >> 1 ? in - (rc2 >> 1) : in) * 8;
+                            const uint16_t* src =
+                                a.low + ((int64_t)ad * a.P + p0 + pr) * a.R + col;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const int piece = (kb - nk) * 8 + c;
-                            const int e = piece / (2 * rc), in = piece - e * 2 * rc;
-                            const int col = (in >= rc ? in - rc : in) * 8;
-                            const bool there = e < cnt;
-                            const bool pl = there && p < a.P, tl = there && id == ad[c];
-                            const uint16_t* ps =
-                                A_MN ? a.low + ((int64_t)ad[c] * a.R + col + pr) * a.P + p
-                                     : a.low + ((int64_t)ad[c] * a.P + p) * a.R + col;
-                            cp_async16(A_MN ? at + (pc >> 3) * 8192 + (8 * c + pr) * 128 +
-                                                  (((pc & 7) ^ pr) << 4)
-                                            : at + tid * 128 + ((c ^ (tid & 7)) << 4),
-                                       pl ? ps : a.low, pl);
-                            if (tid < half)
-                                cp_async16(bt + tid * 128 + ((c ^ (tid & 7)) << 4),
-                                           tl ? a.hp + (int64_t)t * 2 * a.R + in * 8 : a.hp, tl);
+                            for (int i = 0; i < 8; ++i) {
+                                const bool pl = e < cnt && p0 + pr + 16 * i < a.P;
+                                cp_async16(at + swz + 2048 * i,
+                                           pl ? src + (int64_t)(16 * i) * a.R : a.low, pl);
+                            }
                         }
+                        const uint16_t* src = a.hp + (int64_t)tr * 2 * a.R + in * 8;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (16 * i < half) {
+                                const bool tl = e < cnt && ids[i] == ad;
+                                cp_async16(bt + swz + 2048 * i,
+                                           tl ? src + (int64_t)(32 * i) * a.R : a.hp, tl);
+                            }
                     }
                     // handed over a turn later, when the next copies are on their way
                     cp_commit();
