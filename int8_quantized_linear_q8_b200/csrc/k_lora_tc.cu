@@ -27,31 +27,33 @@
 // Two variants.  PRE: the int8 operand was expanded to bf16 in the workspace beforehand
 // (k_lora_expand) and both operands come by TMA.  Otherwise it stays int8 in HBM and L2 and the
 // kernel converts it, which costs nothing extra to read but adds 24 KB of shared-memory traffic
-// to the 64 KB that a stage and CTA move anyway, more than the port carries in the MMAs' time
-// (4096 x 11008 x 4096: about 500 ns a stage against 360 expanded).
+// to the 64 KB that a stage and CTA move anyway, more than the port carries in the MMAs' time.
+// With few rows the converters' own path is what a stage takes (77 rows: 0.57 us a stage when
+// one loop did base and adapter stages, 0.4 with a loop of its own for the base).
 //
 // What bounds it, measured on the expanded form (cycles a stage of 64 c; its MMAs take 512): dgrad
 // 538, tensor pipe active 91% of the time a pair has work; forward 608 (the adapter term's
-// second accumulator, drained between tiles); weight gradient 715 before its stores were
-// streamed past L2.  dgrad of 4096 x 11008 x 4096: 250 us, 1.48 PFLOP/s, of which the fourth round
-// of tiles, which 34 of 74 pairs have, costs 13%.  Two things cost most on the way: cluster-scope
-// acquire and release on the hand-offs (538 -> 328 us), and everything on the issuing warp's
-// path between two stages.  Not kept: a second launch that splits the last round's tiles over
-// clusters of two pairs (only 32 such clusters run at once; the exchange costs what it saves),
-// L2 evict-last hints on the operands (no change), t blocks of 16 and 64 tiles (1% and 8% slower).
+// second accumulator, drained between tiles).  dgrad of 4096 x 11008 x 4096: 250 us, 1.48 PFLOP/s,
+// of which the fourth round of tiles, which 34 of 74 pairs have, costs 13%.  Two things cost most
+// on the way: cluster-scope acquire and release on the hand-offs (538 -> 328 us), and everything
+// on the issuing warp's path between two stages.  Not kept: a second launch that splits the last
+// round's tiles over clusters of two pairs (only 32 such clusters run at once; the exchange costs
+// what it saves), L2 evict-last hints on the operands (no change), t blocks of 16 and 64 tiles
+// (1% and 8% slower), both sums of 16 columns read under one wait (more spills).
 //
 // Few tiles (fewer than half the CTA pairs): S = 2 or 4 pairs of one cluster split a tile's
 // stages; each owns 1 / S of the tile's columns and adds the other pairs' parts, which they
 // store in its shared memory (free by then), in pair order.
 //
-// Roles (15 warps): 0 and 2 TMA producers of the int8 and the bf16 operands; 1 tensor-memory
+// Roles: 0 and 2 TMA producers of the int8 and the bf16 operands; 1 tensor-memory
 // allocator and, in the pair's first CTA, MMA issuer; then converters, two groups of four that
-// take every other stage (PRE: one group, for the adapter columns), and four epilogue warps
-// (PRE: eight).  A stage is 64 of c.  Its int8 box (8 KB) has a ring of its own, eight deep: that
-// path is the longest (copy, conversion, MMA) and runs ahead.  Its P tile and its T tile (16 KB each) share a slot of a ring of five (PRE: seven), so
-// that the issuing warp, whose own steps bound the main loop, has one barrier to wait for
-// and one commit to make per stage; it tests the next stage's barrier before it issues this
-// stage's MMAs, which hides the test.  Every wait is bounded.
+// take every other stage (PRE: one group, for the adapter columns; weight gradient: none), and
+// four epilogue warps (PRE: eight).  A stage is 64 of c.  Its int8 box (8 KB) has a ring of its own,
+// eight deep: that path is the longest (copy, conversion, MMA) and runs ahead.  Its P tile and its
+// T tile (16 KB each) share a slot of a ring of five (PRE: seven), so that the issuing warp, whose
+// own steps bound the main loop, has one barrier to wait for and one commit to make per stage; it
+// tests the next stage's barrier before it issues this stage's MMAs, which hides the test.  Every
+// wait is bounded.
 #include "q8_kernels.cuh"
 
 namespace q8 {
@@ -63,12 +65,22 @@ __host__ __device__ constexpr int lt_slots(bool pre) { return pre ? 7 : 5; }
 constexpr int LT_SLOT = LT_A + LT_B, LT_RT = 5 * LT_SLOT;
 constexpr int LT_CTRL = LT_RT + LT_NR * LT_RAW;
 static_assert(LT_CTRL >= LT_N_MAX * LT_SLOT, "PRE uses the whole region for its slots");
-// warps: 15, which leaves each thread 128 registers (19 would leave 96)
-__host__ __device__ constexpr int lt_conv(bool pre) { return pre ? 4 : 8; }
+// warps: 15, which leaves each thread 128 registers (19 would leave 96); 11 for the expanded
+// weight gradient, which has nothing to convert and keeps its sums in registers (184)
+__host__ __device__ constexpr int lt_conv(int mode, bool pre) {
+    return !pre ? 8 : mode == LORA_WGRAD ? 0 : 4;
+}
 __host__ __device__ constexpr int lt_epi(bool pre) { return pre ? 8 : 4; }
 constexpr int LT_CONV0 = 3;
-constexpr int LT_THREADS = 32 * (LT_CONV0 + lt_conv(true) + lt_epi(true));
-static_assert(LT_THREADS == 32 * (LT_CONV0 + lt_conv(false) + lt_epi(false)), "warps");
+__host__ __device__ constexpr int lt_threads(int mode, bool pre) {
+    return 32 * (LT_CONV0 + lt_conv(mode, pre) + lt_epi(pre));
+}
+// The tensor core cuts a running sum off towards zero at every step, which over thousands of
+// terms adds up (weight gradient of 4096 rows: 2.2e-6 off in the norm; plain fp32 3.0e-7).  Results
+// that are not rounded to bf16, which is 1000 times as coarse, are sums of LT_SUM stages added up
+// outside it (4.1e-7, for 2% of the time): the weight gradient and a forward pass with fp32
+// output.  Pairs that split a tile make one sum each, whatever its length.
+constexpr int LT_SUM = 16;
 constexpr int LT_SMEM = LT_CTRL + 1024 + 512;
 static_assert(LT_SMEM <= 227 * 1024, "shared memory");
 
@@ -227,18 +239,20 @@ __device__ __forceinline__ uint32_t lt_apply(uint32_t v, const LtScale& s) {
 }
 
 // ------------------------------------------------------------------------- the kernel
-// Writes W columns (t0 + j, those below t1) of this lane's p: v + bias.  All lanes of the warp
+// Writes W columns (t0 + j, those below t1) of this lane's p: v + bias, to out; fp32:
+// first added to `from` (at the same places), then, `add`, to what is there.  All lanes of the warp
 // call it.  Whole chunks go without a test or a product per store: with them a weight
 // gradient's tile took 5.7 us to write, without 2.9 (40 x 11008 x 4096: 62 -> 32.5 us a call).
 template <int MODE, int W, bool FULL>
 __device__ __forceinline__ void lt_store_rows(const LoraGemm& a, int t0, int rows, int p,
-                                              float (&v)[W]) {
+                                              float (&v)[W], void* to, const float* from,
+                                              bool add) {
     const int lane = threadIdx.x & 31;
     const int64_t step = a.P;
     if (MODE != LORA_WGRAD && a.out_bf16 && (a.P & 1) == 0) {
         // neighbouring lanes exchange, so that each stores two p of one t
         const int od = lane & 1;
-        uint32_t* out = reinterpret_cast<uint32_t*>(a.out) + (((t0 + od) * step + (p & ~1)) >> 1);
+        uint32_t* out = reinterpret_cast<uint32_t*>(to) + (((t0 + od) * step + (p & ~1)) >> 1);
 #pragma unroll
         for (int j = 0; j < W; j += 2) {
             const float got = __shfl_xor_sync(0xffffffffu, od ? v[j] : v[j + 1], 1);
@@ -248,15 +262,23 @@ __device__ __forceinline__ void lt_store_rows(const LoraGemm& a, int t0, int row
             out += step;
         }
     } else if (MODE != LORA_WGRAD && a.out_bf16) {
-        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + t0 * step + p;
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(to) + t0 * step + p;
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             if ((FULL || j < rows) && p < a.P) *out = __float2bfloat16_rn(v[j]);
             out += step;
         }
     } else if (p < a.P) {
-        float* out = reinterpret_cast<float*>(a.out) + t0 * step + p;
-        if (MODE == LORA_WGRAD && a.accumulate) {
+        float* out = reinterpret_cast<float*>(to) + t0 * step + p;
+        if (MODE != LORA_DGRAD && from) {
+            const float* in = from + t0 * step + p;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                if (FULL || j < rows) v[j] += *in;
+                in += step;
+            }
+        }
+        if (MODE == LORA_WGRAD && add) {
             const float* in = out;
 #pragma unroll
             for (int j = 0; j < W; ++j) {
@@ -280,24 +302,25 @@ __device__ __forceinline__ void lt_store_rows(const LoraGemm& a, int t0, int row
 }
 template <int MODE, int W>
 __device__ __forceinline__ void lt_store(const LoraGemm& a, int t0, int64_t t1, int p, float bs,
-                                         float (&v)[W]) {
+                                         float (&v)[W], void* to, const float* from,
+                                         bool add) {
     if (MODE == LORA_FWD)
 #pragma unroll
         for (int j = 0; j < W; ++j) v[j] += bs;
     if (t0 + W <= t1)
-        lt_store_rows<MODE, W, true>(a, t0, W, p, v);
+        lt_store_rows<MODE, W, true>(a, t0, W, p, v, to, from, add);
     else
-        lt_store_rows<MODE, W, false>(a, t0, (int)(t1 - t0), p, v);
+        lt_store_rows<MODE, W, false>(a, t0, (int)(t1 - t0), p, v, to, from, add);
 }
 
 template <int MODE, bool PRE>
-__global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
+__global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
     const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap tmap,
     const LoraGemm a, int BN, int num_p, int num_t, int S, int* status) {
     constexpr bool A_MN = MODE != LORA_FWD;             // int8 operand with p contiguous
     constexpr bool B_MN = MODE == LORA_WGRAD;           // bf16 operand with t contiguous
-    constexpr int LT_N = lt_slots(PRE), LT_CONV = lt_conv(PRE), LT_EPI = lt_epi(PRE);
-    constexpr int GROUPS = LT_CONV / 4, LT_EPI0 = LT_CONV0 + LT_CONV;
+    constexpr int LT_N = lt_slots(PRE), LT_CONV = lt_conv(MODE, PRE), LT_EPI = lt_epi(PRE);
+    constexpr int GROUPS = LT_CONV == 8 ? 2 : 1, LT_EPI0 = LT_CONV0 + LT_CONV;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t* rfull = reinterpret_cast<uint64_t*>(smem + LT_CTRL);
@@ -321,6 +344,10 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
     const int u0 = blockIdx.x / (2 * S), ustep = gridDim.x / (2 * S);
     const int nk = (a.C + LT_BK - 1) / LT_BK;
     const int half = BN >> 1;
+    // stages of a sum, and sums of a tile; pairs that split a tile make one sum each (of nk / S)
+    const bool sums = S == 1 && (MODE == LORA_WGRAD || (MODE == LORA_FWD && !a.out_bf16));
+    const int sum_n = sums ? (nk + LT_SUM - 1) / LT_SUM : 1, sum_len = (nk + sum_n - 1) / sum_n;
+    const int nsum = sums ? (nk + sum_len - 1) / sum_len : 1;
     // Tiles run over t first, in even blocks of at most 8 t tiles: the pairs that run at once share both
     // operands through L2 and the int8 operand is read from HBM once per block.
     const int tblk = (num_t + (num_t + 7) / 8 - 1) / ((num_t + 7) / 8);
@@ -479,21 +506,25 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 int p0, t0;
                 tile_of(u, p0, t0);
                 bool first = true, in_low = MODE != LORA_FWD;
+                int left = sum_len;
                 for (Walk w = walk(); ok && more(w, t0); ++w.kb) {
-                    // a sum begins: the base, or, forward, the adapter term
-                    const bool fresh = first || (w.kb >= nk && !in_low);
+                    // a sum begins: of the base, or, forward, the adapter term
+                    const bool begin_low = w.kb >= nk && !in_low;
+                    const bool fresh = first || begin_low || (nsum > 1 && w.kb < nk && left == 0);
                     if (fresh) {
-                        if (!first) {                   // base sum complete
+                        if (!first) {                   // the sum before it is complete
                             if (lt_elect()) lt_commit(&tfull[rt.s], both);
                             __syncwarp();
                             rt.next();
-                            in_low = true;
                         }
+                        if (begin_low) in_low = true;
+                        left = sum_len;
                         first = false;
                         ok = __all_sync(0xffffffffu,
                                         mbar_wait(&tempty[rt.s], rt.ph ^ 1u, status, abort_flag));
                         if (!ok) break;
                     }
+                    --left;
                     if (!here) {
                         ok = __all_sync(0xffffffffu,
                                         mbar_wait(&full[r.s], r.ph, status, abort_flag));
@@ -581,9 +612,6 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                     for (int i = 0; i < 4; ++i)
                         cw[i] = A_MN ? lds128(raw + (i * 16 + sc) * 128 + (tid & 7) * 16)
                                     : lds128(raw + tid * 64 + ((i ^ ((tid >> 1) & 3)) << 4));
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&rempty[rq.s]);          // codes in registers
-                    rq.next2();
                     uint32_t cur[4];
                     if (A_MN) {
 #pragma unroll
@@ -608,6 +636,13 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                             for (int j = 0; j < 8; ++j) o[i][j] = lt_apply<MODE>(o[i][j], f);
                         }
                     }
+                    // The box is free once its codes are in registers, all lanes' and for the
+                    // copy engine as well: handed back right behind the loads, it was
+                    // overwritten under them now and then (20000 rows, 264 x 16384).
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&rempty[rq.s]);
+                    rq.next2();
                     const uint32_t at = smem_u32(smem + rc.s * LT_SLOT);
                     live = mbar_wait(&empty[rc.s], rc.ph ^ 1u, status, abort_flag) && live;
                     if (live) {
@@ -752,30 +787,92 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
             const int p = p0 + q * 32 + lane;
             const int64_t t1 = min((int64_t)t0 + BN, a.T);
             const int chunks = (BN + 31) / 32;
-            // forward: whether this pair has an adapter term besides its base sum
-            Walk w = walk();
-            w.kb = w.end;
-            const bool low = MODE == LORA_FWD && more(w, t0);
+            // a sum is there, or its place is free again
+            auto wait_sum = [&](const LtRing<2>& x) {
+                const bool okw = mbar_wait(&tfull[x.s], x.ph, status, abort_flag);
+                live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            };
+            auto free_sum = [&](const LtRing<2>& x) {
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) lt_arrive(tempty0 + x.s * 8);
+            };
+            if (PRE && MODE == LORA_WGRAD) {
+                // the sums are added up in registers, 128 a thread
+                float total[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) total[i][j] = 0.0f;
+#pragma unroll 1
+                for (int n = 0; n < nsum; ++n) {
+                    wait_sum(rt);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (live && par + 2 * i < chunks)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t r[16];
+                                lt_ld16(lanes + (uint32_t)(rt.s * 256 + (par + 2 * i) * 32 + k * 16),
+                                        r);
+                                lt_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    total[i][k * 16 + j] += __uint_as_float(r[j]);
+                            }
+                    free_sum(rt);
+                    rt.next();
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (live && par + 2 * i < chunks)
+                        lt_store<MODE, 32>(a, t0 + (par + 2 * i) * 32, t1, p, 0.0f, total[i], a.out,
+                                           nullptr, a.accumulate);
+                continue;
+            }
             float sw = 1.0f, bs = 0.0f;
             if (MODE == LORA_FWD && p < a.P) {
                 sw = ld_after(a.s_w + p);
                 if (a.bias) bs = ld_after(a.bias + p);
             }
+            // all sums but the last are added up in memory
+            float* const partial = a.partial ? a.partial : reinterpret_cast<float*>(a.out);
+            const float* from = nullptr;
+            if (MODE != LORA_DGRAD)
+#pragma unroll 1
+                for (int n = 1; n < nsum; ++n) {
+                    wait_sum(rt);
+#pragma unroll 1
+                    for (int c = par; live && c < chunks; c += CS) {
+                        uint32_t r[32];
+                        lt_ld32(lanes + (uint32_t)(rt.s * 256 + c * 32), r);
+                        lt_ld_wait();
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = MODE == LORA_FWD ? __uint_as_float(r[j]) * sw
+                                                    : __uint_as_float(r[j]);
+                        lt_store<MODE, 32>(a, t0 + c * 32, t1, p, bs, v, partial, from, false);
+                    }
+                    free_sum(rt);
+                    rt.next();
+                    from = partial;
+                    bs = 0.0f;
+                }
+            // forward: whether this pair has an adapter term besides its base sum
+            Walk w = walk();
+            w.kb = w.end;
+            const bool low = MODE == LORA_FWD && more(w, t0);
             const LtRing<2> r1 = rt;
             rt.next();
             const LtRing<2> r2 = rt;
             if (low) rt.next();
-            bool okw = mbar_wait(&tfull[r1.s], r1.ph, status, abort_flag);
-            if (low) okw = mbar_wait(&tfull[r2.s], r2.ph, status, abort_flag) && okw;
-            live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            wait_sum(r1);
+            if (low) wait_sum(r2);
             auto free_sums = [&]() {
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
-                    lt_arrive(tempty0 + r1.s * 8);
-                    if (low) lt_arrive(tempty0 + r2.s * 8);
-                }
+                free_sum(r1);
+                if (low) free_sum(r2);
             };
             // this pair's part of 32 columns
             auto part = [&](int c, float (&v)[32]) {
@@ -834,7 +931,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
                 for (int c = par; live && c < chunks; c += CS) {
                     float v[32];
                     part(c, v);
-                    lt_store<MODE, 32>(a, t0 + c * 32, t1, p, bs, v);
+                    lt_store<MODE, 32>(a, t0 + c * 32, t1, p, bs, v, a.out, from, a.accumulate);
                 }
             }
             if (held) free_sums();
@@ -922,7 +1019,7 @@ __global__ __launch_bounds__(LT_THREADS, 1) void k_lora_tc(
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] += o == pair ? mine[j] : got[j];
             }
-            lt_store<MODE, 16>(a, t0 + c * 16, t1, p, bs, v);
+            lt_store<MODE, 16>(a, t0 + c * 16, t1, p, bs, v, a.out, nullptr, a.accumulate);
         }
         __syncwarp();
     }
@@ -958,7 +1055,7 @@ static int lora_tc_clusters(int S) {
     if (n > 0) return n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * S);
-    cfg.blockDim = dim3(LT_THREADS);
+    cfg.blockDim = dim3(lt_threads(MODE, PRE));
     cfg.dynamicSmemBytes = LT_SMEM;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1008,7 +1105,7 @@ static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, in
     const int64_t clusters = tiles < num_sms / 2 ? tiles : num_sms / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * S * clusters));
-    cfg.blockDim = dim3(LT_THREADS);
+    cfg.blockDim = dim3(lt_threads(MODE, PRE));
     cfg.dynamicSmemBytes = LT_SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -1079,6 +1176,8 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraGemm a, int64_t n
 // whose conversion rounds: 4096 x 11008, 768: 92 / 90, 1536: 149 / 162, 4096: 311 / 354; 4096 x 4096,
 // 1024: 45 / 45, 2048: 67 / 74; 960 x 2560, 1536 (8e9): 28 / 29.  Weight gradient of M rows:
 // 4096 x 11008, M = 512: 51 / 52, 4096: 310 / 327; 2048 x 8192, 768 (3e10): 30 / 29, 2048: 59 / 62.
+// A weight gradient of more rows than one sum takes is expanded from T = 896 on whatever its size
+// (960 x 2560, 2048 rows: 19 us either way): only that form adds its sums up in registers.
 struct LtPreRule {
     int64_t t;
     double ops;
@@ -1087,8 +1186,13 @@ size_t lora_pre_bytes(int mode, int64_t P, int64_t C, int64_t T) {
     const LtPreRule r = mode == LORA_FWD     ? LtPreRule{2560, 3e10}
                         : mode == LORA_DGRAD ? LtPreRule{1280, 5e9}
                                              : LtPreRule{896, 3e10};
-    return T >= r.t && 2.0 * (double)P * (double)C * (double)T >= r.ops
+    const bool long_sum = mode == LORA_WGRAD && C > LT_SUM * LT_BK;
+    return T >= r.t && (long_sum || 2.0 * (double)P * (double)C * (double)T >= r.ops)
                ? (size_t)P * (size_t)C * 2 : 0;
+}
+size_t lora_partial_bytes(int64_t P, int64_t C, int64_t T) {
+    return C > LT_SUM * LT_BK && lora_pre_bytes(LORA_WGRAD, P, C, T) == 0
+               ? (size_t)P * (size_t)T * 4 : 0;
 }
 cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, bool beside,
                                cudaStream_t st) {

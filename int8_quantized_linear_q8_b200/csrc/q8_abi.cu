@@ -428,7 +428,7 @@ size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K, int extra) 
             return plan_gptq(N, K).bytes;
         case Q8_OP_CHECKPOINT_WGRAD:
             if (M > kLoraMaxM || N > kLoraMaxN) return 0;
-            return M > 0 ? lora_pre_bytes(LORA_WGRAD, K, M, N) : 0;
+            return M > 0 ? lora_pre_bytes(LORA_WGRAD, K, M, N) + lora_partial_bytes(K, M, N) : 0;
         case Q8_OP_LINEAR_W8A16_LORA:
             if (M > kLoraMaxM || N > kLoraMaxN || !valid_rank(extra)) return 0;
             return lora_fwd_bytes(M, N, K, extra);
@@ -616,7 +616,8 @@ q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t
     if (M == 0 && accumulate) return Q8_OK;
     if (!dw || (M > 0 && (!dy || !codes || !exps))) return Q8_ERR_NULL;
     if (!aligned16(dw) || !aligned16(dy) || !aligned16(codes)) return Q8_ERR_ALIGN;
-    const size_t need = M > 0 ? lora_pre_bytes(LORA_WGRAD, K, M, N) : 0;
+    const size_t pre = M > 0 ? lora_pre_bytes(LORA_WGRAD, K, M, N) : 0;
+    const size_t need = M > 0 ? pre + lora_partial_bytes(K, M, N) : 0;     // one or the other
     if (need && (!workspace || ws_bytes < need)) return Q8_ERR_WORKSPACE;
     if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     int sms = 0;
@@ -634,7 +635,8 @@ q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t
     a.P = (int)K;
     a.C = (int)M;
     a.T = N;
-    if (need) {
+    if (need > pre) a.partial = (float*)workspace;
+    if (pre) {
         Q8_TRY(launched(launch_lora_expand(LORA_WGRAD, a, (uint16_t*)workspace, false,
                                            st)));
         a.pre = (const uint16_t*)workspace;

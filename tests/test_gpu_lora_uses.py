@@ -252,3 +252,55 @@ def test_outputs_past_2_to_31():
     wy, wh, by, bh = ref.forward(tail)
     ref.near(h[-40:], wh, bh, "h")
     ref.near(y[-40:], wy, by + ref.EPS8 * wy.abs(), "y")
+
+
+# A sum of up to 1024 terms is made by the tensor core in 64 steps, each of which cuts off less than
+# a unit in the last place (2^-23) of a running sum that is, for terms of one sign, half the sum
+# on average; sums are then added up with a rounding (2^-24) each, and the result is scaled.
+def _one_sign(terms):
+    return 33 * 2.0 ** -23 + (terms / 1024 + 6) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("M,N,K", [(30000, 2560, 960), (20000, 264, 16384), (2048, 1024, 4096)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_long_gradient_sums_of_one_sign(M, N, K, accumulate):
+    g = torch.Generator("cuda").manual_seed(42)
+    codes = torch.randint(1, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    exps = torch.full((M, K // 64), 120, dtype=torch.uint8, device="cuda")
+    dy = torch.rand(M, N, device="cuda", generator=g).bfloat16() + 0.125
+    want = (dy.double().t() @ codes.double()) * 2.0 ** -7
+    base = torch.full((N, K), 3.0, device="cuda") if accumulate else None
+    dw = q8.q8_checkpoint_wgrad(dy, codes, exps, dw=base, accumulate=accumulate)
+    if accumulate:
+        want += 3.0
+    ref.near(dw, want, _one_sign(M) * want, "dw")
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 8192, 65520), (3000, 2064, 16384), (40, 11008, 4096)])
+def test_long_forward_sums_of_one_sign(M, N, K):
+    d = ref.make(M, N, K, 8, 2, seed=43, mix="none", bias=True)
+    d["x"] = d["x"].abs()
+    d["q"] = d["q"].abs()
+    d["bias"] = d["bias"].abs()
+    y, _ = q8.q8_linear_w8a16_lora(d["x"], d["q"], d["s_w"], d["a"], d["b"], d["scale"], d["ids"],
+                                   bias=d["bias"], out_dtype=torch.float32)
+    want = ref.forward(d)[0]
+    ref.near(y, want, _one_sign(K) * want, "y")
+
+
+@pytest.mark.parametrize("M,N,K", [(20000, 264, 16384), (700, 11008, 4096), (9000, 512, 8192)])
+def test_converted_products_have_the_same_bits_every_time(M, N, K):
+    """Long runs of stages through the rings that convert the int8 operand."""
+    d = ref.make(M, N, K, 8, 2, seed=44, mix="runs")
+    codes, exps = q8.q8_checkpoint_save(d["x"], 64)
+    args = (d["q"], d["s_w"], d["a"], d["b"], d["scale"], d["ids"])
+    calls = [lambda: q8.q8_checkpoint_wgrad(d["dy"], codes, exps)]
+    if M < 1000:
+        h = q8.q8_linear_w8a16_lora(d["x"], *args)[1]
+        calls += [lambda: q8.q8_linear_w8a16_lora(d["x"], *args)[0],
+                  lambda: q8.q8_linear_w8a16_lora_backward(d["dy"], *args, h, want_da=False,
+                                                           want_db=False)[0]]
+    for call in calls:
+        first = call()
+        wrong = sum(not torch.equal(call(), first) for _ in range(40))
+        assert wrong == 0, wrong
