@@ -13,10 +13,12 @@
 // weight stream start as soon as the stream's earlier work is done (programmatic dependent
 // launch); the stream waits for t only when its first rows are summed.
 //
-// 16 rows, 4096 x 11008, rank 16, 32 adapters: this kernel 6 us (h 2.7, t 3.2), the whole call 21 us
-// back to back, the plain linear 14; 1 row, 960 x 2560, rank 8: 5.8 and 3.9 us.  What is left is the
-// chain itself: the stream's CTAs need the registers of the SMs that this kernel's CTAs
-// still hold, so 128 of its 148 start when those end.  Two kernels (h, then t) were 5 us slower.
+// 16 rows, 4096 x 11008, rank 16, 32 adapters: this kernel 6 us (h 2.7, t 3.2), the whole call 19.9 us
+// back to back, the plain linear 14; 1 row, 960 x 2560, rank 8: 4.9 and 3.9 us.  What is left is the
+// chain itself: the stream's CTAs of the larger shapes need the registers of the SMs that this
+// kernel's CTAs still hold, so 50 to 130 of its 148 start when those end.  Not kept: a stream
+// held to 128 registers, whose CTAs start at once (21.7 to 25 us: they slow this kernel down and
+// wait for it all the same); this kernel on 128 threads (23.2); two kernels, h and t (5 us more).
 #include "q8_kernels.cuh"
 
 namespace q8 {
