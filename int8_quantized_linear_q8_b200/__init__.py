@@ -452,13 +452,24 @@ def _device(t: torch.Tensor) -> int:
     return torch.cuda.current_device()
 
 
+# An uninitialised tensor on the current device without the parsing of torch.empty's arguments
+# (0.9 us instead of 2.0, of a call that makes three or four).
+_empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None),
+                      "_empty_strided_cuda", None)
+
+
 def _new(shape, like: torch.Tensor, dtype: torch.dtype, stream):
-    """A new tensor on `like`'s device that belongs to the stream the call runs on (the caching
-    allocator may hand its memory on in that stream's order only)."""
+    """A new tensor on `like`'s device, the current one, that belongs to the stream the call runs
+    on (the caching allocator may hand its memory on in that stream's order only)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return like.new_empty(shape, dtype=dtype)
-    return like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
+    if _empty_cuda is None:
+        return like.new_empty(shape, dtype=dtype)
+    if len(shape) == 2:
+        return _empty_cuda(shape, (shape[1], 1), dtype)
+    return _empty_cuda(shape, (1,) if len(shape) == 1 else (shape[1] * shape[2], shape[2], 1),
+                       dtype)
 
 
 def _on(stream, dev: int) -> int:
@@ -484,7 +495,7 @@ def _scratch(ws, op: int, M: int, N: int, K: int, extra: int, like: torch.Tensor
     nbytes = _scratch_bytes(op, M, N, K, extra)
     if nbytes == 0:
         return None, None, 0
-    ws = _new(nbytes, like, like.dtype, stream)
+    ws = _new((nbytes,), like, like.dtype, stream)
     return ws, ws.data_ptr(), nbytes
 
 

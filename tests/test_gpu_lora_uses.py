@@ -48,6 +48,21 @@ def test_many_rows_sorted(M, L, mix):
     _check(d, _step(d, 32))
 
 
+@pytest.mark.parametrize("N,K,R", [(10240, 2048, 16), (8192, 2048, 16), (8192, 2048, 64),
+                                   (11008, 2816, 32), (8192, 8192, 8), (512, 256, 136)])
+@pytest.mark.parametrize("M", [333, 700, 1100])
+def test_gradients_split_over_clusters_of_every_size(M, N, K, R):
+    d = ref.make(M, N, K, R, 1, seed=45, free=0.0)
+    h = ref.forward(d)[1].float()
+    codes, exps = ref.checkpoint(d["x"], 256)
+    _, da, db = q8.q8_linear_w8a16_lora_backward(d["dy"], d["q"], d["s_w"], d["a"], d["b"],
+                                                 d["scale"], d["ids"], h, codes=codes, exps=exps,
+                                                 want_dx=False)
+    _, ga, gb, _, ba, bb = ref.backward(d, h, ref.restore(codes, exps))
+    ref.near(da, ga, ba, "da")
+    ref.near(db, gb, bb, "db")
+
+
 def _expands(M, N, K):
     """Whether all three products expand their int8 operand in the workspace."""
     for op, n in ((q8.Q8_OP_LINEAR_W8A16_LORA, N * K), (q8.Q8_OP_LINEAR_W8A16_LORA_BACKWARD, N * K),
