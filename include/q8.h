@@ -333,7 +333,7 @@ typedef struct {
  *     y[m,n] = s_w[n] * sum_k x[m,k] q[n,k] + bias[n] + scale[i] * sum_r h[m,r] b[i][n,r]
  * fp32 accumulation, one rounding to yt.  (Tensor cores cut a running sum off towards zero.
  * Results in fp32, here and in q8_checkpoint_wgrad, are sums of 1024 terms added up outside
- * them, unless few output tiles make two or four groups of SMs split the sum: one sum each.)
+ * them.)
  * A row whose id is outside [0, count) (-1 by
  * convention) has no adapter: its h is 0 and its y is q8_linear_w8a16_bias's sum.
  *   x device bf16 [M, K]; q device int8 [N, K]; s_w device fp32 [N]; bias device fp32 [N]

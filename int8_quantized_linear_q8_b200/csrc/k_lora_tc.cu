@@ -79,7 +79,7 @@ __host__ __device__ constexpr int lt_threads(int mode, bool pre) {
 // terms adds up (weight gradient of 4096 rows: 2.2e-6 off in the norm; plain fp32 3.0e-7).  Results
 // that are not rounded to bf16, which is 1000 times as coarse, are sums of LT_SUM stages added up
 // outside it (4.1e-7, for 2% of the time): the weight gradient and a forward pass with fp32
-// output.  Pairs that split a tile make one sum each, whatever its length.
+// output.  The expanded weight gradient adds them up in registers, the others in memory.
 constexpr int LT_SUM = 16;
 constexpr int LT_SMEM = LT_CTRL + 1024 + 512;
 static_assert(LT_SMEM <= 227 * 1024, "shared memory");
@@ -344,10 +344,14 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
     const int u0 = blockIdx.x / (2 * S), ustep = gridDim.x / (2 * S);
     const int nk = (a.C + LT_BK - 1) / LT_BK;
     const int half = BN >> 1;
-    // stages of a sum, and sums of a tile; pairs that split a tile make one sum each (of nk / S)
-    const bool sums = S == 1 && (MODE == LORA_WGRAD || (MODE == LORA_FWD && !a.out_bf16));
-    const int sum_n = sums ? (nk + LT_SUM - 1) / LT_SUM : 1, sum_len = (nk + sum_n - 1) / sum_n;
-    const int nsum = sums ? (nk + sum_len - 1) / sum_len : 1;
+    // stages of a sum, and this pair's sums of a tile
+    const bool sums = MODE == LORA_WGRAD || (MODE == LORA_FWD && !a.out_bf16);
+    const int most = (nk + S - 1) / S, own_nk = nk * (pair + 1) / S - nk * pair / S;
+    const int sum_n = sums ? (most + LT_SUM - 1) / LT_SUM : 1, sum_len = (most + sum_n - 1) / sum_n;
+    const int nsum = sums ? (own_nk + sum_len - 1) / sum_len : 1;
+    // where all sums but the last are added up (the pairs of a tile: each in a place of its own)
+    float* const partial = a.partial ? a.partial + (int64_t)pair * a.T * a.P
+                                     : reinterpret_cast<float*>(a.out);
     // Tiles run over t first, in even blocks of at most 8 t tiles: the pairs that run at once share both
     // operands through L2 and the int8 operand is read from HBM once per block.
     const int tblk = (num_t + (num_t + 7) / 8 - 1) / ((num_t + 7) / 8);
@@ -781,7 +785,7 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         LtRing<2> rt;
         bool live = true;
-        for (int u = u0; u < units && S == 1; u += ustep) {
+        for (int u = u0; u < units; u += ustep) {
             int p0, t0;
             tile_of(u, p0, t0);
             const int p = p0 + q * 32 + lane;
@@ -798,7 +802,7 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
                 __syncwarp();
                 if (lane == 0) lt_arrive(tempty0 + x.s * 8);
             };
-            if (PRE && MODE == LORA_WGRAD) {
+            if (PRE && MODE == LORA_WGRAD && S == 1) {
                 // the sums are added up in registers, 128 a thread
                 float total[4][32];
 #pragma unroll
@@ -834,10 +838,8 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
             float sw = 1.0f, bs = 0.0f;
             if (MODE == LORA_FWD && p < a.P) {
                 sw = ld_after(a.s_w + p);
-                if (a.bias) bs = ld_after(a.bias + p);
+                if (a.bias && S == 1) bs = ld_after(a.bias + p);
             }
-            // all sums but the last are added up in memory
-            float* const partial = a.partial ? a.partial : reinterpret_cast<float*>(a.out);
             const float* from = nullptr;
             if (MODE != LORA_DGRAD)
 #pragma unroll 1
@@ -860,6 +862,7 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
                     from = partial;
                     bs = 0.0f;
                 }
+            if (S > 1) break;                           // finished below, by all warps
             // forward: whether this pair has an adapter term besides its base sum
             Walk w = walk();
             w.kb = w.end;
@@ -940,8 +943,8 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
     if (S > 1) {
         // A tile of several pairs: all warps but the first three finish it.  Chunk c of 16 columns
         // belongs to pair c % S; a sender's parts of an owner's chunks lie at [sender][c / S]
-        // [column / 4][128 p][4 columns] of the owner's ring region.  (Chunks of 16 and rolled loops: this code
-        // runs once, and fetching its instructions is what it waits for.)
+        // [column / 4][128 p][4 columns] of the owner's ring region.  (Chunks of 16 and rolled
+        // loops: this code runs once, and fetching its instructions is what it waits for.)
         __syncwarp();
         const int q = warp & 3, par = (warp - LT_CONV0) >> 2, step = (LT_CONV + LT_EPI) / 4;
         const int chunks = BN / 16, own = (chunks + S - 1) / S;
@@ -953,6 +956,7 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
         const int64_t t1 = min((int64_t)t0 + BN, a.T);
         float sw = 1.0f, bs = 0.0f;
         bool low = false, live = warp >= LT_CONV0;
+        const int b1 = (nsum - 1) & 1, b2 = nsum & 1;           // buffers: last sum, adapter term
         if (live) {
             Walk w = walk();
             w.kb = w.end;
@@ -961,27 +965,35 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
                 sw = ld_after(a.s_w + p);
                 if (a.bias) bs = ld_after(a.bias + p);
             }
-            bool okw = mbar_wait(&tfull[0], 0, status, abort_flag);
-            if (low) okw = mbar_wait(&tfull[1], 0, status, abort_flag) && okw;
-            live = __shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         }
         auto part = [&](int c, float (&v)[16]) {
             uint32_t r[16];
-            lt_ld16(lanes + (uint32_t)(c * 16), r);
+            lt_ld16(lanes + (uint32_t)(b1 * 256 + c * 16), r);
             lt_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 v[j] = MODE == LORA_FWD ? __uint_as_float(r[j]) * sw : __uint_as_float(r[j]);
             if (low) {
-                lt_ld16(lanes + (uint32_t)(256 + c * 16), r);
+                lt_ld16(lanes + (uint32_t)(b2 * 256 + c * 16), r);
                 lt_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
             }
+            if (nsum > 1) {
+                const float* from = partial + (int64_t)(t0 + c * 16) * a.P + p;
+                const int rows = p < a.P ? (int)min((int64_t)16, t1 - t0 - c * 16) : 0;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (j < rows) v[j] += ld_after(from + (int64_t)j * a.P);
+            }
         };
+        // Every pair's MMAs (their issuer has waited for the last) and copies are done behind this:
+        // the sums are there and the rings are free.
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        lt_cluster_sync();              // every pair's MMAs and copies are done: rings are free
+        lt_cluster_sync();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        live = live && *abort_flag == 0;
 #pragma unroll 1
         for (int c = par; live && c < chunks; c += step) {
             const int o = c % S;
@@ -1037,6 +1049,11 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
 int lora_tc_tile(int64_t T) {
     const int64_t tiles = (T + 255) / 256;
     return (int)(((T + tiles - 1) / tiles + 31) / 32 * 32);
+}
+// Most pairs that split a tile's stages (148 SMs: 74 pairs).
+static int lora_max_split(int64_t P, int64_t T) {
+    const int64_t BN = lora_tc_tile(T), tiles = (P + 255) / 256 * ((T + BN - 1) / BN);
+    return tiles <= 18 ? 4 : tiles <= 37 ? 2 : 1;
 }
 size_t lora_list_bytes(int64_t T) {
     const int64_t BN = lora_tc_tile(T);
@@ -1099,7 +1116,7 @@ static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, in
     // Pairs that split a tile's stages: while all clusters run at once and each part keeps at
     // least 4 stages.
     int S = 1;
-    while (S < 4 && tiles * 2 <= num_sms / 2 / S && a.C / LT_BK >= 4 * 2 * S &&
+    while (2 * S <= lora_max_split(a.P, a.T) && tiles * 2 <= num_sms / 2 / S && a.C / LT_BK >= 4 * 2 * S &&
            tiles <= lora_tc_clusters<MODE, PRE>(2 * S))
         S *= 2;
     const int64_t clusters = tiles < num_sms / 2 ? tiles : num_sms / 2;
@@ -1190,9 +1207,13 @@ size_t lora_pre_bytes(int mode, int64_t P, int64_t C, int64_t T) {
     return T >= r.t && (long_sum || 2.0 * (double)P * (double)C * (double)T >= r.ops)
                ? (size_t)P * (size_t)C * 2 : 0;
 }
-size_t lora_partial_bytes(int64_t P, int64_t C, int64_t T) {
-    return C > LT_SUM * LT_BK && lora_pre_bytes(LORA_WGRAD, P, C, T) == 0
-               ? (size_t)P * (size_t)T * 4 : 0;
+// Partial sums: of every pair that may split a tile, or of the whole where neither registers nor
+// the result itself (accumulate) can hold them.
+size_t lora_partial_bytes(int mode, int64_t P, int64_t C, int64_t T) {
+    if (C <= LT_SUM * LT_BK || mode == LORA_DGRAD) return 0;
+    int64_t copies = lora_max_split(P, T);
+    if (copies == 1 && (mode == LORA_FWD || lora_pre_bytes(mode, P, C, T) > 0)) copies = 0;
+    return (size_t)copies * (size_t)P * (size_t)T * 4;
 }
 cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, bool beside,
                                cudaStream_t st) {

@@ -228,9 +228,10 @@ static q8_status check_adapter_pointers(const q8_adapters* ad, const int32_t* id
 // Up to 16 rows run the decode GEMV where it takes the shape; it needs the term [M, N].
 static inline bool lora_decodes(int64_t M, int64_t K) { return M <= 16 && w8a16_tma_fits(M, K); }
 // Workspaces of the GEMM forms (byte offsets): backward g fp32 [M, R]; h (or g) in two bf16
-// parts [M, 2 R]; the plan of the rows' adapters; the int8 weight in bf16, where it is expanded.
+// parts [M, 2 R]; the plan of the rows' adapters; the int8 weight in bf16, where it is expanded;
+// partial sums of y.
 struct LoraWs {
-    size_t g = 0, hp = 0, plan = 0, pre = 0, pre_bytes = 0, bytes = 0;
+    size_t g = 0, hp = 0, plan = 0, pre = 0, pre_bytes = 0, partial = 0, partial_bytes = 0, bytes = 0;
 };
 static LoraWs plan_lora(bool bwd, int64_t M, int64_t N, int64_t K, int64_t R) {
     LoraWs w;
@@ -239,7 +240,18 @@ static LoraWs plan_lora(bool bwd, int64_t M, int64_t N, int64_t K, int64_t R) {
     w.plan = w.hp + align_up((size_t)M * R * 4, 256);
     w.pre = w.plan + align_up(lora_plan_bytes(M), 256);
     w.pre_bytes = bwd ? lora_pre_bytes(LORA_DGRAD, K, N, M) : lora_pre_bytes(LORA_FWD, N, K, M);
-    w.bytes = w.pre + w.pre_bytes;
+    w.partial = w.pre + align_up(w.pre_bytes, 256);
+    w.partial_bytes = bwd ? 0 : lora_partial_bytes(LORA_FWD, N, K, M);
+    w.bytes = w.partial + w.partial_bytes;
+    return w;
+}
+static LoraWs plan_wgrad(int64_t M, int64_t N, int64_t K) {
+    LoraWs w;
+    if (M <= 0) return w;
+    w.pre_bytes = lora_pre_bytes(LORA_WGRAD, K, M, N);
+    w.partial = align_up(w.pre_bytes, 256);
+    w.partial_bytes = lora_partial_bytes(LORA_WGRAD, K, M, N);
+    w.bytes = w.partial + w.partial_bytes;
     return w;
 }
 static size_t lora_fwd_bytes(int64_t M, int64_t N, int64_t K, int64_t R) {
@@ -428,7 +440,7 @@ size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K, int extra) 
             return plan_gptq(N, K).bytes;
         case Q8_OP_CHECKPOINT_WGRAD:
             if (M > kLoraMaxM || N > kLoraMaxN) return 0;
-            return M > 0 ? lora_pre_bytes(LORA_WGRAD, K, M, N) + lora_partial_bytes(K, M, N) : 0;
+            return plan_wgrad(M, N, K).bytes;
         case Q8_OP_LINEAR_W8A16_LORA:
             if (M > kLoraMaxM || N > kLoraMaxN || !valid_rank(extra)) return 0;
             return lora_fwd_bytes(M, N, K, extra);
@@ -494,6 +506,7 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     a.lists = lora_plan_lists(ws + w.plan);
     a.R = R;
     Q8_TRY(launched(launch_lora_plan(ids, M, L, ws + w.plan, st)));
+    if (w.partial_bytes) a.partial = (float*)(ws + w.partial);
     Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
                                        ad->scale, ws + w.plan, h, hp, M, (int)K, R, L, st, sms)));
     if (w.pre_bytes) {
@@ -616,8 +629,8 @@ q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t
     if (M == 0 && accumulate) return Q8_OK;
     if (!dw || (M > 0 && (!dy || !codes || !exps))) return Q8_ERR_NULL;
     if (!aligned16(dw) || !aligned16(dy) || !aligned16(codes)) return Q8_ERR_ALIGN;
-    const size_t pre = M > 0 ? lora_pre_bytes(LORA_WGRAD, K, M, N) : 0;
-    const size_t need = M > 0 ? pre + lora_partial_bytes(K, M, N) : 0;     // one or the other
+    const LoraWs w = plan_wgrad(M, N, K);
+    const size_t need = w.bytes;
     if (need && (!workspace || ws_bytes < need)) return Q8_ERR_WORKSPACE;
     if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     int sms = 0;
@@ -635,8 +648,8 @@ q8_status q8_checkpoint_wgrad(const void* dy, const int8_t* codes, const uint8_t
     a.P = (int)K;
     a.C = (int)M;
     a.T = N;
-    if (need > pre) a.partial = (float*)workspace;
-    if (pre) {
+    if (w.partial_bytes) a.partial = (float*)((uint8_t*)workspace + w.partial);
+    if (w.pre_bytes) {
         Q8_TRY(launched(launch_lora_expand(LORA_WGRAD, a, (uint16_t*)workspace, false,
                                            st)));
         a.pre = (const uint16_t*)workspace;

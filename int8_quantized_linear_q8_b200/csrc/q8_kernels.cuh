@@ -211,7 +211,7 @@ struct LoraGemm {
     int gshift;
     void* out;
     int out_bf16, accumulate;
-    float* partial;             // LORA_WGRAD, not expanded, of long sums: partial sums, like out
+    float* partial;             // long sums in fp32: lora_partial_bytes, or nullptr
     int P, C;
     int64_t T;
     // adapter term (LORA_WGRAD: none): low = b (LORA_FWD) or a (LORA_DGRAD)
@@ -238,9 +238,9 @@ cudaError_t launch_lora_wgrad(const void* dy, const float* h, float* db, const v
 // adapter list of a token tile: [0] their number, then their ids in ascending order
 constexpr int LT_LIST = 260;
 int lora_tc_tile(int64_t T);                    // tokens per tile
-// bytes of the expansion, and (LORA_WGRAD) of the partial sums; 0: none
+// bytes of the expansion, and of the partial sums; 0: none
 size_t lora_pre_bytes(int mode, int64_t P, int64_t C, int64_t T);
-size_t lora_partial_bytes(int64_t P, int64_t C, int64_t T);
+size_t lora_partial_bytes(int mode, int64_t P, int64_t C, int64_t T);
 // beside: right behind launch_lora_shrink on the stream, and at the same time
 cudaError_t launch_lora_expand(int mode, const LoraGemm& a, uint16_t* out, bool beside,
                                cudaStream_t st);

@@ -276,7 +276,8 @@ def _one_sign(terms):
     return 33 * 2.0 ** -23 + (terms / 1024 + 6) * 2.0 ** -24
 
 
-@pytest.mark.parametrize("M,N,K", [(30000, 2560, 960), (20000, 264, 16384), (2048, 1024, 4096)])
+@pytest.mark.parametrize("M,N,K", [(30000, 2560, 960), (20000, 264, 16384), (2048, 1024, 4096),
+                                   (16384, 264, 512), (8192, 2048, 1024), (5000, 1000, 960)])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_long_gradient_sums_of_one_sign(M, N, K, accumulate):
     g = torch.Generator("cuda").manual_seed(42)
@@ -291,7 +292,9 @@ def test_long_gradient_sums_of_one_sign(M, N, K, accumulate):
     ref.near(dw, want, _one_sign(M) * want, "dw")
 
 
-@pytest.mark.parametrize("M,N,K", [(300, 8192, 65520), (3000, 2064, 16384), (40, 11008, 4096)])
+@pytest.mark.parametrize("M,N,K", [(300, 8192, 65520), (3000, 2064, 16384), (40, 11008, 4096),
+                                   (40, 4096, 16384), (300, 4096, 8192), (77, 5000, 4112), (33, 77, 4080),
+                                   (4096, 512, 16384)])
 def test_long_forward_sums_of_one_sign(M, N, K):
     d = ref.make(M, N, K, 8, 2, seed=43, mix="none", bias=True)
     d["x"] = d["x"].abs()
