@@ -333,9 +333,8 @@ typedef struct {
  *     y[m,n] = s_w[n] * sum_k x[m,k] q[n,k] + bias[n] + scale[i] * sum_r h[m,r] b[i][n,r]
  * fp32 accumulation, one rounding to yt.  (Tensor cores cut a running sum off towards zero.
  * Results in fp32, here and in q8_checkpoint_wgrad, are sums of 1024 terms added up outside
- * them.)
- * A row whose id is outside [0, count) (-1 by
- * convention) has no adapter: its h is 0 and its y is q8_linear_w8a16_bias's sum.
+ * them.)  A row whose id is outside [0, count) (-1 by convention) has no adapter: its h is 0
+ * and its y is q8_linear_w8a16_bias's sum.
  *   x device bf16 [M, K]; q device int8 [N, K]; s_w device fp32 [N]; bias device fp32 [N]
  *   (nullable, 4-byte aligned); ids device int32 [M] (4-byte aligned, values checked on the
  *   device only); y device [M, N] of type yt (Q8_BF16 or Q8_F32); h device fp32 [M, rank]
@@ -454,8 +453,9 @@ q8_status q8_gptq_int8(const float* W, const double* H, int64_t N, int64_t K, do
 
 /* Host.  Workspace bytes a linear needs for these sizes (0 if none).  `extra` is
  * "two-pass" (0/1) for Q8_OP_LINEAR_W8A8, G for Q8_OP_LINEAR_DQ8CA_Q4GSW, the block
- * size for Q8_OP_GPTQ_INT8 and the rank for the two adapter calls.  The 8da4w size for 17..64 rows also depends on the current
- * device's SM count (it sizes the K split of the 17..64-row GEMM).
+ * size for Q8_OP_GPTQ_INT8 and the rank for the two adapter calls.  The 8da4w size for
+ * 17..64 rows also depends on the current device's SM count (it sizes the K split of the
+ * 17..64-row GEMM).
  * Returns 0 for invalid arguments as well; the linear then reports the error. */
 size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K, int extra);
 

@@ -14,8 +14,8 @@
 // that MMA's rate, 2048 multiply-adds in 8 cycles a quarter of an SM).
 //
 // Measured at M = 4096, rank 16, 4 adapters: plan 10 us beside the expansion; h from 33 MB of x
-// 10 us; g from 90 MB of dy 25 us (3.6 TB/s); dA and dB from 107 MB 54 us, where the largest adapter, with 1.8 times its
-// share of the rows, is the last to end.  Most was gained by letting eight neighbouring threads
+// 10 us; g from 90 MB of dy 25 us (3.6 TB/s); dA and dB from 107 MB 54 us, where the largest
+// adapter, with 1.8 times its share of the rows, is the last to end.  Most was gained by letting eight neighbouring threads
 // copy a row's whole line (g 40 -> 26 us), reading a k step's fragments before the MMAs of the
 // one before, and vector loads of the low rows (84 -> 54 us).
 #include "q8_kernels.cuh"

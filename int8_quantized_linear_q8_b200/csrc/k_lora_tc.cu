@@ -352,8 +352,8 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
     // where all sums but the last are added up (the pairs of a tile: each in a place of its own)
     float* const partial = a.partial ? a.partial + (int64_t)pair * a.T * a.P
                                      : reinterpret_cast<float*>(a.out);
-    // Tiles run over t first, in even blocks of at most 8 t tiles: the pairs that run at once share both
-    // operands through L2 and the int8 operand is read from HBM once per block.
+    // Tiles run over t first, in even blocks of at most 8 t tiles: the pairs that run at once share
+    // both operands through L2 and the int8 operand is read from HBM once per block.
     const int tblk = (num_t + (num_t + 7) / 8 - 1) / ((num_t + 7) / 8);
     auto tile_of = [&](int u, int& p0, int& t0) {
         const int full = num_p * tblk, blk = u / full, rem = u - blk * full;
@@ -1116,8 +1116,8 @@ static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, in
     // Pairs that split a tile's stages: while all clusters run at once and each part keeps at
     // least 4 stages.
     int S = 1;
-    while (2 * S <= lora_max_split(a.P, a.T) && tiles * 2 <= num_sms / 2 / S && a.C / LT_BK >= 4 * 2 * S &&
-           tiles <= lora_tc_clusters<MODE, PRE>(2 * S))
+    while (2 * S <= lora_max_split(a.P, a.T) && tiles * 2 <= num_sms / 2 / S &&
+           a.C / LT_BK >= 4 * 2 * S && tiles <= lora_tc_clusters<MODE, PRE>(2 * S))
         S *= 2;
     const int64_t clusters = tiles < num_sms / 2 ? tiles : num_sms / 2;
     cudaLaunchConfig_t cfg = {};

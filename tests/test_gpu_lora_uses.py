@@ -293,8 +293,8 @@ def test_long_gradient_sums_of_one_sign(M, N, K, accumulate):
 
 
 @pytest.mark.parametrize("M,N,K", [(300, 8192, 65520), (3000, 2064, 16384), (40, 11008, 4096),
-                                   (40, 4096, 16384), (300, 4096, 8192), (77, 5000, 4112), (33, 77, 4080),
-                                   (4096, 512, 16384)])
+                                   (40, 4096, 16384), (300, 4096, 8192), (77, 5000, 4112),
+                                   (33, 77, 4080), (4096, 512, 16384)])
 def test_long_forward_sums_of_one_sign(M, N, K):
     d = ref.make(M, N, K, 8, 2, seed=43, mix="none", bias=True)
     d["x"] = d["x"].abs()
