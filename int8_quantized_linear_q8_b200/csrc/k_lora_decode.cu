@@ -8,8 +8,9 @@
 // M * rank * (K + N) * 2 bytes in all, against N * K of the int8 weight.
 //
 // A cluster of eight CTAs per row: its 64 warps share out the rank's rows of A (and parts of K
-// when the rank is below 64), every warp leaves its sums in all eight CTAs' shared memory, and
-// after one cluster barrier each CTA makes an eighth of the row of t.  The kernel lets the
+// when the rank is below 64), every warp leaves its sums in all eight CTAs' shared memory (behind
+// a cluster barrier, since the others have to have started), and after a second barrier each CTA
+// makes an eighth of the row of t.  The kernel lets the
 // weight stream start as soon as the stream's earlier work is done (programmatic dependent
 // launch); the stream waits for t only when its first rows are summed.
 //
@@ -33,6 +34,9 @@ __global__ __cluster_dims__(LD_CTAS, 1, 1) __launch_bounds__(LD_THREADS) void k_
     float* __restrict__ t, int64_t N, int K, int R, int L) {
     __shared__ float sums[LD_SUMS];
     __shared__ __align__(16) float hs[256];
+    // A CTA's shared memory may be written by another once it runs: each says so here and waits for
+    // the others before its first sum leaves, by when the id has been read and they have.
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int m = blockIdx.y, part = blockIdx.x;            // a row's cluster: its CTAs in order
@@ -51,6 +55,8 @@ __global__ __cluster_dims__(LD_CTAS, 1, 1) __launch_bounds__(LD_THREADS) void k_
     const int parts = R >= 64 ? 1 : 64 / R;
     const int chunks = (K + 255) / 256;                     // of 256 k: 8 a lane
     const uint32_t out = (uint32_t)__cvta_generic_to_shared(sums);
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     for (int j = part * LD_WARPS + warp; j < R * parts; j += LD_CTAS * LD_WARPS) {
         float v = 0.0f;
         if (has) {

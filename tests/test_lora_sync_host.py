@@ -1,0 +1,49 @@
+"""The ordering rules of the adapter kernels, read from their sources (no GPU needed): each is one
+whose breach could lose a value or leave a kernel waiting only now and then, so that no run
+shows it reliably."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "int8_quantized_linear_q8_b200", "csrc")
+
+
+def _code(name):
+    """The file without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def _body(text, name):
+    """The body of the function `name`, braces matched."""
+    at = re.search(r"\b%s\s*\([^;{]*?\)\s*\{" % name, text, re.S).end()
+    depth, end = 1, at
+    while depth:
+        depth += {"{": 1, "}": -1}.get(text[end], 0)
+        end += 1
+    return text[at:end]
+
+
+def _first(body, words):
+    found = [body.find(w) for w in words if w in body]
+    return min(found) if found else None
+
+
+BARRIER = ("barrier.cluster.wait", "cluster_sync_all(", "lt_cluster_sync(")
+PEER = ("st.shared::cluster", "ld.shared::cluster", "cluster_sum4(", "lt_arrive(", "lt_tma_pair(",
+        "lt_commit(")
+
+
+@pytest.mark.parametrize("source,kernel", [("k_lora_decode.cu", "k_lora_decode"),
+                                           ("k_lora.cu", "k_lora_shrink"),
+                                           ("k_lora.cu", "lora_grad_tile"),
+                                           ("k_lora_tc.cu", "k_lora_tc")])
+def test_a_cluster_has_started_before_its_shared_memory_is_used(source, kernel):
+    """Another CTA's shared memory may be touched once that CTA is known to run: behind a
+    cluster barrier."""
+    body = _body(_code(source), kernel)
+    barrier, peer = _first(body, BARRIER), _first(body, PEER)
+    assert peer is not None and barrier is not None
+    assert barrier < peer
