@@ -53,7 +53,7 @@
 // T tile (16 KB each) share a slot of a ring of five (PRE: seven), so that the issuing warp, whose
 // own steps bound the main loop, has one barrier to wait for and one commit to make per stage; it
 // tests the next stage's barrier before it issues this stage's MMAs, which hides the test.  Every
-// wait is bounded.
+// wait is bounded, and what a warp does when one runs out goes by a vote: its lanes may differ.
 #include "q8_kernels.cuh"
 
 namespace q8 {
@@ -610,7 +610,8 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
 #pragma unroll 1
                 for (; kb < w.end; kb += 2) {
                     const uint32_t raw = smem_u32(smem + LT_RT + rq.s * LT_RAW);
-                    live = mbar_wait(&rfull[rq.s], rq.ph, status, abort_flag) && live;
+                    live = __all_sync(0xffffffffu, mbar_wait(&rfull[rq.s], rq.ph, status, abort_flag) &&
+                                                       live);
                     uint4 cw[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -648,7 +649,8 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
                     if (lane == 0) mbar_arrive(&rempty[rq.s]);
                     rq.next2();
                     const uint32_t at = smem_u32(smem + rc.s * LT_SLOT);
-                    live = mbar_wait(&empty[rc.s], rc.ph ^ 1u, status, abort_flag) && live;
+                    live = __all_sync(0xffffffffu, mbar_wait(&empty[rc.s], rc.ph ^ 1u, status,
+                                                             abort_flag) && live);
                     if (live) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -705,11 +707,11 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
             for (; w.kb < w.end; ++w.kb) {
                 if (it % GROUPS == grp) {
                     const uint32_t at = smem_u32(smem + r.s * LT_SLOT), bt = at + LT_A;
-                    const bool okw =
-                        PRE ? mbar_wait(&lgo[r.s], lph >> r.s & 1u, status, abort_flag)
-                            : mbar_wait(&empty[r.s], r.ph ^ 1u, status, abort_flag);
+                    live = __all_sync(0xffffffffu,
+                                      mbar_wait(PRE ? &lgo[r.s] : &empty[r.s],
+                                                PRE ? lph >> r.s & 1u : r.ph ^ 1u, status,
+                                                abort_flag) && live);
                     lph ^= 1u << r.s;
-                    live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
                     // Columns (kb - nk) * 64 .. +64 of the adapter term, in pieces of 8: per adapter
                     // of the list R / 8 pieces against the high parts and R / 8 against the
                     // rest; `in` is a piece's place among an adapter's.
@@ -793,8 +795,8 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
             const int chunks = (BN + 31) / 32;
             // a sum is there, or its place is free again
             auto wait_sum = [&](const LtRing<2>& x) {
-                const bool okw = mbar_wait(&tfull[x.s], x.ph, status, abort_flag);
-                live = live && (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) != 0);
+                live = __all_sync(0xffffffffu, mbar_wait(&tfull[x.s], x.ph, status, abort_flag) &&
+                                                   live);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             };
             auto free_sum = [&](const LtRing<2>& x) {
@@ -993,7 +995,7 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
         __syncwarp();
         lt_cluster_sync();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        live = live && *abort_flag == 0;
+        live = __all_sync(0xffffffffu, *abort_flag == 0) && live;
 #pragma unroll 1
         for (int c = par; live && c < chunks; c += step) {
             const int o = c % S;

@@ -47,3 +47,15 @@ def test_a_cluster_has_started_before_its_shared_memory_is_used(source, kernel):
     barrier, peer = _first(body, BARRIER), _first(body, PEER)
     assert peer is not None and barrier is not None
     assert barrier < peer
+
+
+def test_a_warp_goes_on_from_a_wait_as_one():
+    """A wait that runs out may do so for some lanes of a warp and not for others, so what
+    follows (shuffles, warp barriers, tensor-memory reads, which need the whole warp) goes by a
+    vote."""
+    body = _body(_code("k_lora_tc.cu"), "k_lora_tc")
+    waits = [m.start() for m in re.finditer(r"\bmbar_wait\(", body)]
+    assert len(waits) >= 9
+    for at in waits:
+        statement = body[max(body.rfind(c, 0, at) for c in ";{}"):at]
+        assert "__all_sync(0xffffffffu," in statement, body[at - 120:at + 80]
