@@ -1040,11 +1040,17 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
 
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    lt_cluster_sync();      // the other CTA's MMAs, copies and arrivals here are complete
+    lt_cluster_sync();      // the other CTA's copies and its threads' arrivals here are complete
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (warp == 1)
+    if (warp == 1) {
+        // Arrivals of commits are the tensor core's, not a thread's, and the barrier above says
+        // nothing of those in the pair's second CTA.  They come in the order of the commits, so the
+        // last one's is the end of them.
+        mbar_drain(mma_done, 0, status);
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                      : "memory");
+    }
 }
 
 // ----------------------------------------------------------------------- host side

@@ -59,3 +59,17 @@ def test_a_warp_goes_on_from_a_wait_as_one():
     for at in waits:
         statement = body[max(body.rfind(c, 0, at) for c in ";{}"):at]
         assert "__all_sync(0xffffffffu," in statement, body[at - 120:at + 80]
+
+
+def test_both_ctas_of_a_pair_see_the_last_commit():
+    """The issuer's commits arrive in both CTAs' shared memory some time after it leaves, so
+    each CTA waits for the last of them, the first one before its tensor memory is read and the
+    other one before it ends."""
+    body = _body(_code("k_lora_tc.cu"), "k_lora_tc")
+    assert "lt_commit(mma_done, both)" in body
+    last_sync = body.rfind("lt_cluster_sync();")
+    tail = body[last_sync:]
+    drain, dealloc = tail.find("mbar_drain(mma_done, 0, status)"), tail.find("tcgen05.dealloc")
+    assert 0 < drain < dealloc
+    # not under a condition on the CTA's rank
+    assert "rank" not in tail[:drain]
