@@ -42,7 +42,7 @@ __global__ __launch_bounds__(256) void k_checkpoint_save(const void* __restrict_
             const uint4* p = reinterpret_cast<const uint4*>(x) + 2 * i;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint4 w = ldg_stream(p + h);
+                const uint4 w = ld_after16_stream(p + h);
                 const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -51,14 +51,14 @@ __global__ __launch_bounds__(256) void k_checkpoint_save(const void* __restrict_
                 }
             }
         } else {
-            const float4* p = reinterpret_cast<const float4*>(x) + 4 * i;
+            const uint4* p = reinterpret_cast<const uint4*>(x) + 4 * i;
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-                const float4 w = ldg_f4(reinterpret_cast<const float*>(p + h));
-                v[4 * h] = w.x;
-                v[4 * h + 1] = w.y;
-                v[4 * h + 2] = w.z;
-                v[4 * h + 3] = w.w;
+                const uint4 w = ld_after16_stream(p + h);
+                v[4 * h] = __uint_as_float(w.x);
+                v[4 * h + 1] = __uint_as_float(w.y);
+                v[4 * h + 2] = __uint_as_float(w.z);
+                v[4 * h + 3] = __uint_as_float(w.w);
             }
         }
     }
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(256) void k_checkpoint_load(const int8_t* __restric
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n16) return;
     const int shift = G == 32 ? 1 : G == 64 ? 2 : G == 128 ? 3 : 4;    // pieces of a group, log2
-    const uint4 w = ldg_stream(reinterpret_cast<const uint4*>(codes) + i);
+    const uint4 w = ld_after16_stream(codes + 16 * i);
     const uint32_t e = ld_after(exps + (i >> shift));
     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
     if (BF16) {

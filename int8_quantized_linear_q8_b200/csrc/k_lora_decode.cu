@@ -68,7 +68,7 @@ __global__ __cluster_dims__(LD_CTAS, 1, 1) __launch_bounds__(LD_THREADS) void k_
             for (int c = chunks * q / parts; c < c1; ++c) {
                 const int k = c * 256 + lane * 8;
                 if (k >= K) break;
-                const uint4 a = ldg_keep(ap + k), b = ldg_keep(xp + k);
+                const uint4 a = ld_after16(ap + k), b = ld_after16(xp + k);
                 v = fmaf(bf16lo(a.x), bf16lo(b.x), v);
                 v = fmaf(bf16hi(a.x), bf16hi(b.x), v);
                 v = fmaf(bf16lo(a.y), bf16lo(b.y), v);
@@ -110,8 +110,9 @@ __global__ __cluster_dims__(LD_CTAS, 1, 1) __launch_bounds__(LD_THREADS) void k_
                 uint4 b[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    b[u] = n + u * LD_THREADS < n1 ? ldg_keep(bp + (int64_t)u * LD_THREADS * R + r)
-                                                   : make_uint4(0, 0, 0, 0);
+                    b[u] = n + u * LD_THREADS < n1
+                               ? ld_after16(bp + (int64_t)u * LD_THREADS * R + r)
+                               : make_uint4(0, 0, 0, 0);
                 const float4 h0 = *reinterpret_cast<const float4*>(hs + r);
                 const float4 h1 = *reinterpret_cast<const float4*>(hs + r + 4);
 #pragma unroll

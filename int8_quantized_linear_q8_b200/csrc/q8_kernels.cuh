@@ -71,8 +71,8 @@ __device__ __forceinline__ void cp_wait() {
 
 // Loads of what an earlier kernel may have written, in kernels that start before it ends
 // (programmatic dependent launch): volatile, so that none is moved ahead of the
-// griddepcontrol.wait before it, as the compiler may a __ldg, which it takes to read memory that
-// never changes.
+// griddepcontrol.wait before it, as the compiler may a __ldg, and without the promise of ld.global.nc
+// (ldg_stream and its like) that the memory does not change while the kernel lives.
 __device__ __forceinline__ int ld_after(const int* p) {
     int v;
     asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -88,10 +88,19 @@ __device__ __forceinline__ uint32_t ld_after(const uint8_t* p) {
     asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ float4 ld_after4(const float* p) {
-    float4 v;
-    asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+// 16 bytes at once: kept in L1 (small operands re-read by many warps), or streamed past it
+__device__ __forceinline__ uint4 ld_after16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 ld_after16_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p)
                  : "memory");
     return v;

@@ -37,3 +37,29 @@ def test_rows_of_up_to_16_with_and_without_adapters(M, N, K, R, free):
         wrong += (yb != y).any() | (hb != h).any()
     assert int(wrong) == 0
     assert q8.q8_last_device_status() == q8.Q8_OK
+
+
+@pytest.mark.parametrize("M", [1, 16, 700])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_buffer_written_by_the_call_before(M, dtype):
+    """One buffer, written by a call and read by the next one with nothing in between, its values
+    other ones each time: checkpoints restored, taken again and used."""
+    K, G, n = 960, 32, 4
+    ds = [ref.make(M, 136, K, 8, 2, seed=70 + i) for i in range(n)]
+    kept = [q8.q8_checkpoint_save(d["x"], G) for d in ds]
+    x = torch.empty(M, K, dtype=dtype, device="cuda")
+    c, e = torch.empty_like(kept[0][0]), torch.empty_like(kept[0][1])
+    back = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    got = [[torch.empty_like(back), None, None] for _ in range(20 * n)]
+    args = [ds[0][k] for k in ("q", "s_w", "a", "b", "scale", "ids")]
+    want = [q8.q8_linear_w8a16_lora(q8.q8_checkpoint_load(*k), *args)[0] for k in kept]
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        q8.q8_checkpoint_load(*kept[i % n], y=x, out_dtype=dtype)
+        q8.q8_checkpoint_save(x, G, codes=c, exps=e)
+        q8.q8_checkpoint_load(c, e, y=out[0])
+        q8.q8_checkpoint_load(c, e, y=back)
+        out[1] = q8.q8_linear_w8a16_lora(back, *args)[0]
+    for i, out in enumerate(got):
+        assert torch.equal(out[0], q8.q8_checkpoint_load(*kept[i % n])), i
+        assert torch.equal(out[1], want[i % n]), i

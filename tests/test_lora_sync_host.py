@@ -73,3 +73,12 @@ def test_both_ctas_of_a_pair_see_the_last_commit():
     assert 0 < drain < dealloc
     # not under a condition on the CTA's rank
     assert "rank" not in tail[:drain]
+
+
+@pytest.mark.parametrize("source", ["k_checkpoint.cu", "k_lora_decode.cu", "k_lora.cu"])
+def test_what_the_kernel_before_writes_is_not_read_as_constant(source):
+    """These kernels start while the one before them still writes what they read, so none of
+    their loads may promise memory that does not change while they live (ld.global.nc)."""
+    text = _code(source)
+    assert "griddepcontrol.wait" in text
+    assert not re.findall(r"\bldg_\w+|\b__ldg\b|global\.nc", text)
