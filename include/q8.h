@@ -393,13 +393,17 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
  *     codes[m,k] = clamp(round(x[m,k] * 2^-e), -127, 127)       (ties to even)
  * An all-zero group gets exponent byte 1 and codes 0.  code * 2^e is a bf16 number, so
  * nothing is rounded again when the checkpoint is restored or used.
+ * A group that holds a NaN or an infinity gets exponent byte 255 (2^e infinite), codes of 127
+ * and -127 for its infinities and 0 for the rest: infinities are restored as they were, the
+ * group's other values as NaN, and gradients from it are NaN or infinite where they read it.
  *   x device [M, K] of type xt (Q8_BF16 or Q8_F32); codes device int8 [M, K]; exps device
  *   uint8 [M, K / group], of any alignment; group 32, 64, 128 or 256 (Q8_ERR_ARG),
  *   K % group == 0 (Q8_ERR_SHAPE).  Codes and exponents are bit-identical to the definition. */
 q8_status q8_checkpoint_save(const void* x, q8_dtype xt, int64_t M, int64_t K, int group,
                              int8_t* codes, uint8_t* exps, void* stream);
 
-/* The values a checkpoint stands for, code * 2^(exps - 127), exact in either type.
+/* The values a checkpoint stands for, code * 2^(exps - 127), exact in either type (byte 255:
+ * +-127 stands for an infinity, 0 for NaN).
  *   y device [M, K] of type yt; the other arguments as q8_checkpoint_save. */
 q8_status q8_checkpoint_load(const int8_t* codes, const uint8_t* exps, int group, void* y,
                              q8_dtype yt, int64_t M, int64_t K, void* stream);

@@ -615,7 +615,8 @@ def _saved(codes: torch.Tensor, exps: torch.Tensor, M: int, K: int, dev: int) ->
 
 def q8_checkpoint_save(x: torch.Tensor, group: int = 128, codes=None, exps=None, stream=None):
     """8-bit checkpoint of a bf16 or fp32 [M, K] activation -> (codes int8 [M,K], exponent
-    bytes uint8 [M, K/group]); a code counts steps of 2^(byte - 127)."""
+    bytes uint8 [M, K/group]); a code counts steps of 2^(byte - 127).  A group with a NaN or an
+    infinity gets byte 255: restored, its infinities are the same and its other values NaN."""
     M, K = _rows(x, "x")
     dev = _device(x)
     bf16 = x.dtype is torch.bfloat16

@@ -11,6 +11,10 @@
 // when 1.f <= 127 / 64, else at p - 5; in exponent bytes b = byte(absmax) - 6 (+ 1 when the
 // fraction is above 0x7E0000).  -126 keeps 2^e a normal number, 121 keeps 127 * 2^e finite.
 //
+// A NaN or an infinity must not come back as a number, or the gradients made from it would hide
+// it.  Its group gets b = 255, whose 2^e is infinite in bf16 and fp32 alike: codes of +-127 restore
+// infinities, code 0 a NaN (0 * inf), which the group's other values become as well.
+//
 // Bound by HBM: 3 bytes a bf16 value (and 1 / G) each way.  One thread per 16 values; 4096 x 11008,
 // G = 128: save 26.9 us (5.1 TB/s), load 22.8 us (6.0 TB/s; a copy reaches 6.55).  More pieces a
 // thread were slower (two: 28.0 and 24.6 us, four: 32.4 and 26.5), streaming stores the same.
@@ -18,10 +22,19 @@
 
 namespace q8 {
 
+constexpr uint32_t CKPT_INF = 0x7F800000u, CKPT_NONE = 255u;
 __device__ __forceinline__ uint32_t ckpt_exponent(float amax) {
     const uint32_t u = __float_as_uint(amax) & 0x7FFFFFFFu;
+    if (u >= CKPT_INF) return CKPT_NONE;
     const int b = (int)(u >> 23) - 6 + ((u & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
     return (uint32_t)min(max(b, 1), 248);
+}
+
+// The larger one, or NaN if either is (fmaxf would drop it).
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
 }
 
 // One thread per 16 values; the G / 16 threads of a group are neighbours in a warp.
@@ -64,19 +77,33 @@ __global__ __launch_bounds__(256) void k_checkpoint_save(const void* __restrict_
     }
     float amax = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(v[j]));
-    for (int o = per >> 1; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    for (int j = 0; j < 16; ++j) amax = max_or_nan(amax, fabsf(v[j]));
+    for (int o = per >> 1; o > 0; o >>= 1)
+        amax = max_or_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (!live) return;
     const uint32_t b = ckpt_exponent(amax);
     const float inv = __uint_as_float((254u - b) << 23);       // 2^-e
     uint32_t o[4];
+    if (b != CKPT_NONE) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        int c[4];
+        for (int j = 0; j < 4; ++j) {
+            int c[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            c[k] = __float2int_rn(fminf(fmaxf(rintf(v[4 * j + k] * inv), -127.0f), 127.0f));
-        o[j] = pack4_s8(c[0], c[1], c[2], c[3]);
+            for (int k = 0; k < 4; ++k)
+                c[k] = __float2int_rn(fminf(fmaxf(rintf(v[4 * j + k] * inv), -127.0f), 127.0f));
+            o[j] = pack4_s8(c[0], c[1], c[2], c[3]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            int c[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t u = __float_as_uint(v[4 * j + k]);
+                c[k] = u == CKPT_INF ? 127 : u == (CKPT_INF | 0x80000000u) ? -127 : 0;
+            }
+            o[j] = pack4_s8(c[0], c[1], c[2], c[3]);
+        }
     }
     reinterpret_cast<uint4*>(codes)[i] = make_uint4(o[0], o[1], o[2], o[3]);
     if ((i & (per - 1)) == 0) exps[i / per] = (uint8_t)b;
