@@ -333,7 +333,9 @@ typedef struct {
  *     y[m,n] = s_w[n] * sum_k x[m,k] q[n,k] + bias[n] + scale[i] * sum_r h[m,r] b[i][n,r]
  * fp32 accumulation, one rounding to yt.  (Tensor cores cut a running sum off towards zero.
  * Results in fp32, here and in q8_checkpoint_wgrad, are sums of 1024 terms added up outside
- * them.)  A row whose id is outside [0, count) (-1 by convention) has no adapter: its h is 0
+ * them.  scale * h meets b as a whole fp32 number; with a Q8_BF16 result it may be cut to 16
+ * bits, off by at most 2^-17, against 2^-8 for that result's rounding.)
+ * A row whose id is outside [0, count) (-1 by convention) has no adapter: its h is 0
  * and its y is q8_linear_w8a16_bias's sum.
  *   x device bf16 [M, K]; q device int8 [N, K]; s_w device fp32 [N]; bias device fp32 [N]
  *   (nullable, 4-byte aligned); ids device int32 [M] (4-byte aligned, values checked on the
@@ -365,8 +367,9 @@ typedef struct {
  *     da[i][r,k] = sum_{m: ids[m] = i} g[m,r] x[m,k]
  *     db[i][n,r] = scale[i] * sum_{m: ids[m] = i} dy[m,n] h[m,r]
  * fp32 accumulation.  s_w[n] * q[n,k] is rounded to bf16 once on its way to the tensor
- * cores (s_w varies along the summed axis, so it cannot be applied after the sum); dx is
- * rounded to bf16 once.  Sums are taken in an order that depends on sizes and ids only.
+ * cores (s_w varies along the summed axis, so it cannot be applied after the sum), g meets a
+ * in 16 bits (2^-17) and dx is rounded to bf16 once; da and db use all of g and h.  Sums are
+ * taken in an order that depends on sizes and ids only.
  *   dy device bf16 [M, N]; ids, adapters, q, s_w as in the forward call; h device fp32
  *   [M, rank] as the forward call wrote it (read iff db); input: the layer's input (read iff
  *   da; exps of any alignment, group 0, 32, 64, 128 or 256 with K % group == 0);

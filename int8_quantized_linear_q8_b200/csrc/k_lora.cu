@@ -306,7 +306,7 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
                                                      const int* __restrict__ off,
                                                      const int* __restrict__ tiles, int C, int R,
                                                      int S, float* __restrict__ h,
-                                                     uint16_t* __restrict__ hp) {
+                                                     uint16_t* __restrict__ hp, int hparts) {
     extern __shared__ __align__(1024) uint8_t sm[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -430,15 +430,21 @@ __global__ __launch_bounds__(128) void k_lora_shrink(const uint16_t* __restrict_
             }
         slot = (slot + 1) % LSH;
     }
-    // h (or g) in fp32, and times the scale in two bf16 parts, [M, 2 R]: high, rest
+    // h (or g) in fp32, and times the scale in bf16 parts, [M, parts * R]: each is what the ones
+    // before it leave over, rounded to nearest
     const float f = ld_after(scale + key);
     auto put = [&](int row, int r, float v) {
         const int64_t m = ld_after(perm + start + row);
         const float sv = v * f;
         h[m * R + r0 + r] = BWD ? sv : v;
+        const int parts = BWD ? lora_parts(true) : hparts;
+        uint16_t* to = hp + m * parts * R + r0 + r;
         const uint32_t hi = bf16_bits_rn(sv);
-        hp[m * 2 * R + r0 + r] = (uint16_t)hi;
-        hp[m * 2 * R + R + r0 + r] = (uint16_t)bf16_bits_rn(sv - __uint_as_float(hi << 16));
+        const float rest = sv - __uint_as_float(hi << 16);
+        const uint32_t mid = bf16_bits_rn(rest);
+        to[0] = (uint16_t)hi;
+        to[R] = (uint16_t)mid;
+        if (parts > 2) to[2 * R] = (uint16_t)bf16_bits_rn(rest - __uint_as_float(mid << 16));
     };
     const int g = lane >> 2, t = lane & 3;
     if (S == 1) {
@@ -776,8 +782,8 @@ static_assert(lsh_smem<1>() >= 64 * 12 * 4 && lsh_smem<8>() >= 64 * 68 * 4, "roo
 static int rank_tiles(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : R <= 32 ? 4 : 8; }
 
 cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, const float* scale,
-                               const void* ws, float* h, uint16_t* hp, int64_t M, int C, int R,
-                               int L, cudaStream_t st, int num_sms) {
+                               const void* ws, float* h, uint16_t* hp, int parts, int64_t M, int C,
+                               int R, int L, cudaStream_t st, int num_sms) {
     const LoraPlan p = plan_of(M);
     const uint8_t* wsb = (const uint8_t*)ws;
     const int* perm = (const int*)(wsb + p.perm);
@@ -796,7 +802,7 @@ cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, c
         if (e != cudaSuccess) return e;                                                       \
         return launch_clustered(k_lora_shrink<NT_, B_>, grid, 128, S, lsh_smem<NT_>(), true, st,   \
                                 x, w, scale,                                                  \
-                                perm, off, tl, C, R, S, h, hp);                                   \
+                                perm, off, tl, C, R, S, h, hp, parts);                        \
     } while (0)
 #define LORA_SHRINK_NT(NT_)              \
     do {                                 \

@@ -21,7 +21,8 @@
 // The adapter term is more of the same contraction: for the adapters that the tile's tokens
 // use (a list made per tile beforehand), the rank's columns of b (or a) on the P side and of
 // scale * h (or g) on the T side, zero for tokens of other adapters.  h comes as two bf16 parts
-// (high and rest: off by at most 2^-17), so an adapter takes 2 * rank columns.  Forward it goes
+// (off by at most 2^-17) where the result is bf16, as three (all of the fp32 number) where it is
+// fp32, so an adapter takes 2 or 3 * rank columns.  Forward it goes
 // to the other accumulator buffer, since s_w applies to the base sum alone.
 //
 // Two variants.  PRE: the int8 operand was expanded to bf16 in the workspace beforehand
@@ -313,7 +314,10 @@ __device__ __forceinline__ void lt_store(const LoraGemm& a, int t0, int64_t t1, 
         lt_store_rows<MODE, W, false>(a, t0, (int)(t1 - t0), p, v, to, from, add);
 }
 
-template <int MODE, bool PRE>
+// PARTS: bf16 parts of scale * h or g, lora_parts of the result's type.  (A constant, which leaves
+// the bf16 forms as fast as when there was no third part.  fp32, 77 rows, 2048 x 8192, 8 adapters:
+// rank 64, which takes 24 adapter stages a tile instead of 16, 26.4 -> 28.7 us; rank 16 27.6 -> 28.3.)
+template <int MODE, bool PRE, int PARTS>
 __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
     const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap tmap,
     const LoraGemm a, int BN, int num_p, int num_t, int S, int* status) {
@@ -379,7 +383,7 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
         if (w.low) return false;
         if (EARLY) asm volatile("griddepcontrol.wait;" ::: "memory");
         const int cnt = ld_after(a.lists + (int64_t)(t0 / BN) * LT_LIST);
-        const int total = (cnt * 2 * a.R + LT_BK - 1) / LT_BK;
+        const int total = (cnt * PARTS * a.R + LT_BK - 1) / LT_BK;
         w.low = true;
         w.kb = nk + total * pair / S;
         w.end = nk + total * (pair + 1) / S;
@@ -690,7 +694,12 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
             // one before the last.)
             if (!more(w, t0)) continue;
             const int* list = a.lists + (int64_t)(t0 / BN) * LT_LIST;
-            const int cnt = ld_after(list), rc2 = a.R >> 2;
+            const int cnt = ld_after(list), per = PARTS * (a.R >> 3);
+            auto column = [&](int in) {                     // of the rank
+                const int r8 = a.R >> 3;
+                if (PARTS > 2 && in >= 2 * r8) in -= r8;
+                return (in >= r8 ? in - r8 : in) * 8;
+            };
             // Copies: eight neighbouring threads take a row's 128 bytes (a thread a row, every
             // request touched 32 lines, and a stage took 1.4 us).  Thread: piece pc of rows
             // pr, pr + 16, ...; b's rows for the P tile, h's (or g's) for the T tile.
@@ -702,7 +711,7 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
             for (int i = 0; i < 8; ++i)
                 ids[i] = 16 * i < half && tr + 16 * i < a.T ? ld_after(a.ids + tr + 16 * i) : -1;
             // the list's entries win .. win + 31, one a lane
-            int win = (w.kb - nk) * 8 / rc2;
+            int win = (w.kb - nk) * 8 / per;
             int entry = ld_after(list + 1 + min(win + lane, 255));
             for (; w.kb < w.end; ++w.kb) {
                 if (it % GROUPS == grp) {
@@ -713,36 +722,36 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
                                                 abort_flag) && live);
                     lph ^= 1u << r.s;
                     // Columns (kb - nk) * 64 .. +64 of the adapter term, in pieces of 8: per adapter
-                    // of the list R / 8 pieces against the high parts and R / 8 against the
-                    // rest; `in` is a piece's place among an adapter's.
-                    const int first = (w.kb - nk) * 8, e0 = first / rc2;
+                    // of the list R / 8 pieces against the high parts, then as many against
+                    // each of the others; `in` is a piece's place among an adapter's.
+                    const int first = (w.kb - nk) * 8, e0 = first / per;
                     if (e0 + 4 > win + 31) {                    // a stage spans at most 5 adapters
                         win = e0;
                         entry = ld_after(list + 1 + min(win + lane, 255));
                     }
-                    const int e = (first + pc) / rc2, in = first + pc - e * rc2;
+                    const int e = (first + pc) / per, in = first + pc - e * per;
                     const int ad = __shfl_sync(0xffffffffu, entry, e - win);
                     if (live) {
                         if (A_MN) {                             // rows of a: r, 256 bytes of p each
                             const int ar = tid >> 4, ac = tid & 15, p = p0 + ac * 8;
                             const uint32_t to = at + (ac >> 3) * 8192 + ar * 128 +
                                                 (((ac & 7) ^ ar) << 4);
-                            int ec = e0, ic = first - e0 * rc2;
+                            int ec = e0, ic = first - e0 * per;
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
                                 const int adc = __shfl_sync(0xffffffffu, ad, c);
-                                const int col = (ic >= rc2 >> 1 ? ic - (rc2 >> 1) : ic) * 8;
+                                const int col = column(ic);
                                 const bool pl = ec < cnt && p < a.P;
                                 cp_async16(to + 1024 * c,
                                            pl ? a.low + ((int64_t)adc * a.R + col + ar) * a.P + p
                                               : a.low, pl);
-                                if (++ic == rc2) {
+                                if (++ic == per) {
                                     ic = 0;
                                     ++ec;
                                 }
                             }
                         } else {
-                            const int col = (in >= rc2 >> 1 ? in - (rc2 >> 1) : in) * 8;
+                            const int col = column(in);
                             const uint16_t* src =
                                 a.low + ((int64_t)ad * a.P + p0 + pr) * a.R + col;
 #pragma unroll
@@ -752,13 +761,13 @@ __global__ __launch_bounds__(lt_threads(MODE, PRE), 1) void k_lora_tc(
                                            pl ? src + (int64_t)(16 * i) * a.R : a.low, pl);
                             }
                         }
-                        const uint16_t* src = a.hp + (int64_t)tr * 2 * a.R + in * 8;
+                        const uint16_t* src = a.hp + (int64_t)tr * PARTS * a.R + in * 8;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             if (16 * i < half) {
                                 const bool tl = e < cnt && ids[i] == ad;
                                 cp_async16(bt + swz + 2048 * i,
-                                           tl ? src + (int64_t)(32 * i) * a.R : a.hp, tl);
+                                           tl ? src + (int64_t)(16 * PARTS * i) * a.R : a.hp, tl);
                             }
                     }
                     // handed over a turn later, when the next copies are on their way
@@ -1070,7 +1079,7 @@ size_t lora_list_bytes(int64_t T) {
 
 // Clusters of 2 * S CTAs that run at once (a cluster lies in one GPC, so larger ones leave SMs
 // over), asked for once per device.
-template <int MODE, bool PRE>
+template <int MODE, bool PRE, int PARTS>
 static int lora_tc_clusters(int S) {
     static std::atomic<int> known[128][3];
     int dev = 0;
@@ -1089,7 +1098,7 @@ static int lora_tc_clusters(int S) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, k_lora_tc<MODE, PRE>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, k_lora_tc<MODE, PRE, PARTS>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
@@ -1097,7 +1106,7 @@ static int lora_tc_clusters(int S) {
     return n;
 }
 
-template <int MODE, bool PRE>
+template <int MODE, bool PRE, int PARTS>
 static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, int* status) {
     const int BN = lora_tc_tile(a.T);
     CUtensorMap pm, tm;
@@ -1117,7 +1126,7 @@ static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, in
                          : make_tmap_u8_2d(&tm, a.t, a.T, (int64_t)a.C * 2, 128, BN / 2,
                                            CU_TENSOR_MAP_SWIZZLE_128B);
     if (!okp || !okt) return cudaErrorInvalidValue;
-    cudaError_t e = ensure_dyn_smem<k_lora_tc<MODE, PRE>>(LT_SMEM);
+    cudaError_t e = ensure_dyn_smem<k_lora_tc<MODE, PRE, PARTS>>(LT_SMEM);
     if (e != cudaSuccess) return e;
     const int64_t num_p = (a.P + 255) / 256, num_t = (a.T + BN - 1) / BN, tiles = num_p * num_t;
     if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
@@ -1125,7 +1134,7 @@ static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, in
     // least 4 stages.
     int S = 1;
     while (2 * S <= lora_max_split(a.P, a.T) && tiles * 2 <= num_sms / 2 / S &&
-           a.C / LT_BK >= 4 * 2 * S && tiles <= lora_tc_clusters<MODE, PRE>(2 * S))
+           a.C / LT_BK >= 4 * 2 * S && tiles <= lora_tc_clusters<MODE, PRE, PARTS>(2 * S))
         S *= 2;
     const int64_t clusters = tiles < num_sms / 2 ? tiles : num_sms / 2;
     cudaLaunchConfig_t cfg = {};
@@ -1142,17 +1151,19 @@ static cudaError_t launch_tc(const LoraGemm& a, cudaStream_t st, int num_sms, in
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_lora_tc<MODE, PRE>, pm, tm, a, BN, (int)num_p, (int)num_t,
+    return cudaLaunchKernelEx(&cfg, k_lora_tc<MODE, PRE, PARTS>, pm, tm, a, BN, (int)num_p, (int)num_t,
                               S, status);
 }
 
 cudaError_t launch_lora_tc(int mode, const LoraGemm& a, cudaStream_t st, int num_sms,
                            int* status) {
-#define LT_MODE(M_) \
-    (a.pre ? launch_tc<M_, true>(a, st, num_sms, status) : launch_tc<M_, false>(a, st, num_sms, status))
-    if (mode == LORA_FWD) return LT_MODE(LORA_FWD);
-    if (mode == LORA_DGRAD) return LT_MODE(LORA_DGRAD);
-    return LT_MODE(LORA_WGRAD);
+#define LT_MODE(M_, PARTS_)                                       \
+    (a.pre ? launch_tc<M_, true, PARTS_>(a, st, num_sms, status)  \
+           : launch_tc<M_, false, PARTS_>(a, st, num_sms, status))
+    if (mode == LORA_FWD)
+        return a.out_bf16 ? LT_MODE(LORA_FWD, lora_parts(true)) : LT_MODE(LORA_FWD, lora_parts(false));
+    if (mode == LORA_DGRAD) return LT_MODE(LORA_DGRAD, lora_parts(true));
+    return LT_MODE(LORA_WGRAD, lora_parts(true));
 #undef LT_MODE
 }
 

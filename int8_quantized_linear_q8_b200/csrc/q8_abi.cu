@@ -227,8 +227,8 @@ static q8_status check_adapter_pointers(const q8_adapters* ad, const int32_t* id
 
 // Up to 16 rows run the decode GEMV where it takes the shape; it needs the term [M, N].
 static inline bool lora_decodes(int64_t M, int64_t K) { return M <= 16 && w8a16_tma_fits(M, K); }
-// Workspaces of the GEMM forms (byte offsets): backward g fp32 [M, R]; h (or g) in two bf16
-// parts [M, 2 R]; the plan of the rows' adapters; the int8 weight in bf16, where it is expanded;
+// Workspaces of the GEMM forms (byte offsets): backward g fp32 [M, R]; h (or g) in bf16 parts
+// [M, parts * R], forward always with room for an fp32 result's; the plan of the rows' adapters; the int8 weight in bf16, where it is expanded;
 // partial sums of y.
 struct LoraWs {
     size_t g = 0, hp = 0, plan = 0, pre = 0, pre_bytes = 0, partial = 0, partial_bytes = 0, bytes = 0;
@@ -237,7 +237,7 @@ static LoraWs plan_lora(bool bwd, int64_t M, int64_t N, int64_t K, int64_t R) {
     LoraWs w;
     if (M <= 0) return w;
     w.hp = bwd ? align_up((size_t)M * R * 4, 256) : 0;
-    w.plan = w.hp + align_up((size_t)M * R * 4, 256);
+    w.plan = w.hp + align_up((size_t)M * R * 2 * lora_parts(bwd), 256);
     w.pre = w.plan + align_up(lora_plan_bytes(M), 256);
     w.pre_bytes = bwd ? lora_pre_bytes(LORA_DGRAD, K, N, M) : lora_pre_bytes(LORA_FWD, N, K, M);
     w.partial = w.pre + align_up(w.pre_bytes, 256);
@@ -508,7 +508,8 @@ q8_status q8_linear_w8a16_lora(const void* x, const int8_t* q, const float* s_w,
     Q8_TRY(launched(launch_lora_plan(ids, M, L, ws + w.plan, st)));
     if (w.partial_bytes) a.partial = (float*)(ws + w.partial);
     Q8_TRY(launched(launch_lora_shrink(false, (const uint16_t*)x, (const uint16_t*)ad->a,
-                                       ad->scale, ws + w.plan, h, hp, M, (int)K, R, L, st, sms)));
+                                       ad->scale, ws + w.plan, h, hp, lora_parts(a.out_bf16), M,
+                                       (int)K, R, L, st, sms)));
     if (w.pre_bytes) {
         Q8_TRY(launched(launch_lora_expand(LORA_FWD, a, (uint16_t*)(ws + w.pre), true, st)));
         a.pre = (const uint16_t*)(ws + w.pre);
@@ -575,7 +576,8 @@ q8_status q8_linear_w8a16_lora_backward(const void* dy, const int8_t* q, const f
     Q8_TRY(launched(launch_lora_plan(ids, M, L, plan, st)));
     if (dx || da)
         Q8_TRY(launched(launch_lora_shrink(true, (const uint16_t*)dy, (const uint16_t*)ad->b,
-                                           ad->scale, plan, g, hp, M, (int)N, R, L, st, sms)));
+                                           ad->scale, plan, g, hp, lora_parts(a.out_bf16), M,
+                                           (int)N, R, L, st, sms)));
     if (dx && w.pre_bytes) {
         Q8_TRY(launched(launch_lora_expand(LORA_DGRAD, a, (uint16_t*)(ws + w.pre), true, st)));
         a.pre = (const uint16_t*)(ws + w.pre);

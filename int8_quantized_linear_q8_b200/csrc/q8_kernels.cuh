@@ -226,17 +226,21 @@ struct LoraGemm {
     // adapter term (LORA_WGRAD: none): low = b (LORA_FWD) or a (LORA_DGRAD)
     const int32_t* ids;
     const uint16_t* low;
-    const uint16_t* hp;         // [T, 2 R]: scale * h (LORA_DGRAD: g) in two bf16 parts
+    const uint16_t* hp;         // [T, parts * R]: scale * h (LORA_DGRAD: g) in lora_parts parts
     const int* lists;           // lora_plan_lists
     int R;
 };
+// bf16 parts that a row of scale * h or g enters its large product as.  Two leave off at most
+// 2^-17, next to nothing where the result is rounded to bf16 (2^-8 of it); three hold the whole
+// fp32 number, as results in fp32 need (two made their error that of 16 bits).
+constexpr int lora_parts(bool out_bf16) { return out_bf16 ? 2 : 3; }
 size_t lora_plan_bytes(int64_t M);               // workspace of the plan
 const int* lora_plan_lists(const void* ws);
 cudaError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, void* ws, cudaStream_t st);
-// h (or, backward, g) of every row, and its two bf16 parts hp [M, 2 R]; ws: the plan of its ids
+// h (or, backward, g) of every row, and its bf16 parts hp [M, parts * R]; ws: the plan of its ids
 cudaError_t launch_lora_shrink(bool bwd, const uint16_t* x, const uint16_t* w, const float* scale,
-                               const void* ws, float* h, uint16_t* hp, int64_t M, int C, int R,
-                               int L, cudaStream_t st, int num_sms);
+                               const void* ws, float* h, uint16_t* hp, int parts, int64_t M, int C,
+                               int R, int L, cudaStream_t st, int num_sms);
 // dB from dy and h, dA from the layer's input (bf16, or codes with exps) and g, each if wanted
 cudaError_t launch_lora_wgrad(const void* dy, const float* h, float* db, const void* x,
                               const uint8_t* exps, int gshift, const float* g, float* da,
