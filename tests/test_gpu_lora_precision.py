@@ -73,3 +73,18 @@ def test_every_bit_of_h_reaches_y(M):
     assert ((h.double() - want[:, None]).abs() <= 2.0 ** -23 * want[:, None]).all()
     c = 2.0 * scale[d["ids"].long()].double()
     ref.near(y, (c * h[:, 0].double())[:, None].expand(M, N), 2.0 ** -23 * (c * want)[:, None], "y")
+
+
+@pytest.mark.parametrize("M,N,K,R", [(40, 72, 256, 24), (333, 1025, 2064, 8), (2600, 4096, 2048, 16)])
+def test_workspace_of_an_fp32_call(M, N, K, R):
+    """The size that q8_workspace_bytes gives is enough for three parts, and nothing behind it is
+    written."""
+    d = ref.make(M, N, K, R, 3, seed=190 + M)
+    args = [d[k] for k in ("x", "q", "s_w", "a", "b", "scale", "ids")]
+    want = q8.q8_linear_w8a16_lora(*args, out_dtype=torch.float32)
+    need = q8.q8_workspace_bytes(q8.Q8_OP_LINEAR_W8A16_LORA, M, N, K, R)
+    for fill in (0xFF, 0x01):
+        ws = torch.full((need + 4096,), fill, dtype=torch.uint8, device="cuda")
+        got = q8.q8_linear_w8a16_lora(*args, out_dtype=torch.float32, workspace=ws[:need])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert (ws[need:] == fill).all()
