@@ -369,7 +369,7 @@ typedef struct {
  * fp32 accumulation.  s_w[n] * q[n,k] is rounded to bf16 once on its way to the tensor
  * cores (s_w varies along the summed axis, so it cannot be applied after the sum), g meets a
  * in 16 bits (2^-17) and dx is rounded to bf16 once; da and db use all of g and h.  Sums are
- * taken in an order that depends on sizes and ids only.
+ * taken in an order that depends on sizes, ids and what the device runs at once only.
  *   dy device bf16 [M, N]; ids, adapters, q, s_w as in the forward call; h device fp32
  *   [M, rank] as the forward call wrote it (read iff db); input: the layer's input (read iff
  *   da; exps of any alignment, group 0, 32, 64, 128 or 256 with K % group == 0);

@@ -33,7 +33,7 @@
 // one loop did base and adapter stages, 0.4 with a loop of its own for the base).
 //
 // What bounds it, measured on the expanded form (cycles a stage of 64 c; its MMAs take 512): dgrad
-// 538, tensor pipe active 91% of the time a pair has work; forward 608 (the adapter term's
+// 538, tensor pipe active 93% of the time a pair has work; forward 608 (the adapter term's
 // second accumulator, drained between tiles).  dgrad of 4096 x 11008 x 4096: 250 us, 1.48 PFLOP/s,
 // of which the fourth round of tiles, which 34 of 74 pairs have, costs 13%.  Two things cost most
 // on the way: cluster-scope acquire and release on the hand-offs (538 -> 328 us), and everything
