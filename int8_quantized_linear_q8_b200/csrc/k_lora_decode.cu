@@ -10,9 +10,9 @@
 // A cluster of eight CTAs per row: its 64 warps share out the rank's rows of A (and parts of K
 // when the rank is below 64), every warp leaves its sums in all eight CTAs' shared memory (behind
 // a cluster barrier, since the others have to have started), and after a second barrier each CTA
-// makes an eighth of the row of t.  The kernel lets the
-// weight stream start as soon as the stream's earlier work is done (programmatic dependent
-// launch); the stream waits for t only when its first rows are summed.
+// makes an eighth of the row of t.  The kernel lets the weight stream start as soon as the stream's
+// earlier work is done (programmatic dependent launch); the stream waits for t only when its first
+// rows are summed.
 //
 // 16 rows, 4096 x 11008, rank 16, 32 adapters: this kernel 6 us (h 2.7, t 3.2), the whole call 19.9 us
 // back to back, the plain linear 14; 1 row, 960 x 2560, rank 8: 4.9 and 3.9 us.  What is left is the

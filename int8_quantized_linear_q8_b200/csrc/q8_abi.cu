@@ -228,8 +228,8 @@ static q8_status check_adapter_pointers(const q8_adapters* ad, const int32_t* id
 // Up to 16 rows run the decode GEMV where it takes the shape; it needs the term [M, N].
 static inline bool lora_decodes(int64_t M, int64_t K) { return M <= 16 && w8a16_tma_fits(M, K); }
 // Workspaces of the GEMM forms (byte offsets): backward g fp32 [M, R]; h (or g) in bf16 parts
-// [M, parts * R], forward always with room for an fp32 result's; the plan of the rows' adapters; the int8 weight in bf16, where it is expanded;
-// partial sums of y.
+// [M, parts * R], forward always with room for an fp32 result's; the plan of the rows' adapters;
+// the int8 weight in bf16, where it is expanded; partial sums of y.
 struct LoraWs {
     size_t g = 0, hp = 0, plan = 0, pre = 0, pre_bytes = 0, partial = 0, partial_bytes = 0, bytes = 0;
 };
